@@ -84,6 +84,9 @@ typedef FP4_ENUM {
 #define FP4_FLAG_BARRIER_TIMEOUT 4 /* information, not an error: a grid-barrier
                                       wait timed out and some workgroup took the
                                       fallback; the outputs are exact            */
+#define FP4_FLAG_CACHE_INDEX 8     /* a cache call met a position, a token range or a
+                                      page id outside what the batch and the cache
+                                      hold; those entries were skipped           */
 
 typedef FP4_ENUM { FP4_F32 = 0, FP4_BF16 = 1 } fp4_dtype;
 typedef FP4_ENUM { FP4_MXFP4 = 0, FP4_NVFP4 = 1 } fp4_format;
@@ -555,6 +558,116 @@ fp4_status fp4_debug_linear_mxfp4_spin(const void *x, fp4_dtype xt, int64_t M, i
 /* Bytes of device workspace fp4_quantize_nvfp4 / fp4_scale_search need for a
  * [rows, cols] input (0 for MXFP4). */
 size_t fp4_workspace_bytes(fp4_format fmt, int64_t rows, int64_t cols);
+
+/*
+ * 8-bit key/value cache: keys and values of attention held as E4M3FN codes
+ * with one E8M0 scale byte per block of tokens and head, written as tokens
+ * arrive, read back, and attended over ("FP4, FP8 and INT8/INT4" page: FP8
+ * key/value caches, and attention that keeps its softmax in higher precision;
+ * the scale form is the MX one of the "NVFP4 / MXFP4 format" page, section 2).
+ *
+ * The cache is paged.  A page holds `block` tokens of every kv head:
+ *   k_codes, v_codes    [pages, kv_heads, block, head_dim]  E4M3FN bytes
+ *   k_scales, v_scales  [pages, kv_heads]                   E8M0 bytes
+ * and stands for E4M3(code) * 2^(byte - 127) (byte 255, or code 0x7F / 0xFF:
+ * NaN).  block is a power of two from 16 to 256, head_dim 64, 128, 192 or 256;
+ * pages below 2^31, kv_heads up to 65535.  Codes are 16-byte aligned.  The
+ * caller owns the pages; new ones need no clearing (what a page holds past its
+ * sequence's length is never used).
+ */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t pages;
+    int32_t kv_heads, block, head_dim;
+} fp4_kv_cache;
+
+/*
+ * A ragged batch over the cache (device arrays of int32):
+ *   cu_tokens  [seqs + 1]  prefix sums of the sequences' new tokens, from 0;
+ *              sequence s has rows cu_tokens[s] .. cu_tokens[s+1] - 1 of k, v,
+ *              q and out (none is allowed)
+ *   lengths    [seqs]      each sequence's tokens, its new ones included: new
+ *              token i of sequence s has position lengths[s] - (cu_tokens[s+1]
+ *              - cu_tokens[s]) + i
+ *   table      [seqs, table_width]  page ids, table_stride elements from one
+ *              sequence's to the next: position p is in page
+ *              table[s][p / block], slot p % block.  Entries past a sequence's
+ *              length are not read.  Sequences may share pages, but not one
+ *              that a write touches.
+ *   tokens     rows of k, v, q and out (at most 2^26); those past
+ *              cu_tokens[seqs] belong to no sequence: outputs get zeros there
+ *   seqs       1 .. 2^20
+ * What the kernels find outside these bounds they skip and flag
+ * (FP4_FLAG_CACHE_INDEX): a position below 0 or past the table, a page id
+ * outside 0 .. pages - 1, prefix sums outside 0 .. tokens.
+ */
+typedef struct {
+    const int32_t *cu_tokens, *lengths, *table;
+    int64_t tokens, table_stride;
+    int32_t seqs, table_width;
+} fp4_kv_batch;
+
+/*
+ * Writes the batch's new tokens into the cache.
+ *   k, v   fp32 or bf16, element (t, h, d) at t * token_stride + h *
+ *          head_stride + d (strides in elements: slices of a fused projection's
+ *          rows need no copy); pointers and strides multiples of 16 bytes
+ * Per page and head with new tokens, of keys and of values: A = the largest
+ * magnitude among the new values, e = the smallest integer >= -127 with
+ * 448 * 2^e >= A (-127 for zeros), so nothing saturates.  If the page holds
+ * earlier tokens of the sequence before the first new one, e is at least their
+ * scale's, and where it is greater their codes become E4M3(c * 2^(e_old - e)).
+ * New codes are E4M3(x * 2^-e); every E4M3 rounding is to nearest, ties to the
+ * even code.  The codes depend on how the tokens were split over calls only
+ * through values that became E4M3 subnormals.  Values that are not finite are
+ * stored as NaN, stay out of A, and raise FP4_FLAG_NONFINITE.  One launch.
+ * Deterministic; writing the same rows again changes nothing.
+ */
+fp4_status fp4_kv_cache_write(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *k,
+                              int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                              int64_t v_token_stride, int64_t v_head_stride, fp4_dtype xt,
+                              int32_t *status, void *stream);
+
+/*
+ * Reads the batch's rows (those fp4_kv_cache_write would write; with
+ * cu_tokens the prefix sums of lengths, whole sequences) back as k and v
+ * [tokens, kv_heads, head_dim] of fp32 or bf16, 16-byte aligned.  Exact in fp32,
+ * and in bf16 for scale bytes 8 .. 246.  Rows of no sequence and entries that
+ * raise FP4_FLAG_CACHE_INDEX read as zero.  One launch.  Deterministic.
+ */
+fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batch, void *k,
+                             void *v, fp4_dtype yt, int32_t *status, void *stream);
+
+/*
+ * Attention of the batch's new tokens over the cache (their own keys and
+ * values written to it before).
+ *   q      [tokens, heads, head_dim] fp32 or bf16, strided as k above; heads a
+ *          multiple of kv_heads: query head h reads kv head h / (heads /
+ *          kv_heads)
+ *   scale  multiplies the scores (finite; 1 / sqrt(head_dim) as a rule)
+ *   causal 1: a token at position p sees positions 0 .. p; 0: it sees all of
+ *          its sequence's
+ *   window 0, or (causal only) how many positions up to its own a token sees
+ *   out    [tokens, heads, head_dim] of q's type, 16-byte aligned
+ *   lse    [tokens, heads] fp32 or NULL: the logarithm of the sum of the
+ *          exponentials of a row's scores
+ * A row that sees nothing gets zeros and lse = -inf.  Keys that raise
+ * FP4_FLAG_CACHE_INDEX are not seen.  Scores, their maxima and sums and the output
+ * sums are fp32; bf16 queries use products of bf16 operands (cache values are
+ * exact in bf16; probabilities are rounded to bf16), fp32 queries products
+ * split over several bf16 operands, to fp32 precision.
+ *   workspace  fp4_kv_attention_workspace_bytes(...) bytes of scratch, 16-byte
+ *          aligned (NULL when that is 0); calls that share one must be ordered
+ * How the keys are split over workgroups depends on the arguments given here
+ * alone, not on the arrays; the order of every sum is fixed: deterministic.
+ */
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,
+                                        int32_t heads);
+fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *q,
+                            int64_t q_token_stride, int64_t q_head_stride, fp4_dtype qt,
+                            int32_t heads, float scale, int32_t causal, int32_t window, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes, int32_t *status,
+                            void *stream);
 
 /* Static English text for a status code. */
 const char *fp4_status_str(fp4_status s);

@@ -12,8 +12,15 @@ Functions mirror the C entry points:
     dequantize(fmt, codes, scales, s_g, out_dtype)
     scale_search(x, n_candidates, c_lo, c_hi) -> (codes, scales, global_scale)
     gemm_mxfp4(a_codes, a_scales, bt_codes, bt_scales, out_dtype)
+    new_kv_cache(pages, kv_heads, block, head_dim, device)  -> KVCache
+    kv_cache_write(cache, k, v, cu_tokens, lengths, table)
+    kv_cache_read(cache, cu_tokens, lengths, table, tokens) -> (k, v)
+    kv_attention(q, cache, cu_tokens, lengths, table)       -> out
 
-Inputs are contiguous CUDA (HIP) tensors of dtype float32 or bfloat16 whose
+The last four are the 8-bit key/value cache (E4M3FN codes, one E8M0 byte per
+page and head); include/fp4.h states its layout and what a batch is.
+
+Inputs of the others are contiguous CUDA (HIP) tensors of dtype float32 or bfloat16 whose
 last dimension is a multiple of the block (32 for MXFP4, 16 for NVFP4).
 codes have shape [..., K/2] (uint8, two E2M1 codes per byte, even element in
 the low nibble); scales [..., K/block] (uint8: E8M0 for MXFP4, E4M3FN for
@@ -39,6 +46,7 @@ BF16 = 1
 FLAG_NONFINITE = 1
 FLAG_SCALE_UNDERFLOW = 2
 FLAG_BARRIER_TIMEOUT = 4
+FLAG_CACHE_INDEX = 8
 
 EXPORTS = ("fp4_quantize_mxfp4", "fp4_quantize_mxfp4_rule", "fp4_quantize_nvfp4",
            "fp4_dequantize", "fp4_scale_search", "fp4_scale_search_exhaustive",
@@ -50,12 +58,28 @@ EXPORTS = ("fp4_quantize_mxfp4", "fp4_quantize_mxfp4_rule", "fp4_quantize_nvfp4"
            "fp4_gemm_mxfp4_packed", "fp4_quantize_mxfp4_packed", "fp4_linear_mxfp4_packed",
            "fp4_nv_packed_operand_bytes", "fp4_pack_nvfp4_operand", "fp4_gemm_nvfp4_packed",
            "fp4_quantize_nvfp4_packed", "fp4_linear_nvfp4_packed",
-           "fp4_quantize_nvfp4_noalloc", "fp4_workspace_bytes", "fp4_status_str")
+           "fp4_quantize_nvfp4_noalloc", "fp4_workspace_bytes", "fp4_status_str",
+           "fp4_kv_cache_write", "fp4_kv_cache_read", "fp4_kv_attention",
+           "fp4_kv_attention_workspace_bytes")
 
 # fp4_mx_rule: the MXFP4 block-exponent rules
 MX_RULES = {"ocp": 0, "ceil": 1, "mse": 2}
 
 _lib = None
+
+
+class _CKvCache(ctypes.Structure):  # fp4_kv_cache
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _CKvBatch(ctypes.Structure):  # fp4_kv_batch
+    _fields_ = [("cu_tokens", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32)]
 
 
 class Fp4Error(RuntimeError):
@@ -107,6 +131,12 @@ def lib() -> ctypes.CDLL:
                                                 ctypes.c_uint32]
     L.fp4_debug_linear_mxfp4_spin.argtypes = [P, I, I64, I64, P, P, I64, P, P, P, I, I, P, S, P, P,
                                               ctypes.c_uint32]
+    KC, KB = ctypes.POINTER(_CKvCache), ctypes.POINTER(_CKvBatch)
+    L.fp4_kv_cache_write.argtypes = [KC, KB, P, I64, I64, P, I64, I64, I, P, P]
+    L.fp4_kv_cache_read.argtypes = [KC, KB, P, P, I, P, P]
+    L.fp4_kv_attention.argtypes = [KC, KB, P, I64, I64, I, I32, F, I32, I32, P, P, P, S, P, P]
+    L.fp4_kv_attention_workspace_bytes.argtypes = [KC, KB, I32]
+    L.fp4_kv_attention_workspace_bytes.restype = S
     L.fp4_workspace_bytes.argtypes = [I, I64, I64]
     L.fp4_workspace_bytes.restype = S
     L.fp4_status_str.argtypes = [I]
@@ -163,6 +193,8 @@ def _raise_flags(flags: int):
         raise ValueError("finite input required (NaN or Inf found)")
     if flags & FLAG_SCALE_UNDERFLOW:
         raise ValueError("a nonzero scale rounded to zero (tensor, block scale or alpha underflow)")
+    if flags & FLAG_CACHE_INDEX:
+        raise ValueError("a cache position, token range or page id is out of bounds")
     # FLAG_BARRIER_TIMEOUT is information only: a workgroup took the grid
     # barrier's fallback and the outputs are exact
 
@@ -652,3 +684,143 @@ def dequantize_padded(fmt: int, codes: torch.Tensor, scales: torch.Tensor, cols:
 def padded_storage_bytes(fmt: int, rows: int, cols: int) -> int:
     return int(lib().fp4_padded_storage_bytes(int(fmt), int(rows), int(cols)))
 
+
+
+class KVCache:
+    """An 8-bit key/value cache: k_codes, v_codes [pages, kv_heads, block,
+    head_dim] and k_scales, v_scales [pages, kv_heads], contiguous uint8 tensors
+    on one device (include/fp4.h, fp4_kv_cache)."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_c")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages, kv_heads, block, head_dim]")
+        shape, device = k_codes.shape, k_codes.device
+        for t, want in ((k_codes, shape), (k_scales, shape[:2]), (v_codes, shape),
+                        (v_scales, shape[:2])):
+            if t.dtype != torch.uint8:
+                raise TypeError("a cache holds uint8 codes and scales")
+            if t.shape != want or t.device != device or not t.is_contiguous():
+                raise ValueError(f"expected a contiguous {list(want)} tensor on {device}")
+        if not k_codes.is_cuda:
+            raise TypeError("expected device tensors")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
+                                                                    v_scales)
+        self._c = _CKvCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                            v_scales.data_ptr(), *shape)
+
+
+def new_kv_cache(pages: int, kv_heads: int, block: int, head_dim: int, device) -> KVCache:
+    """A cache with room for pages * block tokens.  Pages need no clearing."""
+    def half():
+        return (torch.empty(pages, kv_heads, block, head_dim, dtype=torch.uint8, device=device),
+                torch.empty(pages, kv_heads, dtype=torch.uint8, device=device))
+    return KVCache(*half(), *half())
+
+
+def _kv_batch(cache: KVCache, cu_tokens, lengths, table, tokens: int) -> _CKvBatch:
+    device = cache.k_codes.device
+    for t, dim, what in ((cu_tokens, 1, "cu_tokens"), (lengths, 1, "lengths"), (table, 2, "table")):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{what} must be an int32 tensor")
+        if t.device != device or t.dim() != dim or (t.stride(-1) != 1 and t.shape[-1] > 1):
+            raise ValueError(f"{what} must be {dim}-dimensional, dense, on {device}")
+    seqs, width = table.shape
+    if lengths.shape[0] != seqs or cu_tokens.shape[0] != seqs + 1:
+        raise ValueError("for a table of n sequences, lengths has n entries and cu_tokens n + 1")
+    return _CKvBatch(cu_tokens.data_ptr(), lengths.data_ptr(), table.data_ptr(), tokens,
+                     table.stride(0) if seqs > 1 else width, seqs, width)
+
+
+def _kv_rows(x: torch.Tensor, cache: KVCache, what: str):
+    """(pointer, token stride, head stride) of rows [tokens, heads, head_dim]."""
+    if x.device != cache.k_codes.device:
+        raise ValueError(f"{what} must be on the cache's device")
+    if x.dim() != 3 or x.shape[2] != cache.k_codes.shape[3] or x.stride(2) != 1:
+        raise ValueError(f"{what} must be [tokens, heads, {cache.k_codes.shape[3]}] with dense "
+                         "last dimension")
+    return (x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0,
+            x.stride(1) if x.shape[1] > 1 else x.shape[2])
+
+
+def _kv_status(status, check: bool, device):
+    if status is None and check:
+        status = torch.zeros(1, dtype=torch.int32, device=device)
+    return status
+
+
+def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor,
+                   lengths: torch.Tensor, table: torch.Tensor, check: bool = True,
+                   status=None) -> None:
+    """Quantize the batch's new keys and values (fp32 or bf16 [tokens, kv_heads,
+    head_dim], slices of a projection's rows allowed) into the cache.  cu_tokens
+    [n + 1], lengths [n] (new tokens included) and table [n, width] are int32."""
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    if k.dim() != 3 or k.shape[1] != cache.k_codes.shape[1]:
+        raise ValueError("k and v must have the cache's kv heads")
+    batch = _kv_batch(cache, cu_tokens, lengths, table, k.shape[0])
+    status = _kv_status(status, check, k.device)
+    _ok(lib().fp4_kv_cache_write(cache._c, batch, *_kv_rows(k, cache, "k"),
+                                 *_kv_rows(v, cache, "v"), _dtype_code(k.dtype), _ptr(status),
+                                 _stream(k)))
+    if check:
+        _raise_flags(int(status.item()))
+
+
+def kv_cache_read(cache: KVCache, cu_tokens: torch.Tensor, lengths: torch.Tensor,
+                  table: torch.Tensor, tokens: int, out_dtype=torch.bfloat16, out=None,
+                  check: bool = True, status=None):
+    """The batch's rows as (k, v), each [tokens, kv_heads, head_dim]; with
+    cu_tokens the prefix sums of lengths, whole sequences."""
+    _, heads, _, dim = cache.k_codes.shape
+    device = cache.k_codes.device
+    if out is None:
+        k = torch.empty(tokens, heads, dim, dtype=out_dtype, device=device)
+        v = torch.empty(tokens, heads, dim, dtype=out_dtype, device=device)
+    else:
+        k, v = out
+        for t in out:
+            if (t.shape != (tokens, heads, dim) or t.dtype != k.dtype or t.device != device
+                    or not t.is_contiguous()):
+                raise ValueError(f"out must be two contiguous [{tokens}, {heads}, {dim}] tensors")
+    batch = _kv_batch(cache, cu_tokens, lengths, table, tokens)
+    status = _kv_status(status, check, device)
+    _ok(lib().fp4_kv_cache_read(cache._c, batch, _ptr(k), _ptr(v), _dtype_code(k.dtype),
+                                _ptr(status), _stream(k)))
+    if check:
+        _raise_flags(int(status.item()))
+    return k, v
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengths: torch.Tensor,
+                 table: torch.Tensor, scale=None, causal: bool = True, window: int = 0, out=None,
+                 return_lse: bool = False, workspace=None, check: bool = True, status=None):
+    """Attention of the batch's new tokens, q [tokens, heads, head_dim] (fp32 or
+    bf16, slices allowed), over the cache; scale defaults to head_dim ** -0.5.
+    Returns out, or (out, lse [tokens, heads] fp32).  The work is laid out for
+    sequences as long as the table is wide: pass a table (or table[:, :width])
+    no wider than the longest one needs."""
+    tokens, heads, dim = q.shape
+    batch = _kv_batch(cache, cu_tokens, lengths, table, tokens)
+    if out is None:
+        out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=q.device)
+    elif (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
+          or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
+    rows = _kv_rows(q, cache, "q")
+    L = lib()
+    need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    status = _kv_status(status, check, q.device)
+    _ok(L.fp4_kv_attention(cache._c, batch, *rows, _dtype_code(q.dtype), heads,
+                           dim ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+                           int(window), _ptr(out), _ptr(lse), _ptr(workspace),
+                           workspace.numel() if workspace is not None else 0, _ptr(status),
+                           _stream(q)))
+    if check:
+        _raise_flags(int(status.item()))
+    return (out, lse) if return_lse else out

@@ -17,7 +17,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp4.so")
 PHASE_LIB = os.path.join(HERE, "libfp4_phase.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-SOURCES = ["fp4_api.hip", "fp4_quant.hip", "fp4_gemm.hip"]
+SOURCES = ["fp4_api.hip", "fp4_quant.hip", "fp4_gemm.hip", "fp4_kv.hip", "fp4_attention.hip"]
 
 # -ffp-contract=off: no implicit fused multiply-add; the kernels spell every
 # fused operation explicitly (the method's fp32 steps are separate roundings).

@@ -10,6 +10,7 @@
 #include "../../include/fp4_phase_clock.h"
 #endif
 #include "fp4_kernels.h"
+#include "fp4_kv.h"
 
 // Device scratch of fp4_quantize_nvfp4_noalloc, for callers that cannot
 // allocate: the same workspace fp4_quantize_nvfp4 takes from its caller
@@ -72,6 +73,48 @@ hipError_t device_scratch(void **out) {
     });
     *out = s.ptr;
     return s.err;
+}
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 26;
+constexpr int32_t kMaxSeqs = 1 << 20;
+static_assert(FP4_FLAG_CACHE_INDEX == fp4dev::FLAG_CACHE_INDEX, "the header states the flag");
+
+// The kernels' forms of a cache and a batch, checked.  A batch without rows is
+// valid and launches nothing.
+fp4_status kv_args(const fp4_kv_cache *cache, const fp4_kv_batch *batch, fp4dev::KvCache *C,
+                   fp4dev::KvBatch *B) {
+    if (!cache || !batch) return FP4_E_ARG;
+    if (!cache->k_codes || !cache->k_scales || !cache->v_codes || !cache->v_scales)
+        return FP4_E_ARG;
+    if (!batch->cu_tokens || !batch->lengths || !batch->table) return FP4_E_ARG;
+    const int32_t block = cache->block, dim = cache->head_dim;
+    if (block < 16 || block > 256 || (block & (block - 1))) return FP4_E_SHAPE;
+    if (dim < 64 || dim > 256 || dim % 64) return FP4_E_SHAPE;
+    if (cache->pages < 1 || cache->pages > INT32_MAX) return FP4_E_SHAPE;
+    if (cache->kv_heads < 1 || cache->kv_heads > 65535) return FP4_E_SHAPE;
+    if (batch->seqs < 1 || batch->seqs > kMaxSeqs || batch->table_width < 1) return FP4_E_SHAPE;
+    if (batch->table_stride < batch->table_width && batch->seqs > 1) return FP4_E_SHAPE;
+    if (batch->tokens < 0 || batch->tokens > kMaxTokens) return FP4_E_SHAPE;
+    if (!aligned(cache->k_codes, 16) || !aligned(cache->v_codes, 16) ||
+        !aligned(batch->cu_tokens, 4) || !aligned(batch->lengths, 4) || !aligned(batch->table, 4))
+        return FP4_E_ALIGN;
+    *C = {cache->k_codes, cache->k_scales, cache->v_codes, cache->v_scales, (int32_t)cache->pages,
+          cache->kv_heads, block, __builtin_ctz((uint32_t)block), dim};
+    *B = {batch->cu_tokens, batch->lengths, batch->table, batch->table_stride, batch->seqs,
+          batch->table_width, (int32_t)batch->tokens};
+    return FP4_OK;
+}
+
+// Rows of k, v or q: the pointer and both strides on 16 bytes, and no offset
+// past what 64 bits hold.
+fp4_status kv_rows(const void *x, int64_t token_stride, int64_t head_stride, fp4_dtype t,
+                   int64_t dim) {
+    const int64_t unit = t == FP4_BF16 ? 8 : 4;
+    if (head_stride < dim || head_stride > kMaxElems || token_stride > kMaxElems ||
+        token_stride < 0)
+        return FP4_E_SHAPE;
+    if (!aligned(x, 16) || token_stride % unit || head_stride % unit) return FP4_E_ALIGN;
+    return FP4_OK;
 }
 
 }  // namespace
@@ -533,6 +576,76 @@ int64_t fp4_padded_storage_bytes(fp4_format fmt, int64_t rows, int64_t cols) {
     if (cols > kMaxElems || rows > kMaxElems / ((cols + block - 1) / block * block)) return -1;
     const int64_t blocks = rows * ((cols + block - 1) / block);
     return blocks * (block / 2 + 1) + (fmt == FP4_NVFP4 ? 4 : 0);
+}
+
+fp4_status fp4_kv_cache_write(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *k,
+                              int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                              int64_t v_token_stride, int64_t v_head_stride, fp4_dtype xt,
+                              int32_t *status, void *stream) {
+    fp4dev::KvCache C;
+    fp4dev::KvBatch B;
+    fp4_status st = kv_args(cache, batch, &C, &B);
+    if (st != FP4_OK) return st;
+    if (!valid_dtype(xt)) return FP4_E_DTYPE;
+    if (B.tokens == 0) return FP4_OK;
+    if (!k || !v) return FP4_E_ARG;
+    st = kv_rows(k, k_token_stride, k_head_stride, xt, C.dim);
+    if (st == FP4_OK) st = kv_rows(v, v_token_stride, v_head_stride, xt, C.dim);
+    if (st != FP4_OK) return st;
+    if (!aligned(status, 4)) return FP4_E_ALIGN;
+    return from_hip(fp4dev::launch_kv_write(C, B, k, v, xt == FP4_BF16, k_token_stride,
+                                            k_head_stride, v_token_stride, v_head_stride, status,
+                                            (hipStream_t)stream));
+}
+
+fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batch, void *k,
+                             void *v, fp4_dtype yt, int32_t *status, void *stream) {
+    fp4dev::KvCache C;
+    fp4dev::KvBatch B;
+    fp4_status st = kv_args(cache, batch, &C, &B);
+    if (st != FP4_OK) return st;
+    if (!valid_dtype(yt)) return FP4_E_DTYPE;
+    if (B.tokens == 0) return FP4_OK;
+    if (!k || !v) return FP4_E_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(status, 4)) return FP4_E_ALIGN;
+    return from_hip(fp4dev::launch_kv_read(C, B, k, v, yt == FP4_BF16, status,
+                                           (hipStream_t)stream));
+}
+
+size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,
+                                        int32_t heads) {
+    fp4dev::KvCache C;
+    fp4dev::KvBatch B;
+    if (kv_args(cache, batch, &C, &B) != FP4_OK) return 0;
+    if (heads < 1 || heads > 65535 || heads % C.heads || B.tokens == 0) return 0;
+    return fp4dev::attention_workspace_bytes(C, B, heads);
+}
+
+fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *q,
+                            int64_t q_token_stride, int64_t q_head_stride, fp4_dtype qt,
+                            int32_t heads, float scale, int32_t causal, int32_t window, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes, int32_t *status,
+                            void *stream) {
+    fp4dev::KvCache C;
+    fp4dev::KvBatch B;
+    fp4_status st = kv_args(cache, batch, &C, &B);
+    if (st != FP4_OK) return st;
+    if (!valid_dtype(qt)) return FP4_E_DTYPE;
+    if (causal != 0 && causal != 1) return FP4_E_ARG;
+    if (window < 0 || (window > 0 && !causal)) return FP4_E_ARG;
+    if (!(__builtin_fabsf(scale) < __builtin_inff())) return FP4_E_ARG;
+    if (heads < 1 || heads > 65535 || heads % C.heads) return FP4_E_SHAPE;
+    if (B.tokens == 0) return FP4_OK;
+    if (!q || !out) return FP4_E_ARG;
+    st = kv_rows(q, q_token_stride, q_head_stride, qt, C.dim);
+    if (st != FP4_OK) return st;
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) || !aligned(status, 4))
+        return FP4_E_ALIGN;
+    const size_t need = fp4dev::attention_workspace_bytes(C, B, heads);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_E_WORKSPACE;
+    return from_hip(fp4dev::launch_attention(C, B, q, q_token_stride, q_head_stride,
+                                             qt == FP4_BF16, heads, scale, causal != 0, window,
+                                             out, lse, workspace, status, (hipStream_t)stream));
 }
 
 #ifdef FP4_PHASE_CLOCK

@@ -111,4 +111,19 @@ hipError_t launch_linear_mxfp4(const void *x, bool x_bf16, const uint8_t *bt_cod
                                bool one_launch, void *workspace, int32_t *status, hipStream_t s,
                                uint32_t spin_limit = kResidentSpinLimit);
 
+// The 8-bit key/value cache (fp4_kv.h): the write of new tokens, the read of
+// the same rows, and attention over the cache.  Strides count elements.
+struct KvCache;
+struct KvBatch;
+hipError_t launch_kv_write(const KvCache &C, const KvBatch &B, const void *k, const void *v,
+                           bool bf16, int64_t k_token, int64_t k_head, int64_t v_token,
+                           int64_t v_head, int32_t *status, hipStream_t s);
+hipError_t launch_kv_read(const KvCache &C, const KvBatch &B, void *k, void *v, bool bf16,
+                          int32_t *status, hipStream_t s);
+size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads);
+hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, int64_t q_token,
+                            int64_t q_head, bool bf16, int heads, float scale, bool causal,
+                            int window, void *out, float *lse, void *workspace, int32_t *status,
+                            hipStream_t s);
+
 }  // namespace fp4dev

@@ -1,0 +1,113 @@
+// fp4_kv.h - the 8-bit key/value cache: kernel arguments, the batch's map from
+// grid to pages, and E4M3 conversion.  Internal to libfp4.so.
+//
+// A cache page holds `block` tokens.  Per page and kv head it has block x D
+// E4M3FN codes (token-major) and one E8M0 byte, for keys and for values; a
+// code stands for E4M3(code) 2^(byte - 127).  Pages are far apart in a long
+// cache, so every page address is 64-bit; inside a page offsets fit 32 bits.
+#pragma once
+
+#include "fp4_device.h"
+
+namespace fp4dev {
+
+constexpr uint32_t FLAG_CACHE_INDEX = 8;
+
+struct KvCache {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int32_t pages, heads, block, block_shift, dim;
+};
+
+struct KvBatch {
+    const int32_t *cu, *lengths, *table;
+    int64_t table_stride;
+    int32_t seqs, width, tokens;
+};
+
+// First code of a page and head.
+__device__ __forceinline__ int64_t page_offset(const KvCache &C, int page, int head) {
+    return ((int64_t)page * C.heads + head) * (C.block * C.dim);
+}
+
+// A work item of a launch over (sequence, piece): the host does not know the
+// sequences' token counts, so sequence s owns the items from
+//   first(s) = cu[s] / unit + extra s
+// on, which is at least as many as its pieces of up to `unit` tokens, whatever
+// they start at: n tokens from a unit's start make ceil(n / unit) <=
+// floor difference + 1 pieces (extra 1), from inside a unit one more (extra
+// 2).  Items past a sequence's pieces end at once.  Sequence `seqs` stands for
+// the rows past cu[seqs].  The search reads 64 candidates at a time, one per
+// lane: one step up to 64 sequences, two up to 4096.
+struct Item {
+    int seq, piece, base, count;  // base, count: the sequence's rows [base, base + count)
+};
+
+__device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit_shift, int extra) {
+    const int lane = threadIdx.x & (WAVE - 1);
+    int lo = 0, n = B.seqs + 1;
+    while (n > 1) {
+        const int step = (n + WAVE - 1) / WAVE;
+        const int i = lo + lane * step;
+        const bool at = lane * step < n && (B.cu[i] >> unit_shift) + extra * i <= item;
+        const uint64_t b = __ballot(at);
+        const int k = b ? 63 - __builtin_clzll(b) : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    Item it;
+    it.seq = lo;
+    it.base = B.cu[lo];
+    it.piece = item - ((it.base >> unit_shift) + extra * lo);
+    it.count = (lo < B.seqs ? B.cu[lo + 1] : B.tokens) - it.base;
+    // a cu that is no prefix sum of at most `tokens` rows gives no piece
+    if (it.base < 0 || it.count < 0 || it.base > B.tokens || it.count > B.tokens - it.base ||
+        it.piece < 0)
+        it.count = -1;
+    return it;
+}
+
+inline int64_t item_count(int64_t tokens, int64_t seqs, int unit, int extra) {
+    return tokens / unit + extra * (seqs + 1);
+}
+
+// The page that holds positions [block b of sequence s], or -1 (flagged by
+// the caller) when the table has none or names none of the cache's.
+__device__ __forceinline__ int find_page(const KvBatch &B, const KvCache &C, int s, int64_t b) {
+    if (b < 0 || b >= B.width) return -1;
+    const int page = B.table[(int64_t)s * B.table_stride + b];
+    return (uint32_t)page < (uint32_t)C.pages ? page : -1;
+}
+
+__device__ __forceinline__ void flag(int32_t *status, uint32_t bits) {
+    if (status != nullptr) atomicOr(status, (int32_t)bits);
+}
+
+// 2^(byte - 127); byte 0 is the subnormal 2^-127, byte 255 is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    return byte == 0u ? 0x1p-127f : (byte == 255u ? __builtin_nanf("") : u2f(byte << 23));
+}
+
+// The page's scale byte: the smallest e >= -127 with 448 2^e >= amax, so
+// nothing saturates.  For a normal amax = m 2^(E-127), m in [1, 2), that is
+// e = E - 127 - 8 + [m > 1.75], since 448 = 1.75 2^8; a zero page takes byte 0,
+// the neutral element of the maximum that joins scales.
+__device__ __forceinline__ uint32_t kv_scale_byte(float amax) {
+    const uint32_t b = f2u(amax);
+    const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return e > 0 ? (uint32_t)e : 0u;
+}
+
+// Four E4M3 codes of four values, nearest with ties to the even code.  The
+// callers keep |q| <= 448, or NaN.
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float d) {
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+template <bool HI>
+__device__ __forceinline__ f32x2_t e4m3_pair(uint32_t codes) {
+    return __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, HI);
+}
+
+}  // namespace fp4dev
