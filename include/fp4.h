@@ -592,9 +592,10 @@ typedef struct {
  *   table      [seqs, table_width]  page ids, table_stride elements from one
  *              sequence's to the next: position p is in page
  *              table[s][p / block], slot p % block.  Entries past a sequence's
- *              length are not read.  Sequences may share pages, but not one
+ *              length are not read.  table_width * block is at most 2^27.
+ *              Sequences may share pages, but not one
  *              that a write touches.
- *   tokens     rows of k, v, q and out (at most 2^26); those past
+ *   tokens     rows of k, v, q and out (at most 2^23); those past
  *              cu_tokens[seqs] belong to no sequence: outputs get zeros there
  *   seqs       1 .. 2^20
  * What the kernels find outside these bounds they skip and flag
@@ -662,7 +663,7 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
  * alone, not on the arrays; the order of every sum is fixed: deterministic.
  */
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,
-                                        int32_t heads);
+                                        int32_t heads, int32_t window);
 fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *q,
                             int64_t q_token_stride, int64_t q_head_stride, fp4_dtype qt,
                             int32_t heads, float scale, int32_t causal, int32_t window, void *out,

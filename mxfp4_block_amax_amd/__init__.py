@@ -135,7 +135,7 @@ def lib() -> ctypes.CDLL:
     L.fp4_kv_cache_write.argtypes = [KC, KB, P, I64, I64, P, I64, I64, I, P, P]
     L.fp4_kv_cache_read.argtypes = [KC, KB, P, P, I, P, P]
     L.fp4_kv_attention.argtypes = [KC, KB, P, I64, I64, I, I32, F, I32, I32, P, P, P, S, P, P]
-    L.fp4_kv_attention_workspace_bytes.argtypes = [KC, KB, I32]
+    L.fp4_kv_attention_workspace_bytes.argtypes = [KC, KB, I32, I32]
     L.fp4_kv_attention_workspace_bytes.restype = S
     L.fp4_workspace_bytes.argtypes = [I, I64, I64]
     L.fp4_workspace_bytes.restype = S
@@ -812,7 +812,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
     rows = _kv_rows(q, cache, "q")
     L = lib()
-    need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads)
+    need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, int(window))
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     status = _kv_status(status, check, q.device)

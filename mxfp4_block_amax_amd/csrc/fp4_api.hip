@@ -75,7 +75,8 @@ hipError_t device_scratch(void **out) {
     return s.err;
 }
 
-constexpr int64_t kMaxTokens = (int64_t)1 << 26;
+constexpr int64_t kMaxTokens = (int64_t)1 << 23;    // rows of a batch
+constexpr int64_t kMaxPositions = (int64_t)1 << 27;  // positions of a sequence's table
 constexpr int32_t kMaxSeqs = 1 << 20;
 static_assert(FP4_FLAG_CACHE_INDEX == fp4dev::FLAG_CACHE_INDEX, "the header states the flag");
 
@@ -94,6 +95,7 @@ fp4_status kv_args(const fp4_kv_cache *cache, const fp4_kv_batch *batch, fp4dev:
     if (cache->kv_heads < 1 || cache->kv_heads > 65535) return FP4_E_SHAPE;
     if (batch->seqs < 1 || batch->seqs > kMaxSeqs || batch->table_width < 1) return FP4_E_SHAPE;
     if (batch->table_stride < batch->table_width && batch->seqs > 1) return FP4_E_SHAPE;
+    if ((int64_t)batch->table_width * block > kMaxPositions) return FP4_E_SHAPE;
     if (batch->tokens < 0 || batch->tokens > kMaxTokens) return FP4_E_SHAPE;
     if (!aligned(cache->k_codes, 16) || !aligned(cache->v_codes, 16) ||
         !aligned(batch->cu_tokens, 4) || !aligned(batch->lengths, 4) || !aligned(batch->table, 4))
@@ -613,12 +615,12 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
 }
 
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,
-                                        int32_t heads) {
+                                        int32_t heads, int32_t window) {
     fp4dev::KvCache C;
     fp4dev::KvBatch B;
-    if (kv_args(cache, batch, &C, &B) != FP4_OK) return 0;
+    if (kv_args(cache, batch, &C, &B) != FP4_OK || window < 0) return 0;
     if (heads < 1 || heads > 65535 || heads % C.heads || B.tokens == 0) return 0;
-    return fp4dev::attention_workspace_bytes(C, B, heads);
+    return fp4dev::attention_workspace_bytes(C, B, heads, window);
 }
 
 fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *q,
@@ -641,7 +643,7 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch
     if (st != FP4_OK) return st;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) || !aligned(status, 4))
         return FP4_E_ALIGN;
-    const size_t need = fp4dev::attention_workspace_bytes(C, B, heads);
+    const size_t need = fp4dev::attention_workspace_bytes(C, B, heads, window);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_E_WORKSPACE;
     return from_hip(fp4dev::launch_attention(C, B, q, q_token_stride, q_head_stride,
                                              qt == FP4_BF16, heads, scale, causal != 0, window,

@@ -1,9 +1,23 @@
 // fp4_attention.hip - attention over the 8-bit key/value cache.
 //
 //   S_rj = scale q_r . k_j over the visible keys j of row r,
-//   out_r = sum_j exp(S_rj - m_r) v_j / sum_j exp(S_rj - m_r),  m_r = max_j S_rj.
+//   out_r = sum_j exp(S_rj) v_j / sum_j exp(S_rj).
 //
-// One pass over the keys with a running maximum and sum per row, both fp32.
+// One pass over the keys with a running reference m_r and sum per row, both
+// fp32: probabilities are p = 2^(S log2 e - m).  The reference is raised (and
+// the sums rescaled) only when some score passes it by more than 15, to 7 below
+// that score: most steps then need no rescaling and no exchange between lanes.
+//
+// First product, on the bf16 MFMA: keys E4M3(c) 2^e are exact in bf16 (the
+// converter applies the scale) and bf16 queries multiply as they are; fp32
+// queries are three bf16 terms, all 24 bits.
+// Second product, on the fp16 MFMA: p is at most 2^15 and rounded to fp16
+// (relative 2^-11, an eighth of what bf16 would lose; a row's largest p is 2^7
+// or more, so what is lost below fp16's range is under 2^-32 of it), for fp32
+// queries two fp16 terms (22 bits).  Values are E4M3(c) 2^(e - E + 6) with E
+// the largest scale exponent among the workgroup's pages: at most 28672, and
+// exact for pages within 2^-12 of the largest.  The sums take 2^(E - 6) back
+// at the end.
 #include <algorithm>
 
 #include "fp4_kernels.h"
@@ -12,119 +26,646 @@
 namespace fp4dev {
 namespace {
 
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRaiseAbove = 15.0f;  // a score this far over its reference raises it ..
+constexpr float kRaiseTo = 7.0f;      // .. to this far below that score
+constexpr int kVBias = 6;             // values are scaled by 2^kVBias over the largest page scale
+
 struct AttnArgs {
     const void *q;
     int64_t q_token, q_head;
     void *out;
     float *lse;
+    float *part_o;   // [tokens, heads, splits, dim]
+    float2 *part_ml;  // [tokens, heads, splits]: reference (base 2), sum
     int32_t heads, group, causal, window;
-    float scale;
+    int32_t sub, sub_heads;          // pieces of a group, and the query heads of one
+    int32_t rows_shift;              // log2 of the tokens of a row tile
+    int32_t splits, split_keys;      // launched splits, keys of one
+    float scale2;                    // scale log2 e
 };
 
-__device__ __forceinline__ float load_q(const void *q, int64_t at, bool bf16) {
-    return bf16 ? u2f((uint32_t)((const uint16_t *)q)[at] << 16) : ((const float *)q)[at];
+// A row tile's tokens and the keys any of them sees.
+struct Tile {
+    int64_t pos0;     // position of its first token
+    int64_t base, end;  // keys [base, end), base a multiple of 32
+    int tokens;
+};
+
+__device__ __forceinline__ Tile tile_range(const KvCache &C, const KvBatch &B, const AttnArgs &A,
+                                           const Item &it, int first_row, int32_t *status) {
+    Tile T;
+    T.tokens = min(1 << A.rows_shift, it.count - first_row);
+    const int64_t len = B.lengths[it.seq];
+    T.pos0 = len - it.count + first_row;
+    int64_t end = A.causal ? T.pos0 + T.tokens : len;
+    const int64_t held = (int64_t)B.width << C.block_shift;
+    if (end > held) {
+        if (threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
+        end = held;
+    }
+    const int64_t first = A.window > 0 ? max(T.pos0 - A.window + 1, (int64_t)0) : 0;
+    T.base = first & ~(int64_t)31;
+    T.end = max(end, T.base);
+    return T;
 }
 
-// One wave per query row.  A step takes 64 keys, one per lane for the scores;
-// then a lane has every 64th dimension of the output.
-template <bool BF16>
-__global__ __launch_bounds__(WAVE) void attention_simple_kernel(KvCache C, KvBatch B, AttnArgs A,
-                                                                int32_t *status) {
-    __shared__ float qs[256], ps[WAVE];
-    __shared__ int64_t vrow[WAVE];
-    __shared__ float vsc[WAVE];
-    const int lane = threadIdx.x;
-    const int64_t t = blockIdx.x;
-    const int hq = blockIdx.y, head = hq / A.group;
-    const Item it = find_item(B, (int)t, 0, 0);
-    const int D = C.dim;
-    for (int d = lane; d < D; d += WAVE)
-        qs[d] = load_q(A.q, t * A.q_token + hq * A.q_head + d, BF16) * A.scale;
+template <typename V, int N>
+struct Parts {
+    V p[N];
+};
+
+// x as N terms of a narrower type: each the nearest to what the ones before
+// left, an exact difference.
+template <typename V, int N>
+__device__ __forceinline__ Parts<V, N> split_parts(const float (&x)[8]) {
+    Parts<V, N> r;
+    float rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = x[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r.p[k][i] = rest[i];
+            if (k + 1 < N) rest[i] = rest[i] - (float)r.p[k][i];
+        }
+    }
+    return r;
+}
+
+// Eight cache values as bf16, the scale applied: two words of codes in order.
+__device__ __forceinline__ bf16x8_t widen_codes(uint32_t a, uint32_t b, float scale) {
+    const bf16x2_t r[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false),
+                           __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true),
+                           __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false),
+                           __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true)};
+    bf16x8_t v;
+    __builtin_memcpy(&v, r, sizeof(v));
+    return v;
+}
+
+__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(f16x8_t a, f16x8_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The converter's scale operand for a value page of scale byte `byte` where
+// the largest is `top` (255, a NaN page, stays NaN).
+__device__ __forceinline__ float v_operand(uint32_t byte, uint32_t top) {
+    const int e = (int)byte - (int)top + kVBias + (int)E8M0_ONE;
+    return u2f(byte == 255u ? 255u << 23 : (uint32_t)max(e, 0) << 23);
+}
+
+constexpr int NARROW_WG = 256;
+constexpr int NARROW_WAVES = NARROW_WG / WAVE;
+constexpr int NARROW_STEP = 32 * NARROW_WAVES;  // keys of a workgroup's step
+constexpr int NARROW_MAX_KEYS = 4096;           // keys of a split, at most
+
+// The pages under a workgroup's keys.
+constexpr int kPageSlots = NARROW_MAX_KEYS / 16 + 2;
+
+template <int D>
+struct NarrowShared {
+    union {
+        struct {
+            int page[kPageSlots];
+            uint32_t k_scale[kPageSlots], v_scale[kPageSlots];  // E8M0 bytes
+            uint32_t v_top;  // the largest of v_scale but NaN
+        };
+        float o[NARROW_WAVES][16][D + 4];
+    };
+    float m[NARROW_WAVES][16], l[NARROW_WAVES][16];
+};
+
+// A lane's values of one token: D / 16 consecutive dimensions.
+template <int D>
+struct VBytes {
+    uint32_t w[D / 64];
+};
+
+template <int D>
+__device__ __forceinline__ VBytes<D> load_v(const uint8_t *p) {
+    VBytes<D> r;
+    if constexpr (D == 64) {
+        r.w[0] = *(const uint32_t *)p;
+    } else if constexpr (D == 128) {
+        const uint2 x = *(const uint2 *)p;
+        r.w[0] = x.x, r.w[1] = x.y;
+    } else if constexpr (D == 192) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) r.w[i] = ((const uint32_t *)p)[i];
+    } else {
+        const uint4 x = *(const uint4 *)p;
+        r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+    }
+    return r;
+}
+
+// The codes of one step (32 keys): a lane's keys and values.
+template <int D>
+struct Step {
+    uint4 k[2][D / 64];  // key lane % 16 of either half, dimensions 64 c + 16 (lane / 16) ..
+    VBytes<D> v[2][4];   // keys 4 (lane / 16) + i of either half, dimensions D / 16 (lane % 16) ..
+};
+
+// Row tiles of up to 16 query rows (tokens x the query heads of one kv head):
+// single tokens, drafts, short chunks.
+//
+// A workgroup has one row tile, one kv head and one range of keys; its four
+// waves take 32 keys at a time in turn.  Scores are computed transposed,
+// S^T = K Q^T, so that a lane's scores are those of one row (lane % 16) and its
+// keys, 4 (lane / 16) + i, are the ones the second product wants from this
+// lane: probabilities go from the first product to the second without leaving
+// their lane.  Out^T = V^T P^T; which keys are which of a product's 32 terms is
+// free as long as V follows P, and which dimension is which row of a tile is
+// free too, so a lane loads D / 16 consecutive bytes of eight value rows and
+// transposes them by byte permutes.  Nothing of keys or values goes through
+// LDS: each byte is used by one lane.
+template <int D, bool F32>
+__global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache C, KvBatch B,
+                                                                        AttnArgs A,
+                                                                        int32_t *status) {
+    constexpr int CH = D / 64, NT = D / 16;
+    constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;  // terms of a query and a probability
+    // values of the next step are loaded a step ahead where registers allow
+    constexpr bool V_AHEAD = D <= 128;
+    __shared__ NarrowShared<D> sh;
+    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
+    const int r = lane & 15, g = lane >> 4;
+    const Item it = find_item(B, (int)blockIdx.x, A.rows_shift, A.rows_shift ? 1 : 0);
+    const int row0 = it.piece << A.rows_shift;
+    if (it.count <= 0 || row0 >= it.count) {
+        if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
+        return;
+    }
+    const int head = blockIdx.y / A.sub, sub = blockIdx.y - head * A.sub;
+    const int split = blockIdx.z;
+    const bool none = it.seq >= B.seqs;
+    Tile T;
+    if (none) {
+        T.tokens = min(1 << A.rows_shift, it.count - row0);
+        T.pos0 = T.base = T.end = 0;
+    } else {
+        T = tile_range(C, B, A, it, row0, status);
+    }
+    // this lane's row: token i, query head h (of the group)
+    const int h0 = sub * A.sub_heads;
+    const int hn = min(A.sub_heads, A.group - h0);
+    const int ri = r / hn, rh = r - ri * hn;
+    const bool row_real = ri < T.tokens && r < (hn << A.rows_shift);
+    const int64_t token = it.base + row0 + ri;
+    const int hq = head * A.group + h0 + rh;
+    const int64_t k0 = T.base + (int64_t)split * A.split_keys;
+    const int64_t k1 = min(k0 + A.split_keys, T.end);
+    const bool whole = T.end - T.base <= A.split_keys;  // the tile has one split
+    if (k0 >= k1 && split > 0) return;
+
+    // the keys this lane's row sees (a row that is none sees all: its sums go
+    // nowhere, and its steps need no masks)
+    const int64_t pos = T.pos0 + ri;
+    const int64_t last = row_real && A.causal ? pos : T.end - 1;
+    const int64_t first = row_real && A.window > 0 ? pos - A.window + 1 : 0;
+    // positions from here on are relative to k0
+    const int keys = (int)max(k1 - k0, (int64_t)0);
+    const int last_r = (int)max(min(last - k0, (int64_t)keys - 1), (int64_t)-1);
+    const int first_r = (int)max(min(first - k0, (int64_t)keys), (int64_t)0);
+
+    // queries: B operand, lane's row r, dimensions 64 c + 16 g + 8 h ..
+    Parts<bf16x8_t, QP> q[CH][2];
+    {
+        const int64_t at = token * A.q_token + hq * A.q_head + 16 * g;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (!F32) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (row_real) w = *(const uint4 *)((const uint16_t *)A.q + at + 64 * c + 8 * h);
+                    q[c][h].p[0] = __builtin_bit_cast(bf16x8_t, w);
+                } else {
+                    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (row_real) {
+                        const uint4 *p = (const uint4 *)((const float *)A.q + at + 64 * c + 8 * h);
+                        widen_f32x8(p[0], p[1], x);
+                    }
+                    q[c][h] = split_parts<bf16x8_t, QP>(x);
+                }
+            }
+    }
+
+    // the pages under [k0, k1)
+    const int64_t b0 = k0 >> C.block_shift;
+    const int pages = keys > 0 ? (int)(((k1 - 1) >> C.block_shift) - b0) + 1 : 0;
+    bool missing = false;
+    if (threadIdx.x == 0) sh.v_top = 0;
     __syncthreads();
-    const bool real = it.count > 0 && it.seq < B.seqs;
-    const int64_t len = real ? B.lengths[it.seq] : 0;
-    const int64_t pos = len - it.count + (t - it.base);
-    const int64_t last = real ? (A.causal ? pos : len - 1) : -1;
-    const int64_t first = A.window ? max(pos - A.window + 1, (int64_t)0) : 0;
-    float m = -__builtin_inff(), l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int64_t j0 = first; j0 <= last; j0 += WAVE) {
-        const int64_t j = j0 + lane;
-        const int page = j <= last ? find_page(B, C, it.seq, j >> C.block_shift) : -1;
-        if (j <= last && page < 0) flag(status, FLAG_CACHE_INDEX);
-        float s = -__builtin_inff();
-        int64_t at = 0;
-        if (page >= 0) {
-            at = page_offset(C, page, head) + (j & (C.block - 1)) * D;
-            float dot = 0.0f;
-            for (int d = 0; d < D; d += 4) {
-                const uint32_t w = *(const uint32_t *)(C.k_codes + at + d);
-                const f32x2_t a = e4m3_pair<false>(w), b = e4m3_pair<true>(w);
-                dot = __builtin_fmaf(qs[d], a.x, dot);
-                dot = __builtin_fmaf(qs[d + 1], a.y, dot);
-                dot = __builtin_fmaf(qs[d + 2], b.x, dot);
-                dot = __builtin_fmaf(qs[d + 3], b.y, dot);
-            }
-            s = dot * e8m0_value(C.k_scales[(int64_t)page * C.heads + head]);
-            vsc[lane] = e8m0_value(C.v_scales[(int64_t)page * C.heads + head]);
+    uint32_t v_top = 0;
+    for (int i = threadIdx.x; i < pages; i += NARROW_WG) {
+        const int page = find_page(B, C, it.seq, b0 + i);
+        const int64_t at = (int64_t)max(page, 0) * C.heads + head;
+        sh.page[i] = page;
+        const uint32_t ks = page < 0 ? 0u : C.k_scales[at], vs = page < 0 ? 0u : C.v_scales[at];
+        sh.k_scale[i] = ks;
+        sh.v_scale[i] = vs;
+        if (vs != 255u) v_top = max(v_top, vs);
+        missing |= page < 0;
+    }
+    if (v_top > 0) atomicMax(&sh.v_top, v_top);
+    if (missing) flag(status, FLAG_CACHE_INDEX);
+    __syncthreads();
+    v_top = __builtin_amdgcn_readfirstlane(sh.v_top);
+
+    const int skew = (int)(k0 & (C.block - 1));
+    const uint32_t k_lane = (uint32_t)(r * D + 16 * g);
+    const uint32_t v_lane = (uint32_t)(4 * g * D + r * (D / 16));
+    auto page_at = [&](int j) {  // of the keys from j on, relative to k0; clamped to the last
+        return __builtin_amdgcn_readfirstlane(min((j + skew) >> C.block_shift, pages - 1));
+    };
+    auto load = [&](int j, Step<D> &s, bool keys_too, bool values_too) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int jj = j + 16 * half;
+            const int page = max(__builtin_amdgcn_readfirstlane(sh.page[page_at(jj)]), 0);
+            const int64_t at = page_offset(C, page, head) + ((jj + skew) & (C.block - 1)) * D;
+            const uint8_t *kp = C.k_codes + at, *vp = C.v_codes + at;
+            if (keys_too)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) s.k[half][c] = *(const uint4 *)(kp + k_lane + 64 * c);
+            if (values_too)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s.v[half][i] = load_v<D>(vp + v_lane + i * D);
         }
-        vrow[lane] = page >= 0 ? at : -1;
-        float top = s;
-        for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, WAVE));
-        // a NaN score makes its row NaN: the maximum skips it, the sum does not
-        const float next = __builtin_fmaxf(m, top);
-        const float ref = next == -__builtin_inff() ? 0.0f : next;
-        const float p = __expf(s - ref), keep = __expf(m - ref);
-        m = next;
-        float sum = p;
-        for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, WAVE);
-        l = __builtin_fmaf(l, keep, sum);
-        ps[lane] = p;
-        __syncthreads();
-        for (int i = 0; i < 4; ++i) o[i] *= keep;
-        for (int k = 0; k < WAVE; ++k) {
-            if (vrow[k] < 0) continue;
-            const float pk = ps[k] * vsc[k];
-            for (int i = 0; i * WAVE < D; ++i) {
-                const f32x2_t v = e4m3_pair<false>(C.v_codes[vrow[k] + lane + i * WAVE]);
-                o[i] = __builtin_fmaf(pk, v.x, o[i]);
+    };
+
+    f32x4_t o[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n] = f32x4_t{0, 0, 0, 0};
+    float m = -__builtin_inff(), l = 0.0f;
+
+    auto compute = [&](int j, Step<D> &st) {
+        f32x4_t s[2];
+        float vs[2];
+        bool held[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int at = page_at(j + 16 * half);
+            held[half] = sh.page[at] >= 0;
+            const float ks = e8m0_operand(__builtin_amdgcn_readfirstlane(sh.k_scale[at]));
+            vs[half] = v_operand(__builtin_amdgcn_readfirstlane(sh.v_scale[at]), v_top);
+            s[half] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint4 w = st.k[half][c];
+                const bf16x8_t ka = widen_codes(w.x, w.y, ks), kb = widen_codes(w.z, w.w, ks);
+#pragma unroll
+                for (int p = QP - 1; p >= 0; --p) {
+                    s[half] = mfma16(ka, q[c][0].p[p], s[half]);
+                    s[half] = mfma16(kb, q[c][1].p[p], s[half]);
+                }
             }
         }
-        __syncthreads();
+        float x[8];  // base-2 scores: keys 4 g + i, then 16 + 4 g + i
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i & 3] * A.scale2;
+        // a step that some row does not see whole
+        const bool clean = j >= first_r && j + 31 <= last_r;
+        const bool edge = __ballot(!clean) != 0 || !held[0] || !held[1];
+        bool fix = false;
+        if (edge) {
+            const int top = min(keys, j + 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int key = j + 16 * (i / 4) + 4 * g + (i & 3);
+                if (key < first_r || key > last_r || !held[i / 4]) x[i] = -__builtin_inff();
+                // values nothing sees are zeros, whatever the page holds there
+                if (key >= top || !held[i / 4])
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) st.v[i / 4][i & 3].w[c] = 0;
+            }
+            // NaN values that only some rows see
+            uint32_t nan = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t &w = st.v[i / 4][i & 3].w[c];
+                    if (f2u(vs[i / 4]) == 0x7F800000u && j + 16 * (i / 4) + 4 * g + (i & 3) < top)
+                        w = 0x7F7F7F7Fu;
+                    nan |= (w & 0x7F7F7F7Fu) + 0x01010101u;
+                }
+            fix = __ballot((nan & 0x80808080u) != 0) != 0;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i]);
+        if (__ballot(top > m + kRaiseAbove) != 0) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, 16, WAVE));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32, WAVE));
+            const float next = __builtin_fmaxf(m, top - kRaiseTo);
+            const float keep = m == next ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= keep;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[n] *= keep;
+        }
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(x[i] - ref);
+            l += p[i];
+        }
+        const Parts<f16x8_t, PP> pb = split_parts<f16x8_t, PP>(p);
+        // values: tile n has dimensions NT row + n; words of two keys interleaved
+        auto codes_of = [&](auto &&word, int n, uint32_t(&w)[4]) {
+            // bytes of dimension n, keys 0..7, two to each half word
+            const int c = n / 4;
+            const uint32_t sel = (n & 2) ? 0x07030602u : 0x05010400u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = __builtin_amdgcn_perm(word(2 * k + 1, c), word(2 * k, c), sel);
+        };
+        auto pair = [&](const uint32_t(&w)[4], bool hi, float s0, float s1) {
+            f16x2_t t[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                t[k] = hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k], k < 2 ? s0 : s1, true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k], k < 2 ? s0 : s1, false);
+            f16x8_t v;
+            __builtin_memcpy(&v, t, sizeof(v));
+            return v;
+        };
+        if (!fix) {
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t w[4];
+                codes_of([&](int i, int c) { return st.v[i / 4][i & 3].w[c]; }, n, w);
+                const f16x8_t va = pair(w, false, vs[0], vs[1]), vb = pair(w, true, vs[0], vs[1]);
+#pragma unroll
+                for (int k = PP - 1; k >= 0; --k) {
+                    o[n] = mfma16(va, pb.p[k], o[n]);
+                    o[n + 1] = mfma16(vb, pb.p[k], o[n + 1]);
+                }
+            }
+        } else {
+            // The sums without the NaN values, then NaN where a row sees one:
+            // a product of where they are with who sees them counts it.
+            float see[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) see[i] = x[i] == -__builtin_inff() ? 0.0f : 1.0f;
+            const f16x8_t sb = split_parts<f16x8_t, 1>(see).p[0];
+            const float s0 = f2u(vs[0]) == 0x7F800000u ? 1.0f : vs[0];
+            const float s1 = f2u(vs[1]) == 0x7F800000u ? 1.0f : vs[1];
+            auto nans = [&](int i, int c) {  // 0x80 in the bytes that are NaN
+                return ((st.v[i / 4][i & 3].w[c] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            };
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t w[4], z[4];
+                codes_of([&](int i, int c) {
+                    const uint32_t b = nans(i, c);
+                    return st.v[i / 4][i & 3].w[c] & ~((b >> 7) * 0xFFu);
+                }, n, w);
+                codes_of([&](int i, int c) { return (nans(i, c) >> 7) * 0x38u; }, n, z);
+                const f16x8_t va = pair(w, false, s0, s1), vb = pair(w, true, s0, s1);
+#pragma unroll
+                for (int k = PP - 1; k >= 0; --k) {
+                    o[n] = mfma16(va, pb.p[k], o[n]);
+                    o[n + 1] = mfma16(vb, pb.p[k], o[n + 1]);
+                }
+                const f32x4_t zero = {0, 0, 0, 0};
+                const f32x4_t ca = mfma16(pair(z, false, 1.0f, 1.0f), sb, zero);
+                const f32x4_t cb = mfma16(pair(z, true, 1.0f, 1.0f), sb, zero);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (ca[i] > 0.0f) o[n][i] = __builtin_nanf("");
+                    if (cb[i] > 0.0f) o[n + 1][i] = __builtin_nanf("");
+                }
+            }
+        }
+    };
+
+    Step<D> now, next;
+    int j = 32 * wave;
+    if (j < keys) load(j, now, true, V_AHEAD);
+    while (j < keys) {
+        const int after = j + NARROW_STEP;
+        if (!V_AHEAD) load(j, now, false, true);
+        if (after < keys) load(after, next, true, V_AHEAD);
+        compute(j, now);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) now.k[half][c] = next.k[half][c];
+            if (V_AHEAD)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now.v[half][i] = next.v[half][i];
+        }
+        j = after;
+    }
+
+    // join the four waves
+    l += __shfl_xor(l, 16, WAVE);
+    l += __shfl_xor(l, 32, WAVE);
+    __syncthreads();  // the pages are done with
+    if (g == 0) {
+        sh.m[wave][r] = m;
+        sh.l[wave][r] = l;
+    }
+    __syncthreads();
+    float top = sh.m[0][r];
+#pragma unroll
+    for (int w = 1; w < NARROW_WAVES; ++w) top = __builtin_fmaxf(top, sh.m[w][r]);
+    const float own = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float *to = &sh.o[wave][r][NT * (4 * g + i)];
+#pragma unroll
+        for (int n = 0; n < NT; n += 4) {
+            f32x4_t y = {o[n][i], o[n + 1][i], o[n + 2][i], o[n + 3][i]};
+            y *= own;
+            *(f32x4_t *)(to + n) = y;
+        }
+    }
+    __syncthreads();
+    // 16 lanes a row, four dimensions at a time
+    const int rr = threadIdx.x >> 4, part = threadIdx.x & 15;
+    const int ti = rr / hn, th = rr - ti * hn;
+    if (ti >= T.tokens || rr >= (hn << A.rows_shift)) return;
+    float m_all = sh.m[0][rr], l_all = 0.0f;
+#pragma unroll
+    for (int w = 1; w < NARROW_WAVES; ++w) m_all = __builtin_fmaxf(m_all, sh.m[w][rr]);
+#pragma unroll
+    for (int w = 0; w < NARROW_WAVES; ++w) {
+        const float mw = sh.m[w][rr];
+        l_all = __builtin_fmaf(sh.l[w][rr],
+                               mw == m_all ? 1.0f : __builtin_amdgcn_exp2f(mw - m_all), l_all);
+    }
+    const int64_t row = (it.base + row0 + ti) * (int64_t)A.heads + head * A.group + h0 + th;
+    const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+    const int back = (int)v_top - (int)E8M0_ONE - kVBias;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int d = 64 * c + 4 * part;
+        f32x4_t y = *(const f32x4_t *)&sh.o[0][rr][d];
+#pragma unroll
+        for (int w = 1; w < NARROW_WAVES; ++w) y += *(const f32x4_t *)&sh.o[w][rr][d];
+        y *= inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_ldexpf(y[i], back);
+        if (!whole) {
+            *(f32x4_t *)(A.part_o + (row * A.splits + split) * D + d) = y;
+        } else if constexpr (!F32) {
+            const f32x2_t lo = {y.x, y.y}, hi = {y.z, y.w};
+            *(uint2 *)((uint16_t *)A.out + row * D + d) =
+                make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
+        } else {
+            *(f32x4_t *)((float *)A.out + row * D + d) = y;
+        }
+    }
+    if (part == 0) {
+        if (!whole)
+            A.part_ml[row * A.splits + split] = make_float2(m_all, l_all);
+        else if (A.lse != nullptr)
+            A.lse[row] = l_all == 0.0f ? -__builtin_inff()
+                                       : ((m_all == -__builtin_inff() ? 0.0f : m_all) +
+                                          __builtin_amdgcn_logf(l_all)) * kLn2;
+    }
+}
+
+// Joins the splits of rows that have more than one, in order: a wave a row.  A
+// split's output is normalised by its own sum, so its weight is that sum.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void attention_join_kernel(KvCache C, KvBatch B, AttnArgs A) {
+    constexpr int N = D / WAVE;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int token = blockIdx.x, hq = blockIdx.y * 4 + threadIdx.x / WAVE;
+    if (hq >= A.heads) return;
+    const int64_t row = (int64_t)token * A.heads + hq;
+    const Item it = find_item(B, token, 0, 0);
+    if (it.count <= 0 || it.seq >= B.seqs || it.piece >= it.count) return;
+    const Tile T = tile_range(C, B, A, it, it.piece >> A.rows_shift << A.rows_shift, nullptr);
+    const int n = (int)((T.end - T.base + A.split_keys - 1) / A.split_keys);
+    if (n <= 1) return;
+    const float2 *ml = A.part_ml + row * A.splits;
+    float top = -__builtin_inff();
+    for (int i = lane; i < n; i += WAVE) top = __builtin_fmaxf(top, ml[i].x);
+    for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, WAVE));
+    float l = 0.0f, o[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = 0.0f;
+    const float *po = A.part_o + row * A.splits * D + N * lane;
+    for (int i = 0; i < n; ++i) {
+        const float2 w = ml[i];
+        const float f = w.y * (w.x == top ? 1.0f : __builtin_amdgcn_exp2f(w.x - top));
+        l += f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) o[k] = __builtin_fmaf(po[(int64_t)i * D + k], f, o[k]);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t row = t * A.heads + hq;
-    for (int i = 0; i * WAVE < D; ++i) {
-        const float y = o[i] * inv;
-        const int64_t at = row * D + lane + i * WAVE;
-        if (BF16)
-            ((__bf16 *)A.out)[at] = (__bf16)y;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int64_t at = row * D + N * lane + k;
+        if constexpr (F32)
+            ((float *)A.out)[at] = o[k] * inv;
         else
-            ((float *)A.out)[at] = y;
+            ((__bf16 *)A.out)[at] = (__bf16)(o[k] * inv);
     }
     if (A.lse != nullptr && lane == 0)
-        A.lse[row] = l == 0.0f ? -__builtin_inff() : (m == -__builtin_inff() ? 0.0f : m) + __logf(l);
+        A.lse[row] = l == 0.0f ? -__builtin_inff()
+                               : ((top == -__builtin_inff() ? 0.0f : top) +
+                                  __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// How a call is laid out: from its shapes alone, which the workspace's size
+// needs too.
+struct Plan {
+    int sub, sub_heads, rows_shift, splits, split_keys;
+    int64_t items;
+};
+
+Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window) {
+    Plan P;
+    const int group = heads / C.heads;
+    P.sub = (group + 15) / 16;
+    P.sub_heads = (group + P.sub - 1) / P.sub;
+    const int64_t per = (B.tokens + B.seqs - 1) / B.seqs;  // new tokens of a sequence, on average
+    P.rows_shift = 0;
+    while ((P.sub_heads << (P.rows_shift + 1)) <= 16 && (1 << P.rows_shift) < per) ++P.rows_shift;
+    P.items = P.rows_shift ? item_count(B.tokens, B.seqs, 1 << P.rows_shift, 1) : B.tokens;
+    int64_t extent = (int64_t)B.width << C.block_shift;
+    if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + (1 << P.rows_shift) + 31);
+    const int64_t tiles = std::max<int64_t>(1, (B.tokens >> P.rows_shift)) * C.heads * P.sub;
+    const int64_t want = std::max<int64_t>(1, 2048 / tiles);
+    int64_t keys = (extent + want - 1) / want;
+    keys = (keys + NARROW_STEP - 1) / NARROW_STEP * NARROW_STEP;
+    keys = std::min<int64_t>(std::max<int64_t>(keys, 2 * NARROW_STEP), NARROW_MAX_KEYS);
+    P.split_keys = (int)keys;
+    P.splits = (int)((extent + keys - 1) / keys);
+    return P;
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads) {
-    (void)C;
-    (void)B;
-    (void)heads;
-    return 0;
+size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, int window) {
+    const Plan P = make_plan(C, B, heads, window);
+    if (P.splits <= 1) return 0;
+    // tokens, heads and splits are at most 2^23, 2^16 and 2^15: the last factor
+    // may pass 64 bits
+    size_t bytes = 0;
+    if (__builtin_mul_overflow((size_t)B.tokens * heads * P.splits,
+                               (size_t)(C.dim + 2) * sizeof(float), &bytes))
+        return SIZE_MAX;
+    return bytes;
+}
+
+template <int D>
+static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, const Plan &P,
+                       bool bf16, int32_t *status, hipStream_t s) {
+    const dim3 grid((uint32_t)P.items, C.heads * P.sub, P.splits);
+    if (bf16)
+        hipLaunchKernelGGL((attention_narrow_kernel<D, false>), grid, dim3(NARROW_WG), 0, s, C, B, A,
+                           status);
+    else
+        hipLaunchKernelGGL((attention_narrow_kernel<D, true>), grid, dim3(NARROW_WG), 0, s, C, B, A,
+                           status);
+    if (P.splits <= 1) return;
+    const dim3 join((uint32_t)B.tokens, (A.heads + 3) / 4);
+    if (bf16)
+        hipLaunchKernelGGL((attention_join_kernel<D, false>), join, dim3(256), 0, s, C, B, A);
+    else
+        hipLaunchKernelGGL((attention_join_kernel<D, true>), join, dim3(256), 0, s, C, B, A);
 }
 
 hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, int64_t q_token,
                             int64_t q_head, bool bf16, int heads, float scale, bool causal,
                             int window, void *out, float *lse, void *workspace, int32_t *status,
                             hipStream_t s) {
-    (void)workspace;
-    const AttnArgs A{q, q_token, q_head, out, lse, heads, heads / C.heads, causal, window, scale};
-    const dim3 grid((uint32_t)B.tokens, (uint32_t)heads);
-    if (bf16)
-        hipLaunchKernelGGL(attention_simple_kernel<true>, grid, dim3(WAVE), 0, s, C, B, A, status);
-    else
-        hipLaunchKernelGGL(attention_simple_kernel<false>, grid, dim3(WAVE), 0, s, C, B, A, status);
+    const Plan P = make_plan(C, B, heads, window);
+    AttnArgs A{};
+    A.q = q, A.q_token = q_token, A.q_head = q_head, A.out = out, A.lse = lse;
+    A.part_o = (float *)workspace;
+    A.part_ml = (float2 *)(A.part_o + (size_t)B.tokens * heads * P.splits * C.dim);
+    A.heads = heads, A.group = heads / C.heads, A.causal = causal, A.window = window;
+    A.sub = P.sub, A.sub_heads = P.sub_heads, A.rows_shift = P.rows_shift;
+    A.splits = P.splits, A.split_keys = P.split_keys;
+    A.scale2 = scale * kLog2e;
+    switch (C.dim) {
+        case 64: launch_dim<64>(C, B, A, P, bf16, status, s); break;
+        case 128: launch_dim<128>(C, B, A, P, bf16, status, s); break;
+        case 192: launch_dim<192>(C, B, A, P, bf16, status, s); break;
+        default: launch_dim<256>(C, B, A, P, bf16, status, s); break;
+    }
     return hipGetLastError();
 }
 
