@@ -663,7 +663,7 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
  * alone, not on the arrays; the order of every sum is fixed: deterministic.
  */
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,
-                                        int32_t heads, int32_t window);
+                                        int32_t heads, int32_t window, fp4_dtype qt);
 fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *q,
                             int64_t q_token_stride, int64_t q_head_stride, fp4_dtype qt,
                             int32_t heads, float scale, int32_t causal, int32_t window, void *out,

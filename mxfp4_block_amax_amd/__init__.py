@@ -135,7 +135,7 @@ def lib() -> ctypes.CDLL:
     L.fp4_kv_cache_write.argtypes = [KC, KB, P, I64, I64, P, I64, I64, I, P, P]
     L.fp4_kv_cache_read.argtypes = [KC, KB, P, P, I, P, P]
     L.fp4_kv_attention.argtypes = [KC, KB, P, I64, I64, I, I32, F, I32, I32, P, P, P, S, P, P]
-    L.fp4_kv_attention_workspace_bytes.argtypes = [KC, KB, I32, I32]
+    L.fp4_kv_attention_workspace_bytes.argtypes = [KC, KB, I32, I32, I]
     L.fp4_kv_attention_workspace_bytes.restype = S
     L.fp4_workspace_bytes.argtypes = [I, I64, I64]
     L.fp4_workspace_bytes.restype = S
@@ -810,13 +810,13 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
-    rows = _kv_rows(q, cache, "q")
+    rows, dtype = _kv_rows(q, cache, "q"), _dtype_code(q.dtype)
     L = lib()
-    need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, int(window))
+    need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, int(window), dtype)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     status = _kv_status(status, check, q.device)
-    _ok(L.fp4_kv_attention(cache._c, batch, *rows, _dtype_code(q.dtype), heads,
+    _ok(L.fp4_kv_attention(cache._c, batch, *rows, dtype, heads,
                            dim ** -0.5 if scale is None else float(scale), 1 if causal else 0,
                            int(window), _ptr(out), _ptr(lse), _ptr(workspace),
                            workspace.numel() if workspace is not None else 0, _ptr(status),

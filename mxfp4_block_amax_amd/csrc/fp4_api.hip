@@ -615,12 +615,12 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
 }
 
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,
-                                        int32_t heads, int32_t window) {
+                                        int32_t heads, int32_t window, fp4_dtype qt) {
     fp4dev::KvCache C;
     fp4dev::KvBatch B;
-    if (kv_args(cache, batch, &C, &B) != FP4_OK || window < 0) return 0;
+    if (kv_args(cache, batch, &C, &B) != FP4_OK || window < 0 || !valid_dtype(qt)) return 0;
     if (heads < 1 || heads > 65535 || heads % C.heads || B.tokens == 0) return 0;
-    return fp4dev::attention_workspace_bytes(C, B, heads, window);
+    return fp4dev::attention_workspace_bytes(C, B, heads, window, qt == FP4_BF16);
 }
 
 fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch, const void *q,
@@ -643,7 +643,7 @@ fp4_status fp4_kv_attention(const fp4_kv_cache *cache, const fp4_kv_batch *batch
     if (st != FP4_OK) return st;
     if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) || !aligned(status, 4))
         return FP4_E_ALIGN;
-    const size_t need = fp4dev::attention_workspace_bytes(C, B, heads, window);
+    const size_t need = fp4dev::attention_workspace_bytes(C, B, heads, window, qt == FP4_BF16);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_E_WORKSPACE;
     return from_hip(fp4dev::launch_attention(C, B, q, q_token_stride, q_head_stride,
                                              qt == FP4_BF16, heads, scale, causal != 0, window,

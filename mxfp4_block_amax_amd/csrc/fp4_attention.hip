@@ -46,7 +46,7 @@ struct AttnArgs {
     float2 *part_ml;  // [tokens, heads, splits]: reference (base 2), sum
     int32_t heads, group, causal, window;
     int32_t sub, sub_heads;          // pieces of a group, and the query heads of one
-    int32_t rows_shift;              // log2 of the tokens of a row tile
+    int32_t items, tokens;           // row tiles launched, and the tokens of one
     int32_t splits, split_keys;      // launched splits, keys of one
     float scale2;                    // scale log2 e
 };
@@ -61,7 +61,7 @@ struct Tile {
 __device__ __forceinline__ Tile tile_range(const KvCache &C, const KvBatch &B, const AttnArgs &A,
                                            const Item &it, int first_row, int32_t *status) {
     Tile T;
-    T.tokens = min(1 << A.rows_shift, it.count - first_row);
+    T.tokens = min(A.tokens, it.count - first_row);
     const int64_t len = B.lengths[it.seq];
     T.pos0 = len - it.count + first_row;
     int64_t end = A.causal ? T.pos0 + T.tokens : len;
@@ -201,8 +201,8 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     __shared__ NarrowShared<D> sh;
     const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
     const int r = lane & 15, g = lane >> 4;
-    const Item it = find_item(B, (int)blockIdx.x, A.rows_shift, A.rows_shift ? 1 : 0);
-    const int row0 = it.piece << A.rows_shift;
+    const Item it = find_item(B, (int)blockIdx.x, A.tokens, A.tokens > 1 ? 1 : 0);
+    const int row0 = it.piece * A.tokens;
     if (it.count <= 0 || row0 >= it.count) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     const bool none = it.seq >= B.seqs;
     Tile T;
     if (none) {
-        T.tokens = min(1 << A.rows_shift, it.count - row0);
+        T.tokens = min(A.tokens, it.count - row0);
         T.pos0 = T.base = T.end = 0;
     } else {
         T = tile_range(C, B, A, it, row0, status);
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     const int h0 = sub * A.sub_heads;
     const int hn = min(A.sub_heads, A.group - h0);
     const int ri = r / hn, rh = r - ri * hn;
-    const bool row_real = ri < T.tokens && r < (hn << A.rows_shift);
+    const bool row_real = ri < T.tokens;
     const int64_t token = it.base + row0 + ri;
     const int hq = head * A.group + h0 + rh;
     const int64_t k0 = T.base + (int64_t)split * A.split_keys;
@@ -500,7 +500,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     // 16 lanes a row, four dimensions at a time
     const int rr = threadIdx.x >> 4, part = threadIdx.x & 15;
     const int ti = rr / hn, th = rr - ti * hn;
-    if (ti >= T.tokens || rr >= (hn << A.rows_shift)) return;
+    if (ti >= T.tokens) return;
     float m_all = sh.m[0][rr], l_all = 0.0f;
 #pragma unroll
     for (int w = 1; w < NARROW_WAVES; ++w) m_all = __builtin_fmaxf(m_all, sh.m[w][rr]);
@@ -552,9 +552,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(KvCache C, KvBatch 
     const int token = blockIdx.x, hq = blockIdx.y * 4 + threadIdx.x / WAVE;
     if (hq >= A.heads) return;
     const int64_t row = (int64_t)token * A.heads + hq;
-    const Item it = find_item(B, token, 0, 0);
+    const Item it = find_item(B, token, 1, 0);
     if (it.count <= 0 || it.seq >= B.seqs || it.piece >= it.count) return;
-    const Tile T = tile_range(C, B, A, it, it.piece >> A.rows_shift << A.rows_shift, nullptr);
+    const Tile T = tile_range(C, B, A, it, it.piece / A.tokens * A.tokens, nullptr);
     const int n = (int)((T.end - T.base + A.split_keys - 1) / A.split_keys);
     if (n <= 1) return;
     const float2 *ml = A.part_ml + row * A.splits;
@@ -587,25 +587,423 @@ __global__ __launch_bounds__(256) void attention_join_kernel(KvCache C, KvBatch 
                                   __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+// ---- row tiles of 128 ------------------------------------------------------
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mfma32(f16x8_t a, f16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f16x8_t widen_values(uint2 w, float scale) {
+    const f16x2_t r[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, scale, false),
+                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, scale, true),
+                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, scale, false),
+                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, scale, true)};
+    f16x8_t v;
+    __builtin_memcpy(&v, r, sizeof(v));
+    return v;
+}
+
+constexpr int WIDE_WG = 256;
+constexpr int WIDE_ROWS = 128;
+constexpr int WIDE_STEP = 64;       // keys of a step
+constexpr int WIDE_SEGMENT = 2048;  // keys whose pages are held in LDS
+
+template <int D>
+struct WideShared {
+    uint4 k[2][WIDE_STEP * D / 16];  // [key][16-byte chunk ^ swizzle]
+    uint2 v[2][WIDE_STEP * D / 8];   // [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
+    int page[WIDE_SEGMENT / 16 + 1];
+    uint8_t k_scale[WIDE_SEGMENT / 16 + 1], v_scale[WIDE_SEGMENT / 16 + 1];
+    uint32_t v_top;
+};
+
+// The chunk of a key row that LDS chunk c of the row holds: rows of D bytes
+// that start in the same banks spread their chunks over all of them.
+template <int D>
+__device__ __forceinline__ int key_swizzle(int row) {
+    return D % 128 == 0 ? row & 7 : (row >> 1) & 3;
+}
+
+// Row tiles of up to 128 query rows: chunks and whole prompts, bf16 queries.
+//
+// As above, but the four waves share the keys and have 32 rows each: scores
+// S^T = K Q^T and sums out^T = V^T P^T on 32 x 32 tiles, probabilities staying
+// in their lanes.  A step of 64 keys is loaded a step ahead and put into LDS as
+// codes, half of what bf16 tiles would take (four waves reading 32 KB a step
+// would keep LDS as busy as the MFMA); each wave widens what it multiplies.
+// Values are transposed on their way into LDS, eight keys of a dimension side by
+// side, once for the four waves.
+template <int D>
+__global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, KvBatch B,
+                                                                    AttnArgs A, int32_t *status) {
+    constexpr int KC = D / 16;               // 16-byte chunks of a key
+    constexpr int NT = D / 32;               // 32-dimension tiles of the output
+    constexpr int W4 = D / 128, W2 = D % 128 / 64;  // a lane's words and half words of a value
+    constexpr int KL = WIDE_STEP * KC / WIDE_WG;    // key chunks a thread loads
+    __shared__ WideShared<D> sh;
+    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
+    const int r = lane & 31, h = lane >> 5;
+    // workgroups in launch order: head, then row tile (the last, with the most
+    // keys, first), then split
+    const uint32_t hs = A.sub * C.heads;
+    const int headsub = blockIdx.x % hs;
+    const uint32_t rest = blockIdx.x / hs;
+    const int split = rest / (uint32_t)A.items;
+    const int item = A.items - 1 - (int)(rest - (uint32_t)split * A.items);
+    const Item it = find_item(B, item, A.tokens, A.tokens > 1 ? 1 : 0);
+    const int row0 = it.piece * A.tokens;
+    if (it.count <= 0 || row0 >= it.count) {
+        if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
+        return;
+    }
+    const int head = headsub / A.sub, sub = headsub - head * A.sub;
+    Tile T;
+    if (it.seq >= B.seqs) {
+        T.tokens = min(A.tokens, it.count - row0);
+        T.pos0 = T.base = T.end = 0;
+    } else {
+        T = tile_range(C, B, A, it, row0, status);
+    }
+    const int h0 = sub * A.sub_heads;
+    const int hn = min(A.sub_heads, A.group - h0);
+    const int row = 32 * wave + r;
+    const int ri = row / hn, rh = row - ri * hn;
+    const bool row_real = ri < T.tokens;
+    const int64_t token = it.base + row0 + ri;
+    const int hq = head * A.group + h0 + rh;
+    const int64_t k0 = T.base + (int64_t)split * A.split_keys;
+    const int64_t k1 = min(k0 + A.split_keys, T.end);
+    const bool whole = T.end - T.base <= A.split_keys;
+    if (k0 >= k1 && split > 0) return;
+
+    const int64_t pos = T.pos0 + ri;
+    const int64_t last = row_real && A.causal ? pos : T.end - 1;
+    const int64_t first = row_real && A.window > 0 ? pos - A.window + 1 : 0;
+    const int keys = (int)max(k1 - k0, (int64_t)0);
+    const int last_r = (int)max(min(last - k0, (int64_t)keys - 1), (int64_t)-1);
+    const int first_r = (int)max(min(first - k0, (int64_t)keys), (int64_t)0);
+    // the keys any row of this wave sees
+    const int wave_last = (int)wave_max_u32(row_real ? (uint32_t)(last_r + 1) : 0u) - 1;
+    const int wave_first = (int)wave_min_u32(row_real ? (uint32_t)first_r : 0x7FFFFFFFu);
+
+    bf16x8_t q[KC / 2][2];
+    {
+        const uint16_t *p = (const uint16_t *)A.q + token * A.q_token + hq * A.q_head + 16 * h;
+#pragma unroll
+        for (int c = 0; c < KC / 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (row_real) w = *(const uint4 *)(p + 32 * c + 8 * e);
+                q[c][e] = __builtin_bit_cast(bf16x8_t, w);
+            }
+    }
+
+    // the next step's codes, in registers
+    uint4 kr[KL];
+    uint32_t vr[W4 + W2][8];
+    const int vt = threadIdx.x >> 6, vh = h, vm = r;  // this thread's values: keys of 16 vt, half vh
+    const int skew = (int)(k0 & (C.block - 1));
+    auto load = [&](int j, int seg) {  // keys j .. of the split, in the segment from seg on
+        const int lim = ((min(seg + WIDE_SEGMENT, keys) - 1 + skew) >> C.block_shift) -
+                        ((seg + skew) >> C.block_shift);
+        auto place = [&](int key, int64_t &at) {  // a 16-key group's codes; whether it has any
+            const int p = ((key + skew) >> C.block_shift) - ((seg + skew) >> C.block_shift);
+            const int page = sh.page[min(p, lim)];
+            at = page_offset(C, max(page, 0), head) + ((key + skew) & (C.block - 1)) * D;
+            return page >= 0;
+        };
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+            const int c = threadIdx.x + i * WIDE_WG;
+            const int key = c / KC;
+            int64_t at;
+            place(j + (key & ~15), at);
+            kr[i] = *(const uint4 *)(C.k_codes + at + (key & 15) * D + 16 * (c - key * KC));
+        }
+        int64_t at;
+        const bool held = place(j + 16 * vt, at);
+        const uint8_t *vp = C.v_codes + at + 4 * vh * D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row_at = (8 * (i / 4) + (i & 3)) * D;  // keys 4 h + 0..3, 8 + 4 h + 0..3
+#pragma unroll
+            for (int w = 0; w < W4; ++w)
+                vr[w][i] = *(const uint32_t *)(vp + row_at + 128 * w + 4 * vm);
+            if (W2) vr[W4][i] = *(const uint16_t *)(vp + row_at + 128 * W4 + 2 * vm);
+        }
+        // values nothing sees are zeros, whatever the page holds there
+        if (!held || j + WIDE_STEP > keys) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int key = j + 16 * vt + 4 * vh + 8 * (i / 4) + (i & 3);
+#pragma unroll
+                for (int w = 0; w < W4 + W2; ++w)
+                    if (!held || key >= keys) vr[w][i] = 0;
+            }
+        }
+    };
+    auto store = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+            const int c = threadIdx.x + i * WIDE_WG;
+            const int key = c / KC;
+            sh.k[buf][key * KC + ((c - key * KC) ^ key_swizzle<D>(key))] = kr[i];
+        }
+#pragma unroll
+        for (int w = 0; w < W4 + W2; ++w) {
+            // bytes of two keys side by side, then of four
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                lo[k] = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], 0x05010400u);
+                hi[k] = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], 0x07030602u);
+            }
+            uint2 *to = &sh.v[buf][((vt * NT + 4 * w) * 2 + vh) * 32 + vm];
+#pragma unroll
+            for (int n = 0; n < (w < W4 ? 4 : 2); ++n) {
+                const uint32_t sel = (n & 1) ? 0x07060302u : 0x05040100u;
+                const uint32_t a0 = n < 2 ? lo[0] : hi[0], a1 = n < 2 ? lo[1] : hi[1];
+                const uint32_t b0 = n < 2 ? lo[2] : hi[2], b1 = n < 2 ? lo[3] : hi[3];
+                to[n * 64] = make_uint2(__builtin_amdgcn_perm(a1, a0, sel),
+                                        __builtin_amdgcn_perm(b1, b0, sel));
+            }
+        }
+    };
+
+    f32x16_t o[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n] = f32x16_t{};
+    float m = -__builtin_inff(), l = 0.0f;
+    uint32_t v_top = 0;
+
+    auto compute = [&](int buf, int j, int seg) {
+        // pages of the step's four 16-key groups
+        const int p0 = (seg + skew) >> C.block_shift;
+        const int lim = ((min(seg + WIDE_SEGMENT, keys) - 1 + skew) >> C.block_shift) - p0;
+        int at[4];
+        bool held = true;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            at[t] = min(((j + 16 * t + skew) >> C.block_shift) - p0, lim);
+            held = held && sh.page[at[t]] >= 0;
+        }
+        f32x16_t s[2];
+        float ks[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            s[u] = f32x16_t{};
+            ks[u] = e8m0_operand(sh.k_scale[(r & 16) ? at[2 * u + 1] : at[2 * u]]);
+        }
+#pragma unroll
+        for (int c = 0; c < KC / 2; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint4 w = sh.k[buf][(32 * u + r) * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
+                s[u] = mfma32(widen_codes(w.x, w.y, ks[u]), q[c][0], s[u]);
+                s[u] = mfma32(widen_codes(w.z, w.w, ks[u]), q[c][1], s[u]);
+            }
+        const bool clean = j >= first_r && j + WIDE_STEP - 1 <= last_r;
+        const bool edge = __ballot(!clean) != 0 || !held;
+        bool fix = false;
+        if (edge) {
+            uint32_t nan = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = j + 32 * u + 8 * (i / 4) + 4 * h + (i & 3);
+                    const bool in = key >= first_r && key <= last_r;
+                    s[u][i] = in && sh.page[at[2 * u + i / 8]] >= 0 ? s[u][i] * A.scale2
+                                                                     : -__builtin_inff();
+                }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (sh.v_scale[at[t]] == 255u && sh.page[at[t]] >= 0) nan = 0x80808080u;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 w = sh.v[buf][((t * NT + n) * 2 + h) * 32 + r];
+                    nan |= (w.x & 0x7F7F7F7Fu) + 0x01010101u;
+                    nan |= (w.y & 0x7F7F7F7Fu) + 0x01010101u;
+                }
+            }
+            fix = __ballot((nan & 0x80808080u) != 0) != 0;
+        }
+        // scores in base 2 are s times this
+        const float c2 = edge ? 1.0f : A.scale2;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[u][i] * c2);
+        if (__ballot(top > m + kRaiseAbove) != 0) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32, WAVE));
+            const float next = __builtin_fmaxf(m, top - kRaiseTo);
+            const float keep = m == next ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= keep;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[n] *= keep;
+        }
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -ref));
+                l += p[i];
+            }
+            const f16x8_t pb = split_parts<f16x8_t, 1>(p).p[0];
+            const uint32_t vb = __builtin_amdgcn_readfirstlane(sh.v_scale[at[t]]);
+            const float vs = v_operand(vb, v_top);
+            const uint2 *from = &sh.v[buf][(t * NT * 2 + h) * 32 + r];
+            if (!fix) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    o[n] = mfma32(widen_values(from[n * 64], vs), pb, o[n]);
+            } else {
+                // the sums without NaN values, then NaN where a row sees one
+                float see[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    see[i] = s[t / 2][8 * (t & 1) + i] == -__builtin_inff() ? 0.0f : 1.0f;
+                const f16x8_t sb = split_parts<f16x8_t, 1>(see).p[0];
+                const bool all = vb == 255u;
+                const uint32_t empty = all ? 0x01010101u : 0u;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 w = from[n * 64];
+                    const uint32_t za = ((((w.x & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | empty;
+                    const uint32_t zb = ((((w.y & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | empty;
+                    o[n] = mfma32(widen_values(make_uint2(w.x & ~(za * 0xFFu), w.y & ~(zb * 0xFFu)),
+                                               all ? 1.0f : vs), pb, o[n]);
+                    const f32x16_t count = mfma32(
+                        widen_values(make_uint2(za * 0x38u, zb * 0x38u), 1.0f), sb, f32x16_t{});
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (count[i] > 0.0f) o[n][i] = __builtin_nanf("");
+                }
+            }
+        }
+    };
+
+    for (int seg = 0; seg < keys; seg += WIDE_SEGMENT) {
+        const int seg_end = min(seg + WIDE_SEGMENT, keys);
+        const int64_t b0 = (k0 + seg) >> C.block_shift;
+        const int pages = (int)(((k0 + seg_end - 1) >> C.block_shift) - b0) + 1;
+        __syncthreads();  // the last segment's pages are done with
+        if (threadIdx.x == 0) sh.v_top = v_top;
+        __syncthreads();
+        bool missing = false;
+        if (threadIdx.x < pages) {
+            const int page = find_page(B, C, it.seq, b0 + threadIdx.x);
+            const int64_t at = (int64_t)max(page, 0) * C.heads + head;
+            const uint32_t kb = page < 0 ? 0u : C.k_scales[at], vb = page < 0 ? 0u : C.v_scales[at];
+            sh.page[threadIdx.x] = page;
+            sh.k_scale[threadIdx.x] = (uint8_t)kb;
+            sh.v_scale[threadIdx.x] = (uint8_t)vb;
+            missing = page < 0;
+            if (vb != 255u && vb > v_top) atomicMax(&sh.v_top, vb);
+        }
+        if (missing) flag(status, FLAG_CACHE_INDEX);
+        __syncthreads();
+        const uint32_t v_next = __builtin_amdgcn_readfirstlane(sh.v_top);
+        if (v_next > v_top) {
+            const float down = e8m0_value(E8M0_ONE - min(v_next - v_top, E8M0_ONE));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[n] *= down;
+            v_top = v_next;
+        }
+        load(seg, seg);
+        store(0);
+        __syncthreads();
+        int buf = 0;
+        for (int j = seg; j < seg_end; j += WIDE_STEP) {
+            const bool more = j + WIDE_STEP < seg_end;
+            if (more) load(j + WIDE_STEP, seg);
+            if (j <= wave_last && j + WIDE_STEP > wave_first) compute(buf, j, seg);
+            if (more) store(buf ^ 1);
+            __syncthreads();
+            buf ^= 1;
+        }
+    }
+
+    if (!row_real) return;
+    l += __shfl_xor(l, 32, WAVE);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int back = (int)v_top - (int)E8M0_ONE - kVBias;
+    const int64_t to = token * A.heads + hq;
+    auto put = [&](int d, const float *y, int n) {  // n (2 or 4) values from dimension d on
+        if (!whole) {
+            float *p = A.part_o + (to * A.splits + split) * D + d;
+            for (int i = 0; i < n; ++i) p[i] = y[i];
+        } else {
+            __bf16 *p = (__bf16 *)A.out + to * D + d;
+            typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+            if (n == 4)
+                *(bf16x4_t *)p = bf16x4_t{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+            else
+                *(bf16x2_t *)p = bf16x2_t{(__bf16)y[0], (__bf16)y[1]};
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int mm = 8 * (i / 4) + 4 * h + (i & 3);
+#pragma unroll
+        for (int w = 0; w < W4 + W2; ++w) {
+            constexpr int N4 = 4;
+            const int n = w < W4 ? N4 : 2;
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < (w < W4 ? 4 : 2); ++k)
+                y[k] = __builtin_ldexpf(o[4 * w + k][i] * inv, back);
+            put(128 * w + n * mm, y, n);
+        }
+    }
+    if (h == 0) {
+        if (!whole)
+            A.part_ml[to * A.splits + split] = make_float2(m, l);
+        else if (A.lse != nullptr)
+            A.lse[to] = l == 0.0f ? -__builtin_inff()
+                                  : ((m == -__builtin_inff() ? 0.0f : m) + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+}
+
 // How a call is laid out: from its shapes alone, which the workspace's size
 // needs too.
 struct Plan {
-    int sub, sub_heads, rows_shift, splits, split_keys;
+    bool wide;
+    int sub, sub_heads, tokens, splits, split_keys;
     int64_t items;
 };
 
-Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window) {
+Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool bf16) {
     Plan P;
     const int group = heads / C.heads;
-    P.sub = (group + 15) / 16;
-    P.sub_heads = (group + P.sub - 1) / P.sub;
     const int64_t per = (B.tokens + B.seqs - 1) / B.seqs;  // new tokens of a sequence, on average
-    P.rows_shift = 0;
-    while ((P.sub_heads << (P.rows_shift + 1)) <= 16 && (1 << P.rows_shift) < per) ++P.rows_shift;
-    P.items = P.rows_shift ? item_count(B.tokens, B.seqs, 1 << P.rows_shift, 1) : B.tokens;
+    P.wide = bf16 && per * group > 64 && C.dim <= 128;
+    const int rows = P.wide ? WIDE_ROWS : 16;
+    P.sub = (group + rows - 1) / rows;
+    P.sub_heads = (group + P.sub - 1) / P.sub;
+    P.tokens = (int)std::min<int64_t>(rows / P.sub_heads, per);
+    P.items = P.tokens > 1 ? item_count(B.tokens, B.seqs, P.tokens, 1) : B.tokens;
     int64_t extent = (int64_t)B.width << C.block_shift;
-    if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + (1 << P.rows_shift) + 31);
-    const int64_t tiles = std::max<int64_t>(1, (B.tokens >> P.rows_shift)) * C.heads * P.sub;
+    if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + P.tokens + 31);
+    const int64_t tiles = std::max<int64_t>(1, B.tokens / P.tokens) * C.heads * P.sub;
+    if (P.wide) {
+        const int64_t want = std::max<int64_t>(1, 512 / tiles);
+        int64_t keys = (extent + want - 1) / want;
+        keys = (keys + WIDE_SEGMENT - 1) / WIDE_SEGMENT * WIDE_SEGMENT;
+        P.split_keys = (int)keys;
+        P.splits = (int)((extent + keys - 1) / keys);
+        return P;
+    }
     const int64_t want = std::max<int64_t>(1, 2048 / tiles);
     int64_t keys = (extent + want - 1) / want;
     keys = (keys + NARROW_STEP - 1) / NARROW_STEP * NARROW_STEP;
@@ -617,8 +1015,9 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window) {
 
 }  // namespace
 
-size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, int window) {
-    const Plan P = make_plan(C, B, heads, window);
+size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, int window,
+                                 bool bf16) {
+    const Plan P = make_plan(C, B, heads, window, bf16);
     if (P.splits <= 1) return 0;
     // tokens, heads and splits are at most 2^23, 2^16 and 2^15: the last factor
     // may pass 64 bits
@@ -633,12 +1032,18 @@ template <int D>
 static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, const Plan &P,
                        bool bf16, int32_t *status, hipStream_t s) {
     const dim3 grid((uint32_t)P.items, C.heads * P.sub, P.splits);
-    if (bf16)
-        hipLaunchKernelGGL((attention_narrow_kernel<D, false>), grid, dim3(NARROW_WG), 0, s, C, B, A,
-                           status);
-    else
+    if (P.wide) {
+        if constexpr (D <= 128)
+            hipLaunchKernelGGL(attention_wide_kernel<D>,
+                               dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)), dim3(WIDE_WG),
+                               0, s, C, B, A, status);
+    } else if (bf16) {
+        hipLaunchKernelGGL((attention_narrow_kernel<D, false>), grid, dim3(NARROW_WG), 0, s, C, B,
+                           A, status);
+    } else {
         hipLaunchKernelGGL((attention_narrow_kernel<D, true>), grid, dim3(NARROW_WG), 0, s, C, B, A,
                            status);
+    }
     if (P.splits <= 1) return;
     const dim3 join((uint32_t)B.tokens, (A.heads + 3) / 4);
     if (bf16)
@@ -651,13 +1056,13 @@ hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, i
                             int64_t q_head, bool bf16, int heads, float scale, bool causal,
                             int window, void *out, float *lse, void *workspace, int32_t *status,
                             hipStream_t s) {
-    const Plan P = make_plan(C, B, heads, window);
+    const Plan P = make_plan(C, B, heads, window, bf16);
     AttnArgs A{};
     A.q = q, A.q_token = q_token, A.q_head = q_head, A.out = out, A.lse = lse;
     A.part_o = (float *)workspace;
     A.part_ml = (float2 *)(A.part_o + (size_t)B.tokens * heads * P.splits * C.dim);
     A.heads = heads, A.group = heads / C.heads, A.causal = causal, A.window = window;
-    A.sub = P.sub, A.sub_heads = P.sub_heads, A.rows_shift = P.rows_shift;
+    A.sub = P.sub, A.sub_heads = P.sub_heads, A.items = (int)P.items, A.tokens = P.tokens;
     A.splits = P.splits, A.split_keys = P.split_keys;
     A.scale2 = scale * kLog2e;
     switch (C.dim) {

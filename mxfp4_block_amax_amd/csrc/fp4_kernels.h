@@ -120,7 +120,8 @@ hipError_t launch_kv_write(const KvCache &C, const KvBatch &B, const void *k, co
                            int64_t v_head, int32_t *status, hipStream_t s);
 hipError_t launch_kv_read(const KvCache &C, const KvBatch &B, void *k, void *v, bool bf16,
                           int32_t *status, hipStream_t s);
-size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, int window);
+size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, int window,
+                                 bool bf16);
 hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, int64_t q_token,
                             int64_t q_head, bool bf16, int heads, float scale, bool causal,
                             int window, void *out, float *lse, void *workspace, int32_t *status,

@@ -42,13 +42,13 @@ struct Item {
     int seq, piece, base, count;  // base, count: the sequence's rows [base, base + count)
 };
 
-__device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit_shift, int extra) {
+__device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit, int extra) {
     const int lane = threadIdx.x & (WAVE - 1);
     int lo = 0, n = B.seqs + 1;
     while (n > 1) {
         const int step = (n + WAVE - 1) / WAVE;
         const int i = lo + lane * step;
-        const bool at = lane * step < n && (B.cu[i] >> unit_shift) + extra * i <= item;
+        const bool at = lane * step < n && B.cu[i] / unit + extra * i <= item;
         const uint64_t b = __ballot(at);
         const int k = b ? 63 - __builtin_clzll(b) : 0;
         lo += k * step;
@@ -58,7 +58,7 @@ __device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit_s
     Item it;
     it.seq = lo;
     it.base = B.cu[lo];
-    it.piece = item - ((it.base >> unit_shift) + extra * lo);
+    it.piece = item - (it.base / unit + extra * lo);
     it.count = (lo < B.seqs ? B.cu[lo + 1] : B.tokens) - it.base;
     // a cu that is no prefix sum of at most `tokens` rows gives no piece
     if (it.base < 0 || it.count < 0 || it.base > B.tokens || it.count > B.tokens - it.base ||

@@ -63,7 +63,7 @@ template <bool BF16>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, const void *k,
                                                        const void *v, KvStrides S,
                                                        int32_t *status) {
-    const Item it = find_item(B, (int)blockIdx.x, C.block_shift, 2);
+    const Item it = find_item(B, (int)blockIdx.x, C.block, 2);
     if (it.seq >= B.seqs || it.count <= 0) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
 template <bool BF16>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache C, KvBatch B, void *k, void *v,
                                                       int32_t *status) {
-    const Item it = find_item(B, (int)blockIdx.x, C.block_shift, 2);
+    const Item it = find_item(B, (int)blockIdx.x, C.block, 2);
     if (it.count <= 0) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
