@@ -19,6 +19,7 @@
 // exact for pages within 2^-12 of the largest.  The sums take 2^(E - 6) back
 // at the end.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4_kernels.h"
 #include "fp4_kv.h"
@@ -48,7 +49,8 @@ struct AttnArgs {
     int32_t sub, sub_heads;          // pieces of a group, and the query heads of one
     int32_t items, tokens;           // row tiles launched, and the tokens of one
     int32_t splits, split_keys;      // launched splits, keys of one
-    float scale2;                    // scale log2 e
+    float scale2;                    // |scale| log2 e
+    uint32_t q_sign;                 // sign bits of two bf16 queries (or of one fp32) if scale < 0
 };
 
 // A row tile's tokens and the keys any of them sees.
@@ -250,6 +252,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
                 if constexpr (!F32) {
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (row_real) w = *(const uint4 *)((const uint16_t *)A.q + at + 64 * c + 8 * h);
+                    w.x ^= A.q_sign, w.y ^= A.q_sign, w.z ^= A.q_sign, w.w ^= A.q_sign;
                     q[c][h].p[0] = __builtin_bit_cast(bf16x8_t, w);
                 } else {
                     float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -257,6 +260,8 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
                         const uint4 *p = (const uint4 *)((const float *)A.q + at + 64 * c + 8 * h);
                         widen_f32x8(p[0], p[1], x);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = u2f(f2u(x[i]) ^ A.q_sign);
                     q[c][h] = split_parts<bf16x8_t, QP>(x);
                 }
             }
@@ -615,11 +620,13 @@ constexpr int WIDE_SEGMENT = 2048;  // keys whose pages are held in LDS
 
 template <int D>
 struct WideShared {
-    uint4 k[2][WIDE_STEP * D / 16];  // [key][16-byte chunk ^ swizzle]
+    u32x4_t k[2][WIDE_STEP * D / 16];  // [key][16-byte chunk ^ swizzle]
     uint2 v[2][WIDE_STEP * D / 8];   // [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
     int page[WIDE_SEGMENT / 16 + 1];
     uint8_t k_scale[WIDE_SEGMENT / 16 + 1], v_scale[WIDE_SEGMENT / 16 + 1];
-    uint32_t v_top;
+    uint8_t v_nan[WIDE_SEGMENT / 16 + 1];  // pages whose value scale is NaN
+    uint32_t v_top, seg_nan;
+    uint32_t nan[2];  // whether values of the step were NaN and taken out
 };
 
 // The chunk of a key row that LDS chunk c of the row holds: rows of D bytes
@@ -689,6 +696,10 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     const int first_r = (int)max(min(first - k0, (int64_t)keys), (int64_t)0);
     // the keys any row of this wave sees
     const int wave_last = (int)wave_max_u32(row_real ? (uint32_t)(last_r + 1) : 0u) - 1;
+    // the keys every row of the tile sees
+    const int tile_last = (int)min((A.causal ? T.pos0 : T.end - 1) - k0, (int64_t)keys - 1);
+    const int tile_first =
+        A.window > 0 ? (int)max(min(T.pos0 + T.tokens - A.window - k0, (int64_t)keys), (int64_t)0) : 0;
     const int wave_first = (int)wave_min_u32(row_real ? (uint32_t)first_r : 0x7FFFFFFFu);
 
     bf16x8_t q[KC / 2][2];
@@ -700,21 +711,25 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             for (int e = 0; e < 2; ++e) {
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (row_real) w = *(const uint4 *)(p + 32 * c + 8 * e);
+                w.x ^= A.q_sign, w.y ^= A.q_sign, w.z ^= A.q_sign, w.w ^= A.q_sign;
                 q[c][e] = __builtin_bit_cast(bf16x8_t, w);
             }
     }
 
     // the next step's codes, in registers
-    uint4 kr[KL];
-    uint32_t vr[W4 + W2][8];
+    u32x4_t kr[KL];
+    uint32_t vr[W4 + W2][8], any_nan = 0;
+    bool seg_nan = false;
     const int vt = threadIdx.x >> 6, vh = h, vm = r;  // this thread's values: keys of 16 vt, half vh
     const int skew = (int)(k0 & (C.block - 1));
     auto load = [&](int j, int seg) {  // keys j .. of the split, in the segment from seg on
         const int lim = ((min(seg + WIDE_SEGMENT, keys) - 1 + skew) >> C.block_shift) -
                         ((seg + skew) >> C.block_shift);
+        auto place_at = [&](int key) {  // its page among the segment's
+            return min(((key + skew) >> C.block_shift) - ((seg + skew) >> C.block_shift), lim);
+        };
         auto place = [&](int key, int64_t &at) {  // a 16-key group's codes; whether it has any
-            const int p = ((key + skew) >> C.block_shift) - ((seg + skew) >> C.block_shift);
-            const int page = sh.page[min(p, lim)];
+            const int page = sh.page[place_at(key)];
             at = page_offset(C, max(page, 0), head) + ((key + skew) & (C.block - 1)) * D;
             return page >= 0;
         };
@@ -724,7 +739,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             const int key = c / KC;
             int64_t at;
             place(j + (key & ~15), at);
-            kr[i] = *(const uint4 *)(C.k_codes + at + (key & 15) * D + 16 * (c - key * KC));
+            kr[i] = *(const u32x4_t *)(C.k_codes + at + (key & 15) * D + 16 * (c - key * KC));
         }
         int64_t at;
         const bool held = place(j + 16 * vt, at);
@@ -747,6 +762,21 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
                     if (!held || key >= keys) vr[w][i] = 0;
             }
         }
+        // NaN values of a step that not every row sees whole would reach rows
+        // that do not see them (0 times NaN): they are taken out here and marked
+        // afterwards.  Where every row sees them the sums do it by themselves.
+        any_nan = 0;
+        if (seg_nan || j < tile_first || j + WIDE_STEP - 1 > tile_last) {
+            const uint32_t every = held && sh.v_nan[place_at(j + 16 * vt)] ? 0x01010101u : 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int w = 0; w < W4 + W2; ++w) {
+                    const uint32_t z = ((((vr[w][i] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | every;
+                    vr[w][i] &= ~(z * 0xFFu);
+                    any_nan |= z;
+                }
+        }
     };
     auto store = [&](int buf) {
 #pragma unroll
@@ -755,6 +785,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             const int key = c / KC;
             sh.k[buf][key * KC + ((c - key * KC) ^ key_swizzle<D>(key))] = kr[i];
         }
+        if (any_nan) sh.nan[buf] = 1;
 #pragma unroll
         for (int w = 0; w < W4 + W2; ++w) {
             // bytes of two keys side by side, then of four
@@ -804,43 +835,30 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
         for (int c = 0; c < KC / 2; ++c)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint4 w = sh.k[buf][(32 * u + r) * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
+                const u32x4_t w = sh.k[buf][(32 * u + r) * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
                 s[u] = mfma32(widen_codes(w.x, w.y, ks[u]), q[c][0], s[u]);
                 s[u] = mfma32(widen_codes(w.z, w.w, ks[u]), q[c][1], s[u]);
             }
-        const bool clean = j >= first_r && j + WIDE_STEP - 1 <= last_r;
-        const bool edge = __ballot(!clean) != 0 || !held;
-        bool fix = false;
-        if (edge) {
-            uint32_t nan = 0;
+        // the base-2 scores are s c2
+        float c2 = A.scale2;
+        const bool clean = j >= first_r && j + WIDE_STEP - 1 <= last_r && held;
+        if (__ballot(!clean) != 0) {
+            c2 = 1.0f;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int key = j + 32 * u + 8 * (i / 4) + 4 * h + (i & 3);
-                    const bool in = key >= first_r && key <= last_r;
-                    s[u][i] = in && sh.page[at[2 * u + i / 8]] >= 0 ? s[u][i] * A.scale2
-                                                                     : -__builtin_inff();
+                    const bool in = key >= first_r && key <= last_r && sh.page[at[2 * u + i / 8]] >= 0;
+                    s[u][i] = in ? s[u][i] * A.scale2 : -__builtin_inff();
                 }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (sh.v_scale[at[t]] == 255u && sh.page[at[t]] >= 0) nan = 0x80808080u;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint2 w = sh.v[buf][((t * NT + n) * 2 + h) * 32 + r];
-                    nan |= (w.x & 0x7F7F7F7Fu) + 0x01010101u;
-                    nan |= (w.y & 0x7F7F7F7Fu) + 0x01010101u;
-                }
-            }
-            fix = __ballot((nan & 0x80808080u) != 0) != 0;
         }
-        // scores in base 2 are s times this
-        const float c2 = edge ? 1.0f : A.scale2;
-        float top = -__builtin_inff();
+        float top = s[0][0];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[u][i] * c2);
+            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[u][i]);
+        top *= c2;
         if (__ballot(top > m + kRaiseAbove) != 0) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 32, WAVE));
             const float next = __builtin_fmaxf(m, top - kRaiseTo);
@@ -860,35 +878,46 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
                 l += p[i];
             }
             const f16x8_t pb = split_parts<f16x8_t, 1>(p).p[0];
-            const uint32_t vb = __builtin_amdgcn_readfirstlane(sh.v_scale[at[t]]);
-            const float vs = v_operand(vb, v_top);
+            const float vs = v_operand(__builtin_amdgcn_readfirstlane(sh.v_scale[at[t]]), v_top);
             const uint2 *from = &sh.v[buf][(t * NT * 2 + h) * 32 + r];
-            if (!fix) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    o[n] = mfma32(widen_values(from[n * 64], vs), pb, o[n]);
-            } else {
-                // the sums without NaN values, then NaN where a row sees one
-                float see[8];
+            for (int n = 0; n < NT; ++n)
+                o[n] = mfma32(widen_values(from[n * 64], vs), pb, o[n]);
+        }
+    };
+
+    // A step whose NaN values were taken out: NaN where a row sees one.  A
+    // product of where they are with who sees them counts them.
+    auto mark_nan = [&](int j, int seg) {
+#pragma unroll 1
+        for (int t = 0; t < 4; ++t) {
+            const int p = ((j + 16 * t + skew) >> C.block_shift) - ((seg + skew) >> C.block_shift);
+            if (j + 16 * t >= keys || sh.page[p] < 0) break;
+            const bool every = sh.v_nan[p] != 0;
+            const uint8_t *codes = C.v_codes + page_offset(C, sh.page[p], head) +
+                                   ((j + 16 * t + skew) & (C.block - 1)) * D;
+            float seen[8];
+            bool in[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    see[i] = s[t / 2][8 * (t & 1) + i] == -__builtin_inff() ? 0.0f : 1.0f;
-                const f16x8_t sb = split_parts<f16x8_t, 1>(see).p[0];
-                const bool all = vb == 255u;
-                const uint32_t empty = all ? 0x01010101u : 0u;
+            for (int i = 0; i < 8; ++i) {
+                const int key = j + 16 * t + 8 * (i / 4) + 4 * h + (i & 3);
+                in[i] = key < keys;
+                seen[i] = key >= first_r && key <= last_r ? 1.0f : 0.0f;
+            }
+            const f16x8_t sb = split_parts<f16x8_t, 1>(seen).p[0];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint2 w = from[n * 64];
-                    const uint32_t za = ((((w.x & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | empty;
-                    const uint32_t zb = ((((w.y & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | empty;
-                    o[n] = mfma32(widen_values(make_uint2(w.x & ~(za * 0xFFu), w.y & ~(zb * 0xFFu)),
-                                               all ? 1.0f : vs), pb, o[n]);
-                    const f32x16_t count = mfma32(
-                        widen_values(make_uint2(za * 0x38u, zb * 0x38u), 1.0f), sb, f32x16_t{});
+            for (int n = 0; n < NT; ++n) {
+                const int d = n < 4 * W4 ? 128 * (n / 4) + 4 * r + (n & 3) : 128 * W4 + 2 * r + (n & 1);
+                f16x8_t a;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (count[i] > 0.0f) o[n][i] = __builtin_nanf("");
+                for (int i = 0; i < 8; ++i) {
+                    const int c = codes[(8 * (i / 4) + 4 * h + (i & 3)) * D + d];
+                    a[i] = in[i] && (every || (c & 127) == 127) ? 1.0f : 0.0f;
                 }
+                const f32x16_t count = mfma32(a, sb, f32x16_t{});
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (count[i] > 0.0f) o[n][i] = __builtin_nanf("");
             }
         }
     };
@@ -898,7 +927,10 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
         const int64_t b0 = (k0 + seg) >> C.block_shift;
         const int pages = (int)(((k0 + seg_end - 1) >> C.block_shift) - b0) + 1;
         __syncthreads();  // the last segment's pages are done with
-        if (threadIdx.x == 0) sh.v_top = v_top;
+        if (threadIdx.x == 0) {
+            sh.v_top = v_top;
+            sh.seg_nan = sh.nan[0] = sh.nan[1] = 0;
+        }
         __syncthreads();
         bool missing = false;
         if (threadIdx.x < pages) {
@@ -907,8 +939,10 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             const uint32_t kb = page < 0 ? 0u : C.k_scales[at], vb = page < 0 ? 0u : C.v_scales[at];
             sh.page[threadIdx.x] = page;
             sh.k_scale[threadIdx.x] = (uint8_t)kb;
-            sh.v_scale[threadIdx.x] = (uint8_t)vb;
+            sh.v_scale[threadIdx.x] = vb == 255u ? 0 : (uint8_t)vb;
+            sh.v_nan[threadIdx.x] = vb == 255u;
             missing = page < 0;
+            if (vb == 255u) sh.seg_nan = 1;
             if (vb != 255u && vb > v_top) atomicMax(&sh.v_top, vb);
         }
         if (missing) flag(status, FLAG_CACHE_INDEX);
@@ -920,6 +954,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             for (int n = 0; n < NT; ++n) o[n] *= down;
             v_top = v_next;
         }
+        seg_nan = __builtin_amdgcn_readfirstlane(sh.seg_nan) != 0;
         load(seg, seg);
         store(0);
         __syncthreads();
@@ -927,9 +962,13 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
         for (int j = seg; j < seg_end; j += WIDE_STEP) {
             const bool more = j + WIDE_STEP < seg_end;
             if (more) load(j + WIDE_STEP, seg);
-            if (j <= wave_last && j + WIDE_STEP > wave_first) compute(buf, j, seg);
+            if (j <= wave_last && j + WIDE_STEP > wave_first) {
+                compute(buf, j, seg);
+                if (sh.nan[buf]) mark_nan(j, seg);
+            }
             if (more) store(buf ^ 1);
             __syncthreads();
+            if (threadIdx.x == 0) sh.nan[buf] = 0;  // before the barrier ahead of its next store
             buf ^= 1;
         }
     }
@@ -1064,7 +1103,8 @@ hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, i
     A.heads = heads, A.group = heads / C.heads, A.causal = causal, A.window = window;
     A.sub = P.sub, A.sub_heads = P.sub_heads, A.items = (int)P.items, A.tokens = P.tokens;
     A.splits = P.splits, A.split_keys = P.split_keys;
-    A.scale2 = scale * kLog2e;
+    A.scale2 = (scale < 0.0f ? -scale : scale) * kLog2e;
+    A.q_sign = scale < 0.0f ? (bf16 ? 0x80008000u : 0x80000000u) : 0u;
     switch (C.dim) {
         case 64: launch_dim<64>(C, B, A, P, bf16, status, s); break;
         case 128: launch_dim<128>(C, B, A, P, bf16, status, s); break;
