@@ -55,8 +55,9 @@ struct AttnArgs {
 
 // A row tile's tokens and the keys any of them sees.
 struct Tile {
-    int64_t pos0;     // position of its first token
-    int64_t base, end;  // keys [base, end), base a multiple of 32
+    int64_t pos0;       // position of its first token
+    int64_t base, end;  // keys [base, end), base a page's first
+    int64_t first;      // the first key any of them sees
     int tokens;
 };
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ Tile tile_range(const KvCache &C, const KvBatch &B, c
                                            const Item &it, int first_row, int32_t *status) {
     Tile T;
     T.tokens = min(A.tokens, it.count - first_row);
-    const int64_t len = B.lengths[it.seq];
+    const int64_t len = __builtin_amdgcn_readfirstlane(B.lengths[it.seq]);
     T.pos0 = len - it.count + first_row;
     int64_t end = A.causal ? T.pos0 + T.tokens : len;
     const int64_t held = (int64_t)B.width << C.block_shift;
@@ -73,7 +74,8 @@ __device__ __forceinline__ Tile tile_range(const KvCache &C, const KvBatch &B, c
         end = held;
     }
     const int64_t first = A.window > 0 ? max(T.pos0 - A.window + 1, (int64_t)0) : 0;
-    T.base = first & ~(int64_t)31;
+    T.first = first;
+    T.base = first & ~(int64_t)(C.block - 1);
     T.end = max(end, T.base);
     return T;
 }
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     Tile T;
     if (none) {
         T.tokens = min(A.tokens, it.count - row0);
-        T.pos0 = T.base = T.end = 0;
+        T.pos0 = T.base = T.first = T.end = 0;
     } else {
         T = tile_range(C, B, A, it, row0, status);
     }
@@ -289,18 +291,17 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     __syncthreads();
     v_top = __builtin_amdgcn_readfirstlane(sh.v_top);
 
-    const int skew = (int)(k0 & (C.block - 1));
     const uint32_t k_lane = (uint32_t)(r * D + 16 * g);
     const uint32_t v_lane = (uint32_t)(4 * g * D + r * (D / 16));
     auto page_at = [&](int j) {  // of the keys from j on, relative to k0; clamped to the last
-        return __builtin_amdgcn_readfirstlane(min((j + skew) >> C.block_shift, pages - 1));
+        return __builtin_amdgcn_readfirstlane(min(j >> C.block_shift, pages - 1));
     };
     auto load = [&](int j, Step<D> &s, bool keys_too, bool values_too) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int jj = j + 16 * half;
             const int page = max(__builtin_amdgcn_readfirstlane(sh.page[page_at(jj)]), 0);
-            const int64_t at = page_offset(C, page, head) + ((jj + skew) & (C.block - 1)) * D;
+            const int64_t at = page_offset(C, page, head) + (jj & (C.block - 1)) * D;
             const uint8_t *kp = C.k_codes + at, *vp = C.v_codes + at;
             if (keys_too)
 #pragma unroll
@@ -460,7 +461,8 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     };
 
     Step<D> now, next;
-    int j = 32 * wave;
+    // a window may start inside its first page
+    int j = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / NARROW_STEP * NARROW_STEP + 32 * wave;
     if (j < keys) load(j, now, true, V_AHEAD);
     while (j < keys) {
         const int after = j + NARROW_STEP;
@@ -603,30 +605,23 @@ __device__ __forceinline__ f32x16_t mfma32(f16x8_t a, f16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ f16x8_t widen_values(uint2 w, float scale) {
-    const f16x2_t r[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, scale, false),
-                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, scale, true),
-                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, scale, false),
-                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, scale, true)};
-    f16x8_t v;
-    __builtin_memcpy(&v, r, sizeof(v));
-    return v;
-}
-
 constexpr int WIDE_WG = 256;
 constexpr int WIDE_ROWS = 128;
 constexpr int WIDE_STEP = 64;       // keys of a step
 constexpr int WIDE_SEGMENT = 2048;  // keys whose pages are held in LDS
+// a segment's pages, and those a step that ends past it may ask for
+constexpr int WIDE_PAGES = (WIDE_SEGMENT + WIDE_STEP) / 16;
+constexpr uint32_t PAGE_MISSING = 1, PAGE_NAN = 2;
 
 template <int D>
 struct WideShared {
-    u32x4_t k[2][WIDE_STEP * D / 16];  // [key][16-byte chunk ^ swizzle]
-    uint2 v[2][WIDE_STEP * D / 8];   // [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
-    int page[WIDE_SEGMENT / 16 + 1];
-    uint8_t k_scale[WIDE_SEGMENT / 16 + 1], v_scale[WIDE_SEGMENT / 16 + 1];
-    uint8_t v_nan[WIDE_SEGMENT / 16 + 1];  // pages whose value scale is NaN
-    uint32_t v_top, seg_nan;
-    uint32_t nan[2];  // whether values of the step were NaN and taken out
+    u32x4_t k[2][WIDE_STEP * D / 16];  // codes: [key][16-byte chunk ^ swizzle]
+    u32x4_t v[2][WIDE_STEP * D / 8];   // fp16: [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
+    int64_t offset[WIDE_PAGES];        // a page's codes
+    float k_operand[WIDE_PAGES], v_operand[WIDE_PAGES];
+    uint8_t bad[WIDE_PAGES];           // PAGE_*
+    uint32_t v_top, special;           // special: some page of the segment is bad
+    uint32_t nan[2];                   // whether values of a step were NaN and taken out
 };
 
 // The chunk of a key row that LDS chunk c of the row holds: rows of D bytes
@@ -640,11 +635,10 @@ __device__ __forceinline__ int key_swizzle(int row) {
 //
 // As above, but the four waves share the keys and have 32 rows each: scores
 // S^T = K Q^T and sums out^T = V^T P^T on 32 x 32 tiles, probabilities staying
-// in their lanes.  A step of 64 keys is loaded a step ahead and put into LDS as
-// codes, half of what bf16 tiles would take (four waves reading 32 KB a step
-// would keep LDS as busy as the MFMA); each wave widens what it multiplies.
-// Values are transposed on their way into LDS, eight keys of a dimension side by
-// side, once for the four waves.
+// in their lanes.  A step of 64 keys is loaded a step ahead.  Keys go into LDS
+// as codes, and each wave widens what it multiplies; values are transposed
+// (eight keys of a dimension side by side) and widened to fp16 once, on their way
+// into LDS.
 template <int D>
 __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, KvBatch B,
                                                                     AttnArgs A, int32_t *status) {
@@ -672,7 +666,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     Tile T;
     if (it.seq >= B.seqs) {
         T.tokens = min(A.tokens, it.count - row0);
-        T.pos0 = T.base = T.end = 0;
+        T.pos0 = T.base = T.first = T.end = 0;
     } else {
         T = tile_range(C, B, A, it, row0, status);
     }
@@ -688,6 +682,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     const bool whole = T.end - T.base <= A.split_keys;
     if (k0 >= k1 && split > 0) return;
 
+    // from here on keys count from k0, a page's first
     const int64_t pos = T.pos0 + ri;
     const int64_t last = row_real && A.causal ? pos : T.end - 1;
     const int64_t first = row_real && A.window > 0 ? pos - A.window + 1 : 0;
@@ -696,11 +691,11 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     const int first_r = (int)max(min(first - k0, (int64_t)keys), (int64_t)0);
     // the keys any row of this wave sees
     const int wave_last = (int)wave_max_u32(row_real ? (uint32_t)(last_r + 1) : 0u) - 1;
+    const int wave_first = (int)wave_min_u32(row_real ? (uint32_t)first_r : 0x7FFFFFFFu);
     // the keys every row of the tile sees
     const int tile_last = (int)min((A.causal ? T.pos0 : T.end - 1) - k0, (int64_t)keys - 1);
     const int tile_first =
         A.window > 0 ? (int)max(min(T.pos0 + T.tokens - A.window - k0, (int64_t)keys), (int64_t)0) : 0;
-    const int wave_first = (int)wave_min_u32(row_real ? (uint32_t)first_r : 0x7FFFFFFFu);
 
     bf16x8_t q[KC / 2][2];
     {
@@ -719,63 +714,52 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     // the next step's codes, in registers
     u32x4_t kr[KL];
     uint32_t vr[W4 + W2][8], any_nan = 0;
-    bool seg_nan = false;
-    const int vt = threadIdx.x >> 6, vh = h, vm = r;  // this thread's values: keys of 16 vt, half vh
-    const int skew = (int)(k0 & (C.block - 1));
-    auto load = [&](int j, int seg) {  // keys j .. of the split, in the segment from seg on
-        const int lim = ((min(seg + WIDE_SEGMENT, keys) - 1 + skew) >> C.block_shift) -
-                        ((seg + skew) >> C.block_shift);
-        auto place_at = [&](int key) {  // its page among the segment's
-            return min(((key + skew) >> C.block_shift) - ((seg + skew) >> C.block_shift), lim);
-        };
-        auto place = [&](int key, int64_t &at) {  // a 16-key group's codes; whether it has any
-            const int page = sh.page[place_at(key)];
-            at = page_offset(C, max(page, 0), head) + ((key + skew) & (C.block - 1)) * D;
-            return page >= 0;
-        };
+    float v_scale = 0.0f;
+    const int vt = threadIdx.x >> 6;  // this thread's values: keys of group vt, half h, lane r
+    const int slots = C.block - 1;
+    bool special = false;
+    auto load = [&](int j, int seg) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
             const int c = threadIdx.x + i * WIDE_WG;
             const int key = c / KC;
-            int64_t at;
-            place(j + (key & ~15), at);
-            kr[i] = *(const u32x4_t *)(C.k_codes + at + (key & 15) * D + 16 * (c - key * KC));
+            const uint8_t *p = C.k_codes + sh.offset[(j - seg + key) >> C.block_shift] +
+                               (uint32_t)(((j + key) & slots) * D + 16 * (c - key * KC));
+            kr[i] = *(const u32x4_t *)p;
         }
-        int64_t at;
-        const bool held = place(j + 16 * vt, at);
-        const uint8_t *vp = C.v_codes + at + 4 * vh * D;
+        const int page = (j - seg + 16 * vt) >> C.block_shift;
+        const uint8_t *vp = C.v_codes + sh.offset[page] +
+                            (uint32_t)((((j + 16 * vt) & slots) + 4 * h) * D);
+        v_scale = sh.v_operand[page];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int row_at = (8 * (i / 4) + (i & 3)) * D;  // keys 4 h + 0..3, 8 + 4 h + 0..3
+            const int at = (8 * (i / 4) + (i & 3)) * D;  // keys 4 h + 0..3, 8 + 4 h + 0..3
 #pragma unroll
-            for (int w = 0; w < W4; ++w)
-                vr[w][i] = *(const uint32_t *)(vp + row_at + 128 * w + 4 * vm);
-            if (W2) vr[W4][i] = *(const uint16_t *)(vp + row_at + 128 * W4 + 2 * vm);
+            for (int w = 0; w < W4; ++w) vr[w][i] = ((const uint32_t *)(vp + at + 128 * w))[r];
+            if (W2) vr[W4][i] = ((const uint16_t *)(vp + at + 128 * W4))[r];
         }
-        // values nothing sees are zeros, whatever the page holds there
-        if (!held || j + WIDE_STEP > keys) {
+        any_nan = 0;
+        if (special || j < tile_first || j + WIDE_STEP - 1 > tile_last) {
+            // Values nothing sees are zeros, whatever the page holds there.  NaN
+            // values of a step that not every row sees whole would reach rows
+            // that do not see them (0 times NaN): they are taken out here and
+            // marked afterwards.  Where every row sees them the sums do it by
+            // themselves.
+            const uint32_t bad = sh.bad[page];
+            const uint32_t every = bad & PAGE_NAN ? 0x01010101u : 0u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int key = j + 16 * vt + 4 * vh + 8 * (i / 4) + (i & 3);
-#pragma unroll
-                for (int w = 0; w < W4 + W2; ++w)
-                    if (!held || key >= keys) vr[w][i] = 0;
-            }
-        }
-        // NaN values of a step that not every row sees whole would reach rows
-        // that do not see them (0 times NaN): they are taken out here and marked
-        // afterwards.  Where every row sees them the sums do it by themselves.
-        any_nan = 0;
-        if (seg_nan || j < tile_first || j + WIDE_STEP - 1 > tile_last) {
-            const uint32_t every = held && sh.v_nan[place_at(j + 16 * vt)] ? 0x01010101u : 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
+                const int key = j + 16 * vt + 4 * h + 8 * (i / 4) + (i & 3);
+                const bool none = key >= keys || (bad & PAGE_MISSING);
 #pragma unroll
                 for (int w = 0; w < W4 + W2; ++w) {
-                    const uint32_t z = ((((vr[w][i] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | every;
-                    vr[w][i] &= ~(z * 0xFFu);
+                    const uint32_t x = vr[w][i];
+                    uint32_t z = ((((x & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | every;
+                    if (none) z = 0;
+                    vr[w][i] = none ? 0u : x & ~(z * 0xFFu);
                     any_nan |= z;
                 }
+            }
         }
     };
     auto store = [&](int buf) {
@@ -788,21 +772,22 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
         if (any_nan) sh.nan[buf] = 1;
 #pragma unroll
         for (int w = 0; w < W4 + W2; ++w) {
-            // bytes of two keys side by side, then of four
-            uint32_t lo[4], hi[4];
+            u32x4_t *to = &sh.v[buf][((vt * NT + 4 * w) * 2 + h) * 32 + r];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                lo[k] = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], 0x05010400u);
-                hi[k] = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], 0x07030602u);
-            }
-            uint2 *to = &sh.v[buf][((vt * NT + 4 * w) * 2 + vh) * 32 + vm];
+            for (int n = 0; n < (w < W4 ? 4 : 2); n += 2) {
+                // bytes of dimensions n and n + 1, two keys to a half word
+                const uint32_t sel = n ? 0x07030602u : 0x05010400u;
+                u32x4_t a, b;
 #pragma unroll
-            for (int n = 0; n < (w < W4 ? 4 : 2); ++n) {
-                const uint32_t sel = (n & 1) ? 0x07060302u : 0x05040100u;
-                const uint32_t a0 = n < 2 ? lo[0] : hi[0], a1 = n < 2 ? lo[1] : hi[1];
-                const uint32_t b0 = n < 2 ? lo[2] : hi[2], b1 = n < 2 ? lo[3] : hi[3];
-                to[n * 64] = make_uint2(__builtin_amdgcn_perm(a1, a0, sel),
-                                        __builtin_amdgcn_perm(b1, b0, sel));
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t x = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], sel);
+                    a[k] = __builtin_bit_cast(
+                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, v_scale, false));
+                    b[k] = __builtin_bit_cast(
+                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, v_scale, true));
+                }
+                to[n * 64] = a;
+                to[n * 64 + 64] = b;
             }
         }
     };
@@ -814,22 +799,12 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     uint32_t v_top = 0;
 
     auto compute = [&](int buf, int j, int seg) {
-        // pages of the step's four 16-key groups
-        const int p0 = (seg + skew) >> C.block_shift;
-        const int lim = ((min(seg + WIDE_SEGMENT, keys) - 1 + skew) >> C.block_shift) - p0;
-        int at[4];
-        bool held = true;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            at[t] = min(((j + 16 * t + skew) >> C.block_shift) - p0, lim);
-            held = held && sh.page[at[t]] >= 0;
-        }
         f32x16_t s[2];
         float ks[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             s[u] = f32x16_t{};
-            ks[u] = e8m0_operand(sh.k_scale[(r & 16) ? at[2 * u + 1] : at[2 * u]]);
+            ks[u] = sh.k_operand[(j - seg + 32 * u + (r & 16)) >> C.block_shift];
         }
 #pragma unroll
         for (int c = 0; c < KC / 2; ++c)
@@ -841,15 +816,20 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             }
         // the base-2 scores are s c2
         float c2 = A.scale2;
-        const bool clean = j >= first_r && j + WIDE_STEP - 1 <= last_r && held;
+        const bool clean = j >= first_r && j + WIDE_STEP - 1 <= last_r && !special;
         if (__ballot(!clean) != 0) {
             c2 = 1.0f;
+            uint32_t missing = 0;  // a bit for each 16-key group
+            if (special)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    missing |= (uint32_t)(sh.bad[(j - seg + 16 * t) >> C.block_shift] & PAGE_MISSING) << t;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int key = j + 32 * u + 8 * (i / 4) + 4 * h + (i & 3);
-                    const bool in = key >= first_r && key <= last_r && sh.page[at[2 * u + i / 8]] >= 0;
+                    const bool in = key >= first_r && key <= last_r && !((missing >> (2 * u + i / 8)) & 1u);
                     s[u][i] = in ? s[u][i] * A.scale2 : -__builtin_inff();
                 }
         }
@@ -877,12 +857,12 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
                 p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -ref));
                 l += p[i];
             }
+            asm("" : "+v"(l));  // summed here: later, 32 probabilities would be held for it
             const f16x8_t pb = split_parts<f16x8_t, 1>(p).p[0];
-            const float vs = v_operand(__builtin_amdgcn_readfirstlane(sh.v_scale[at[t]]), v_top);
-            const uint2 *from = &sh.v[buf][(t * NT * 2 + h) * 32 + r];
+            const u32x4_t *from = &sh.v[buf][(t * NT * 2 + h) * 32 + r];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                o[n] = mfma32(widen_values(from[n * 64], vs), pb, o[n]);
+                o[n] = mfma32(__builtin_bit_cast(f16x8_t, from[n * 64]), pb, o[n]);
         }
     };
 
@@ -891,17 +871,14 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     auto mark_nan = [&](int j, int seg) {
 #pragma unroll 1
         for (int t = 0; t < 4; ++t) {
-            const int p = ((j + 16 * t + skew) >> C.block_shift) - ((seg + skew) >> C.block_shift);
-            if (j + 16 * t >= keys || sh.page[p] < 0) break;
-            const bool every = sh.v_nan[p] != 0;
-            const uint8_t *codes = C.v_codes + page_offset(C, sh.page[p], head) +
-                                   ((j + 16 * t + skew) & (C.block - 1)) * D;
+            const int page = (j - seg + 16 * t) >> C.block_shift;
+            if (j + 16 * t >= keys || (sh.bad[page] & PAGE_MISSING)) continue;
+            const bool every = sh.bad[page] & PAGE_NAN;
+            const uint8_t *codes = C.v_codes + sh.offset[page] + ((j + 16 * t) & slots) * D;
             float seen[8];
-            bool in[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int key = j + 16 * t + 8 * (i / 4) + 4 * h + (i & 3);
-                in[i] = key < keys;
                 seen[i] = key >= first_r && key <= last_r ? 1.0f : 0.0f;
             }
             const f16x8_t sb = split_parts<f16x8_t, 1>(seen).p[0];
@@ -912,54 +889,60 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c = codes[(8 * (i / 4) + 4 * h + (i & 3)) * D + d];
-                    a[i] = in[i] && (every || (c & 127) == 127) ? 1.0f : 0.0f;
+                    a[i] = every || (c & 127) == 127 ? 1.0f : 0.0f;
                 }
                 const f32x16_t count = mfma32(a, sb, f32x16_t{});
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (count[i] > 0.0f) o[n][i] = __builtin_nanf("");
+                for (int i = 0; i < 16; ++i)  // a count is 0 or positive: its negated bits' sign
+                    o[n][i] = u2f(f2u(o[n][i]) | ((uint32_t)((int)-f2u(count[i]) >> 31) & 0x7FC00000u));
             }
         }
     };
 
-    for (int seg = 0; seg < keys; seg += WIDE_SEGMENT) {
+    // a window may start inside its first page
+    const int start = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / WIDE_STEP * WIDE_STEP;
+    for (int seg = start / WIDE_SEGMENT * WIDE_SEGMENT; seg < keys; seg += WIDE_SEGMENT) {
         const int seg_end = min(seg + WIDE_SEGMENT, keys);
         const int64_t b0 = (k0 + seg) >> C.block_shift;
-        const int pages = (int)(((k0 + seg_end - 1) >> C.block_shift) - b0) + 1;
+        const int pages = (seg_end - seg + slots) >> C.block_shift;
         __syncthreads();  // the last segment's pages are done with
         if (threadIdx.x == 0) {
             sh.v_top = v_top;
-            sh.seg_nan = sh.nan[0] = sh.nan[1] = 0;
+            sh.special = sh.nan[0] = sh.nan[1] = 0;
         }
         __syncthreads();
-        bool missing = false;
-        if (threadIdx.x < pages) {
-            const int page = find_page(B, C, it.seq, b0 + threadIdx.x);
-            const int64_t at = (int64_t)max(page, 0) * C.heads + head;
-            const uint32_t kb = page < 0 ? 0u : C.k_scales[at], vb = page < 0 ? 0u : C.v_scales[at];
-            sh.page[threadIdx.x] = page;
-            sh.k_scale[threadIdx.x] = (uint8_t)kb;
-            sh.v_scale[threadIdx.x] = vb == 255u ? 0 : (uint8_t)vb;
-            sh.v_nan[threadIdx.x] = vb == 255u;
-            missing = page < 0;
-            if (vb == 255u) sh.seg_nan = 1;
-            if (vb != 255u && vb > v_top) atomicMax(&sh.v_top, vb);
+        uint32_t kb = 0, vb = 0;
+        if (threadIdx.x < WIDE_PAGES) {  // past the segment's pages, the last again
+            const int page = find_page(B, C, it.seq, b0 + min((int)threadIdx.x, pages - 1));
+            uint32_t bad = page < 0 ? PAGE_MISSING : 0u;
+            if (page >= 0) {
+                const int64_t at = (int64_t)page * C.heads + head;
+                kb = C.k_scales[at], vb = C.v_scales[at];
+                if (vb == 255u) bad = PAGE_NAN, vb = 0;
+            }
+            sh.offset[threadIdx.x] = page_offset(C, max(page, 0), head);
+            sh.k_operand[threadIdx.x] = e8m0_operand(kb);
+            sh.bad[threadIdx.x] = (uint8_t)bad;
+            if (bad) sh.special = 1;
+            if (bad & PAGE_MISSING) flag(status, FLAG_CACHE_INDEX);
+            if (vb > v_top) atomicMax(&sh.v_top, vb);
         }
-        if (missing) flag(status, FLAG_CACHE_INDEX);
         __syncthreads();
         const uint32_t v_next = __builtin_amdgcn_readfirstlane(sh.v_top);
+        special = __builtin_amdgcn_readfirstlane(sh.special) != 0;
         if (v_next > v_top) {
             const float down = e8m0_value(E8M0_ONE - min(v_next - v_top, E8M0_ONE));
 #pragma unroll
             for (int n = 0; n < NT; ++n) o[n] *= down;
             v_top = v_next;
         }
-        seg_nan = __builtin_amdgcn_readfirstlane(sh.seg_nan) != 0;
-        load(seg, seg);
+        if (threadIdx.x < WIDE_PAGES) sh.v_operand[threadIdx.x] = v_operand(vb, v_top);
+        __syncthreads();
+        int buf = 0, j = max(seg, start);
+        load(j, seg);
         store(0);
         __syncthreads();
-        int buf = 0;
-        for (int j = seg; j < seg_end; j += WIDE_STEP) {
+        for (; j < seg_end; j += WIDE_STEP) {
             const bool more = j + WIDE_STEP < seg_end;
             if (more) load(j + WIDE_STEP, seg);
             if (j <= wave_last && j + WIDE_STEP > wave_first) {
@@ -978,33 +961,28 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int back = (int)v_top - (int)E8M0_ONE - kVBias;
     const int64_t to = token * A.heads + hq;
-    auto put = [&](int d, const float *y, int n) {  // n (2 or 4) values from dimension d on
-        if (!whole) {
-            float *p = A.part_o + (to * A.splits + split) * D + d;
-            for (int i = 0; i < n; ++i) p[i] = y[i];
-        } else {
-            __bf16 *p = (__bf16 *)A.out + to * D + d;
-            typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-            if (n == 4)
-                *(bf16x4_t *)p = bf16x4_t{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
-            else
-                *(bf16x2_t *)p = bf16x2_t{(__bf16)y[0], (__bf16)y[1]};
-        }
-    };
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int mm = 8 * (i / 4) + 4 * h + (i & 3);
+    for (int w = 0; w < W4 + W2; ++w)
 #pragma unroll
-        for (int w = 0; w < W4 + W2; ++w) {
-            constexpr int N4 = 4;
-            const int n = w < W4 ? N4 : 2;
-            float y[4];
+        for (int i = 0; i < 16; ++i) {
+            // 4 (of a half word 2) dimensions side by side
+            const int mm = 8 * (i / 4) + 4 * h + (i & 3);
+            const int d = 128 * w + (w < W4 ? 4 : 2) * mm;
+            f32x4_t y = {0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < (w < W4 ? 4 : 2); ++k)
                 y[k] = __builtin_ldexpf(o[4 * w + k][i] * inv, back);
-            put(128 * w + n * mm, y, n);
+            const f32x2_t lo = {y.x, y.y}, hi = {y.z, y.w};
+            if (!whole) {
+                float *p = A.part_o + (to * A.splits + split) * D + d;
+                *(f32x2_t *)p = lo;
+                if (w < W4) *(f32x2_t *)(p + 2) = hi;
+            } else {
+                uint32_t *p = (uint32_t *)((uint16_t *)A.out + to * D + d);
+                p[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t));
+                if (w < W4) p[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t));
+            }
         }
-    }
     if (h == 0) {
         if (!whole)
             A.part_ml[to * A.splits + split] = make_float2(m, l);
@@ -1033,7 +1011,7 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     P.tokens = (int)std::min<int64_t>(rows / P.sub_heads, per);
     P.items = P.tokens > 1 ? item_count(B.tokens, B.seqs, P.tokens, 1) : B.tokens;
     int64_t extent = (int64_t)B.width << C.block_shift;
-    if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + P.tokens + 31);
+    if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + P.tokens + C.block);
     const int64_t tiles = std::max<int64_t>(1, B.tokens / P.tokens) * C.heads * P.sub;
     if (P.wide) {
         const int64_t want = std::max<int64_t>(1, 512 / tiles);
@@ -1045,8 +1023,8 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     }
     const int64_t want = std::max<int64_t>(1, 2048 / tiles);
     int64_t keys = (extent + want - 1) / want;
-    keys = (keys + NARROW_STEP - 1) / NARROW_STEP * NARROW_STEP;
-    keys = std::min<int64_t>(std::max<int64_t>(keys, 2 * NARROW_STEP), NARROW_MAX_KEYS);
+    keys = (keys + 2 * NARROW_STEP - 1) / (2 * NARROW_STEP) * (2 * NARROW_STEP);  // whole pages
+    keys = std::min<int64_t>(keys, NARROW_MAX_KEYS);
     P.split_keys = (int)keys;
     P.splits = (int)((extent + keys - 1) / keys);
     return P;

@@ -57,9 +57,9 @@ __device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit, 
     lo = __builtin_amdgcn_readfirstlane(lo);
     Item it;
     it.seq = lo;
-    it.base = B.cu[lo];
+    it.base = __builtin_amdgcn_readfirstlane(B.cu[lo]);
     it.piece = item - (it.base / unit + extra * lo);
-    it.count = (lo < B.seqs ? B.cu[lo + 1] : B.tokens) - it.base;
+    it.count = (lo < B.seqs ? __builtin_amdgcn_readfirstlane(B.cu[lo + 1]) : B.tokens) - it.base;
     // a cu that is no prefix sum of at most `tokens` rows gives no piece
     if (it.base < 0 || it.count < 0 || it.base > B.tokens || it.count > B.tokens - it.base ||
         it.piece < 0)
