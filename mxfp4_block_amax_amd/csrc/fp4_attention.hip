@@ -594,7 +594,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(KvCache C, KvBatch 
                                   __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// ---- row tiles of 128 ------------------------------------------------------
+// ---- row tiles of 128 and 256 ------------------------------------------------------
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
@@ -605,48 +605,47 @@ __device__ __forceinline__ f32x16_t mfma32(f16x8_t a, f16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-constexpr int WIDE_WG = 256;
-constexpr int WIDE_ROWS = 128;
-constexpr int WIDE_STEP = 64;       // keys of a step
 constexpr int WIDE_SEGMENT = 2048;  // keys whose pages are held in LDS
 // a segment's pages, and those a step that ends past it may ask for
-constexpr int WIDE_PAGES = (WIDE_SEGMENT + WIDE_STEP) / 16;
+constexpr int WIDE_PAGES = (WIDE_SEGMENT + 128) / 16;
 constexpr uint32_t PAGE_MISSING = 1, PAGE_NAN = 2;
 
-template <int D>
+template <int D, int STEP>
 struct WideShared {
-    u32x4_t k[2][WIDE_STEP * D / 16];  // codes: [key][16-byte chunk ^ swizzle]
-    u32x4_t v[2][WIDE_STEP * D / 8];   // fp16: [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
+    u32x4_t k[2][STEP * D / 8];  // bf16: [key][8 dimensions ^ swizzle]
+    u32x4_t v[2][STEP * D / 8];  // fp16: [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
     int64_t offset[WIDE_PAGES];        // a page's codes
     float k_operand[WIDE_PAGES], v_operand[WIDE_PAGES];
     uint8_t bad[WIDE_PAGES];           // PAGE_*
     uint32_t v_top, special;           // special: some page of the segment is bad
-    uint32_t nan[2];                   // whether values of a step were NaN and taken out
+    int nan[2];                        // the last step (its end) with NaN values taken out
 };
 
 // The chunk of a key row that LDS chunk c of the row holds: rows of D bytes
 // that start in the same banks spread their chunks over all of them.
 template <int D>
 __device__ __forceinline__ int key_swizzle(int row) {
-    return D % 128 == 0 ? row & 7 : (row >> 1) & 3;
+    return D % 128 == 0 ? row & 15 : (row >> 1) & 7;
 }
 
-// Row tiles of up to 128 query rows: chunks and whole prompts, bf16 queries.
+// Row tiles of up to 32 WAVES query rows: chunks and whole prompts, bf16 queries.
 //
-// As above, but the four waves share the keys and have 32 rows each: scores
+// As above, but the waves share the keys and have 32 rows each: scores
 // S^T = K Q^T and sums out^T = V^T P^T on 32 x 32 tiles, probabilities staying
-// in their lanes.  A step of 64 keys is loaded a step ahead.  Keys go into LDS
-// as codes, and each wave widens what it multiplies; values are transposed
-// (eight keys of a dimension side by side) and widened to fp16 once, on their way
-// into LDS.
-template <int D>
-__global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, KvBatch B,
-                                                                    AttnArgs A, int32_t *status) {
-    constexpr int KC = D / 16;               // 16-byte chunks of a key
+// in their lanes.  A step of 16 WAVES keys is loaded a step ahead as codes and
+// widened once for all waves on its way into LDS, keys to bf16, values
+// transposed (eight keys of a dimension side by side) to fp16.
+template <int D, int WAVES>
+__global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_kernel(
+    KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
+    constexpr int WG = WAVES * WAVE;
+    constexpr int STEP = 16 * WAVES;         // keys of a step
+    constexpr int KC = D / 16;               // 16-byte chunks of a key's codes
     constexpr int NT = D / 32;               // 32-dimension tiles of the output
     constexpr int W4 = D / 128, W2 = D % 128 / 64;  // a lane's words and half words of a value
-    constexpr int KL = WIDE_STEP * KC / WIDE_WG;    // key chunks a thread loads
-    __shared__ WideShared<D> sh;
+    constexpr int KL = STEP * KC / WG;       // key chunks a thread loads
+    static_assert(KL * WG == STEP * KC, "whole loads");
+    __shared__ WideShared<D, STEP> sh;
     const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
     const int r = lane & 31, h = lane >> 5;
     // workgroups in launch order: head, then row tile (the last, with the most
@@ -697,22 +696,21 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     const int tile_first =
         A.window > 0 ? (int)max(min(T.pos0 + T.tokens - A.window - k0, (int64_t)keys), (int64_t)0) : 0;
 
-    bf16x8_t q[KC / 2][2];
+    bf16x8_t q[KC];
     {
-        const uint16_t *p = (const uint16_t *)A.q + token * A.q_token + hq * A.q_head + 16 * h;
+        const uint16_t *p = (const uint16_t *)A.q + token * A.q_token + hq * A.q_head + 8 * h;
 #pragma unroll
-        for (int c = 0; c < KC / 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (row_real) w = *(const uint4 *)(p + 32 * c + 8 * e);
-                w.x ^= A.q_sign, w.y ^= A.q_sign, w.z ^= A.q_sign, w.w ^= A.q_sign;
-                q[c][e] = __builtin_bit_cast(bf16x8_t, w);
-            }
+        for (int c = 0; c < KC; ++c) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row_real) w = *(const uint4 *)(p + 16 * c);
+            w.x ^= A.q_sign, w.y ^= A.q_sign, w.z ^= A.q_sign, w.w ^= A.q_sign;
+            q[c] = __builtin_bit_cast(bf16x8_t, w);
+        }
     }
 
     // the next step's codes, in registers
     u32x4_t kr[KL];
+    float k_scale[KL];
     uint32_t vr[W4 + W2][8], any_nan = 0;
     float v_scale = 0.0f;
     const int vt = threadIdx.x >> 6;  // this thread's values: keys of group vt, half h, lane r
@@ -721,10 +719,12 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     auto load = [&](int j, int seg) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
-            const int c = threadIdx.x + i * WIDE_WG;
+            const int c = threadIdx.x + i * WG;
             const int key = c / KC;
-            const uint8_t *p = C.k_codes + sh.offset[(j - seg + key) >> C.block_shift] +
+            const int page = (j - seg + key) >> C.block_shift;
+            const uint8_t *p = C.k_codes + sh.offset[page] +
                                (uint32_t)(((j + key) & slots) * D + 16 * (c - key * KC));
+            k_scale[i] = sh.k_operand[page];
             kr[i] = *(const u32x4_t *)p;
         }
         const int page = (j - seg + 16 * vt) >> C.block_shift;
@@ -739,7 +739,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             if (W2) vr[W4][i] = ((const uint16_t *)(vp + at + 128 * W4))[r];
         }
         any_nan = 0;
-        if (special || j < tile_first || j + WIDE_STEP - 1 > tile_last) {
+        if (special || j < tile_first || j + STEP - 1 > tile_last) {
             // Values nothing sees are zeros, whatever the page holds there.  NaN
             // values of a step that not every row sees whole would reach rows
             // that do not see them (0 times NaN): they are taken out here and
@@ -762,14 +762,18 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             }
         }
     };
-    auto store = [&](int buf) {
+    auto store = [&](int buf, int j) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
-            const int c = threadIdx.x + i * WIDE_WG;
+            const int c = threadIdx.x + i * WG;
             const int key = c / KC;
-            sh.k[buf][key * KC + ((c - key * KC) ^ key_swizzle<D>(key))] = kr[i];
+            const int at = 2 * (c - key * KC), swz = key_swizzle<D>(key);
+            sh.k[buf][key * 2 * KC + (at ^ swz)] =
+                __builtin_bit_cast(u32x4_t, widen_codes(kr[i].x, kr[i].y, k_scale[i]));
+            sh.k[buf][key * 2 * KC + ((at + 1) ^ swz)] =
+                __builtin_bit_cast(u32x4_t, widen_codes(kr[i].z, kr[i].w, k_scale[i]));
         }
-        if (any_nan) sh.nan[buf] = 1;
+        if (any_nan) sh.nan[buf] = j + STEP;
 #pragma unroll
         for (int w = 0; w < W4 + W2; ++w) {
             u32x4_t *to = &sh.v[buf][((vt * NT + 4 * w) * 2 + h) * 32 + r];
@@ -798,25 +802,23 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     float m = -__builtin_inff(), l = 0.0f;
     uint32_t v_top = 0;
 
-    auto compute = [&](int buf, int j, int seg) {
+    // 64 keys, part `part` of the step at j0
+    auto compute = [&](int buf, int j0, int part, int seg) {
+        const int j = j0 + 64 * part;
         f32x16_t s[2];
-        float ks[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = f32x16_t{};
-            ks[u] = sh.k_operand[(j - seg + 32 * u + (r & 16)) >> C.block_shift];
-        }
+        for (int u = 0; u < 2; ++u) s[u] = f32x16_t{};
+        const u32x4_t *kp = &sh.k[buf][64 * part * 2 * KC];
 #pragma unroll
-        for (int c = 0; c < KC / 2; ++c)
+        for (int c = 0; c < KC; ++c)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const u32x4_t w = sh.k[buf][(32 * u + r) * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
-                s[u] = mfma32(widen_codes(w.x, w.y, ks[u]), q[c][0], s[u]);
-                s[u] = mfma32(widen_codes(w.z, w.w, ks[u]), q[c][1], s[u]);
+                const u32x4_t w = kp[(32 * u + r) * 2 * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
+                s[u] = mfma32(__builtin_bit_cast(bf16x8_t, w), q[c], s[u]);
             }
         // the base-2 scores are s c2
         float c2 = A.scale2;
-        const bool clean = j >= first_r && j + WIDE_STEP - 1 <= last_r && !special;
+        const bool clean = j >= first_r && j + 63 <= last_r && !special;
         if (__ballot(!clean) != 0) {
             c2 = 1.0f;
             uint32_t missing = 0;  // a bit for each 16-key group
@@ -859,7 +861,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
             }
             asm("" : "+v"(l));  // summed here: later, 32 probabilities would be held for it
             const f16x8_t pb = split_parts<f16x8_t, 1>(p).p[0];
-            const u32x4_t *from = &sh.v[buf][(t * NT * 2 + h) * 32 + r];
+            const u32x4_t *from = &sh.v[buf][((4 * part + t) * NT * 2 + h) * 32 + r];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 o[n] = mfma32(__builtin_bit_cast(f16x8_t, from[n * 64]), pb, o[n]);
@@ -870,7 +872,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     // product of where they are with who sees them counts them.
     auto mark_nan = [&](int j, int seg) {
 #pragma unroll 1
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < WAVES; ++t) {
             const int page = (j - seg + 16 * t) >> C.block_shift;
             if (j + 16 * t >= keys || (sh.bad[page] & PAGE_MISSING)) continue;
             const bool every = sh.bad[page] & PAGE_NAN;
@@ -900,7 +902,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
     };
 
     // a window may start inside its first page
-    const int start = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / WIDE_STEP * WIDE_STEP;
+    const int start = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / STEP * STEP;
     for (int seg = start / WIDE_SEGMENT * WIDE_SEGMENT; seg < keys; seg += WIDE_SEGMENT) {
         const int seg_end = min(seg + WIDE_SEGMENT, keys);
         const int64_t b0 = (k0 + seg) >> C.block_shift;
@@ -940,18 +942,18 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
         __syncthreads();
         int buf = 0, j = max(seg, start);
         load(j, seg);
-        store(0);
+        store(0, j);
         __syncthreads();
-        for (; j < seg_end; j += WIDE_STEP) {
-            const bool more = j + WIDE_STEP < seg_end;
-            if (more) load(j + WIDE_STEP, seg);
-            if (j <= wave_last && j + WIDE_STEP > wave_first) {
-                compute(buf, j, seg);
-                if (sh.nan[buf]) mark_nan(j, seg);
-            }
-            if (more) store(buf ^ 1);
+        for (; j < seg_end; j += STEP) {
+            const bool more = j + STEP < seg_end;
+            if (more) load(j + STEP, seg);
+#pragma unroll 1
+            for (int part = 0; part < STEP / 64; ++part)
+                if (j + 64 * part <= wave_last && j + 64 * part + 63 >= wave_first)
+                    compute(buf, j, part, seg);
+            if (sh.nan[buf] == j + STEP) mark_nan(j, seg);
+            if (more) store(buf ^ 1, j + STEP);
             __syncthreads();
-            if (threadIdx.x == 0) sh.nan[buf] = 0;  // before the barrier ahead of its next store
             buf ^= 1;
         }
     }
@@ -995,7 +997,7 @@ __global__ __launch_bounds__(WIDE_WG, 2) void attention_wide_kernel(KvCache C, K
 // How a call is laid out: from its shapes alone, which the workspace's size
 // needs too.
 struct Plan {
-    bool wide;
+    int wide;  // waves of a wide workgroup, 0 for narrow tiles
     int sub, sub_heads, tokens, splits, split_keys;
     int64_t items;
 };
@@ -1004,8 +1006,8 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     Plan P;
     const int group = heads / C.heads;
     const int64_t per = (B.tokens + B.seqs - 1) / B.seqs;  // new tokens of a sequence, on average
-    P.wide = bf16 && per * group > 64 && C.dim <= 128;
-    const int rows = P.wide ? WIDE_ROWS : 16;
+    P.wide = bf16 && per * group > 64 && C.dim <= 128 ? 8 : 0;
+    const int rows = P.wide ? 32 * P.wide : 16;
     P.sub = (group + rows - 1) / rows;
     P.sub_heads = (group + P.sub - 1) / P.sub;
     P.tokens = (int)std::min<int64_t>(rows / P.sub_heads, per);
@@ -1051,9 +1053,9 @@ static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, co
     const dim3 grid((uint32_t)P.items, C.heads * P.sub, P.splits);
     if (P.wide) {
         if constexpr (D <= 128)
-            hipLaunchKernelGGL(attention_wide_kernel<D>,
-                               dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)), dim3(WIDE_WG),
-                               0, s, C, B, A, status);
+            hipLaunchKernelGGL((attention_wide_kernel<D, 8>),
+                               dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)),
+                               dim3(P.wide * WAVE), 0, s, C, B, A, status);
     } else if (bf16) {
         hipLaunchKernelGGL((attention_narrow_kernel<D, false>), grid, dim3(NARROW_WG), 0, s, C, B,
                            A, status);
