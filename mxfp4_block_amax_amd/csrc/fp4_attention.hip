@@ -605,6 +605,9 @@ __device__ __forceinline__ f32x16_t mfma32(f16x8_t a, f16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// kinds of instructions for the scheduler's groups
+constexpr int SCHED_MFMA = 8, SCHED_LDS_READ = 256;
+
 constexpr int WIDE_SEGMENT = 2048;  // keys whose pages are held in LDS
 // a segment's pages, and those a step that ends past it may ask for
 constexpr int WIDE_PAGES = (WIDE_SEGMENT + 128) / 16;
@@ -816,6 +819,15 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
                 const u32x4_t w = kp[(32 * u + r) * 2 * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
                 s[u] = mfma32(__builtin_bit_cast(bf16x8_t, w), q[c], s[u]);
             }
+        // LDS reads stay AHEAD products ahead of the one that takes them
+        constexpr int AHEAD = 6;
+        __builtin_amdgcn_sched_group_barrier(SCHED_LDS_READ, AHEAD, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * KC - AHEAD; ++i) {
+            __builtin_amdgcn_sched_group_barrier(SCHED_MFMA, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(SCHED_LDS_READ, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(SCHED_MFMA, AHEAD, 0);
         // the base-2 scores are s c2
         float c2 = A.scale2;
         const bool clean = j >= first_r && j + 63 <= last_r && !special;
@@ -835,6 +847,10 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
                     s[u][i] = in ? s[u][i] * A.scale2 : -__builtin_inff();
                 }
         }
+        const u32x4_t *vp = &sh.v[buf][(4 * part * NT * 2 + h) * 32 + r];
+        u32x4_t vf[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) vf[n] = vp[n * 64];
         float top = s[0][0];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -851,20 +867,29 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
             for (int n = 0; n < NT; ++n) o[n] *= keep;
         }
         const float ref = m == -__builtin_inff() ? 0.0f : m;
+        // The probabilities of 16 keys are computed between the products of the
+        // 16 before, and a product's values are read as soon as the last one
+        // has taken its own.
+        float p[8];
+        auto probability = [&](int t, int i) {
+            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -ref));
+            l += p[i];
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) probability(0, i);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            float p[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -ref));
-                l += p[i];
-            }
-            asm("" : "+v"(l));  // summed here: later, 32 probabilities would be held for it
             const f16x8_t pb = split_parts<f16x8_t, 1>(p).p[0];
-            const u32x4_t *from = &sh.v[buf][((4 * part + t) * NT * 2 + h) * 32 + r];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                o[n] = mfma32(__builtin_bit_cast(f16x8_t, from[n * 64]), pb, o[n]);
+            for (int n = 0; n < NT; ++n) {
+                o[n] = mfma32(__builtin_bit_cast(f16x8_t, vf[n]), pb, o[n]);
+                if (t < 3) {
+                    vf[n] = vp[(t + 1) * NT * 64 + n * 64];
+#pragma unroll
+                    for (int i = 8 * n / NT; i < 8 * (n + 1) / NT; ++i) probability(t + 1, i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
 
