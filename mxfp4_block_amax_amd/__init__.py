@@ -686,27 +686,40 @@ def padded_storage_bytes(fmt: int, rows: int, cols: int) -> int:
 
 
 
+# The cache calls below run once or more a layer of every decoding step, where
+# the host's own time counts: checks read each property once, pointers go to
+# ctypes as integers, and the stream is the raw handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_KV_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 class KVCache:
     """An 8-bit key/value cache: k_codes, v_codes [pages, kv_heads, block,
     head_dim] and k_scales, v_scales [pages, kv_heads], contiguous uint8 tensors
     on one device (include/fp4.h, fp4_kv_cache)."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_c")
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_shape", "_device", "_c")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
-        if k_codes.dim() != 4:
+        shape = k_codes.shape
+        if len(shape) != 4:
             raise ValueError("codes must be [pages, kv_heads, block, head_dim]")
-        shape, device = k_codes.shape, k_codes.device
-        for t, want in ((k_codes, shape), (k_scales, shape[:2]), (v_codes, shape),
-                        (v_scales, shape[:2])):
-            if t.dtype != torch.uint8:
-                raise TypeError("a cache holds uint8 codes and scales")
-            if t.shape != want or t.device != device or not t.is_contiguous():
-                raise ValueError(f"expected a contiguous {list(want)} tensor on {device}")
         if not k_codes.is_cuda:
             raise TypeError("expected device tensors")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
-                                                                    v_scales)
+        device = k_codes.get_device()
+        u8 = torch.uint8
+        if not (k_codes.dtype is u8 and k_scales.dtype is u8 and v_codes.dtype is u8
+                and v_scales.dtype is u8):
+            raise TypeError("a cache holds uint8 codes and scales")
+        if not (v_codes.shape == shape and k_scales.shape == v_scales.shape == shape[:2]):
+            raise ValueError("v_codes must have k_codes' shape, scales [pages, kv_heads]")
+        if not (k_scales.get_device() == v_codes.get_device() == v_scales.get_device() == device
+                and k_codes.is_contiguous() and k_scales.is_contiguous()
+                and v_codes.is_contiguous() and v_scales.is_contiguous()):
+            raise ValueError("a cache's tensors must be contiguous, on one device")
+        self.k_codes, self.k_scales = k_codes, k_scales
+        self.v_codes, self.v_scales = v_codes, v_scales
+        self._shape, self._device = shape, device
         self._c = _CKvCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                             v_scales.data_ptr(), *shape)
 
@@ -720,34 +733,46 @@ def new_kv_cache(pages: int, kv_heads: int, block: int, head_dim: int, device) -
 
 
 def _kv_batch(cache: KVCache, cu_tokens, lengths, table, tokens: int) -> _CKvBatch:
-    device = cache.k_codes.device
-    for t, dim, what in ((cu_tokens, 1, "cu_tokens"), (lengths, 1, "lengths"), (table, 2, "table")):
-        if t.dtype != torch.int32:
-            raise TypeError(f"{what} must be an int32 tensor")
-        if t.device != device or t.dim() != dim or (t.stride(-1) != 1 and t.shape[-1] > 1):
-            raise ValueError(f"{what} must be {dim}-dimensional, dense, on {device}")
+    i32, device = torch.int32, cache._device
+    if not (cu_tokens.dtype is i32 and lengths.dtype is i32 and table.dtype is i32):
+        raise TypeError("cu_tokens, lengths and table must be int32 tensors")
+    if not (cu_tokens.get_device() == lengths.get_device() == table.get_device() == device):
+        raise ValueError("cu_tokens, lengths and table must be on the cache's device")
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, pages]")
     seqs, width = table.shape
-    if lengths.shape[0] != seqs or cu_tokens.shape[0] != seqs + 1:
+    if lengths.shape != (seqs,) or cu_tokens.shape != (seqs + 1,):
         raise ValueError("for a table of n sequences, lengths has n entries and cu_tokens n + 1")
+    stride, inner = table.stride()
+    if not (cu_tokens.is_contiguous() and lengths.is_contiguous()) or (inner != 1 and width > 1):
+        raise ValueError("cu_tokens, lengths and the rows of table must be dense")
     return _CKvBatch(cu_tokens.data_ptr(), lengths.data_ptr(), table.data_ptr(), tokens,
-                     table.stride(0) if seqs > 1 else width, seqs, width)
+                     stride if seqs > 1 else width, seqs, width)
 
 
 def _kv_rows(x: torch.Tensor, cache: KVCache, what: str):
     """(pointer, token stride, head stride) of rows [tokens, heads, head_dim]."""
-    if x.device != cache.k_codes.device:
+    if x.get_device() != cache._device:
         raise ValueError(f"{what} must be on the cache's device")
-    if x.dim() != 3 or x.shape[2] != cache.k_codes.shape[3] or x.stride(2) != 1:
-        raise ValueError(f"{what} must be [tokens, heads, {cache.k_codes.shape[3]}] with dense "
-                         "last dimension")
-    return (x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0,
-            x.stride(1) if x.shape[1] > 1 else x.shape[2])
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != cache._shape[3]:
+        raise ValueError(f"{what} must be [tokens, heads, {cache._shape[3]}]")
+    token, head, inner = x.stride()
+    if inner != 1:
+        raise ValueError(f"{what} must have a dense last dimension")
+    return x.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else shape[2]
 
 
-def _kv_status(status, check: bool, device):
-    if status is None and check:
-        status = torch.zeros(1, dtype=torch.int32, device=device)
-    return status
+def _kv_call(fn, cache, batch, args, check, status):
+    """One cache call on the current stream; with check, its flags raise."""
+    if check and status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=cache.k_codes.device)
+    code = fn(cache._c, batch, *args, None if status is None else status.data_ptr(),
+              _raw_stream(cache._device))
+    if code:
+        _ok(code)
+    if check:
+        _raise_flags(int(status.item()))
 
 
 def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor,
@@ -756,17 +781,17 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_tokens: 
     """Quantize the batch's new keys and values (fp32 or bf16 [tokens, kv_heads,
     head_dim], slices of a projection's rows allowed) into the cache.  cu_tokens
     [n + 1], lengths [n] (new tokens included) and table [n, width] are int32."""
-    if k.shape != v.shape or k.dtype != v.dtype:
+    shape, dtype = k.shape, k.dtype
+    if v.shape != shape or v.dtype is not dtype:
         raise ValueError("k and v must have the same shape and dtype")
-    if k.dim() != 3 or k.shape[1] != cache.k_codes.shape[1]:
-        raise ValueError("k and v must have the cache's kv heads")
-    batch = _kv_batch(cache, cu_tokens, lengths, table, k.shape[0])
-    status = _kv_status(status, check, k.device)
-    _ok(lib().fp4_kv_cache_write(cache._c, batch, *_kv_rows(k, cache, "k"),
-                                 *_kv_rows(v, cache, "v"), _dtype_code(k.dtype), _ptr(status),
-                                 _stream(k)))
-    if check:
-        _raise_flags(int(status.item()))
+    if len(shape) != 3 or shape[1] != cache._shape[1]:
+        raise ValueError("k and v must be [tokens, the cache's kv heads, head_dim]")
+    code = _KV_DTYPES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    batch = _kv_batch(cache, cu_tokens, lengths, table, shape[0])
+    _kv_call((_lib or lib()).fp4_kv_cache_write, cache, batch,
+             (*_kv_rows(k, cache, "k"), *_kv_rows(v, cache, "v"), code), check, status)
 
 
 def kv_cache_read(cache: KVCache, cu_tokens: torch.Tensor, lengths: torch.Tensor,
@@ -774,7 +799,7 @@ def kv_cache_read(cache: KVCache, cu_tokens: torch.Tensor, lengths: torch.Tensor
                   check: bool = True, status=None):
     """The batch's rows as (k, v), each [tokens, kv_heads, head_dim]; with
     cu_tokens the prefix sums of lengths, whole sequences."""
-    _, heads, _, dim = cache.k_codes.shape
+    _, heads, _, dim = cache._shape
     device = cache.k_codes.device
     if out is None:
         k = torch.empty(tokens, heads, dim, dtype=out_dtype, device=device)
@@ -786,11 +811,8 @@ def kv_cache_read(cache: KVCache, cu_tokens: torch.Tensor, lengths: torch.Tensor
                     or not t.is_contiguous()):
                 raise ValueError(f"out must be two contiguous [{tokens}, {heads}, {dim}] tensors")
     batch = _kv_batch(cache, cu_tokens, lengths, table, tokens)
-    status = _kv_status(status, check, device)
-    _ok(lib().fp4_kv_cache_read(cache._c, batch, _ptr(k), _ptr(v), _dtype_code(k.dtype),
-                                _ptr(status), _stream(k)))
-    if check:
-        _raise_flags(int(status.item()))
+    _kv_call((_lib or lib()).fp4_kv_cache_read, cache, batch,
+             (k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype)), check, status)
     return k, v
 
 
@@ -802,25 +824,28 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
     Returns out, or (out, lse [tokens, heads] fp32).  The work is laid out for
     sequences as long as the table is wide: pass a table (or table[:, :width])
     no wider than the longest one needs."""
+    rows = _kv_rows(q, cache, "q")
     tokens, heads, dim = q.shape
+    dtype = _KV_DTYPES.get(q.dtype)
+    if dtype is None:
+        dtype = _dtype_code(q.dtype)
     batch = _kv_batch(cache, cu_tokens, lengths, table, tokens)
+    device = q.device
     if out is None:
-        out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=q.device)
-    elif (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device
+        out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=device)
+    elif (out.shape != q.shape or out.dtype != q.dtype or out.device != device
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
-    lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device) if return_lse else None
-    rows, dtype = _kv_rows(q, cache, "q"), _dtype_code(q.dtype)
-    L = lib()
-    need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, int(window), dtype)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    status = _kv_status(status, check, q.device)
-    _ok(L.fp4_kv_attention(cache._c, batch, *rows, dtype, heads,
-                           dim ** -0.5 if scale is None else float(scale), 1 if causal else 0,
-                           int(window), _ptr(out), _ptr(lse), _ptr(workspace),
-                           workspace.numel() if workspace is not None else 0, _ptr(status),
-                           _stream(q)))
-    if check:
-        _raise_flags(int(status.item()))
+    lse = torch.empty(tokens, heads, dtype=torch.float32, device=device) if return_lse else None
+    L = _lib or lib()
+    window = int(window)
+    if workspace is None:
+        need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, window, dtype)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    space, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _kv_call(L.fp4_kv_attention, cache, batch,
+             (*rows, dtype, heads, dim ** -0.5 if scale is None else scale, 1 if causal else 0,
+              window, out.data_ptr(), None if lse is None else lse.data_ptr(), space, size),
+             check, status)
     return (out, lse) if return_lse else out

@@ -65,7 +65,7 @@ __device__ __forceinline__ Tile tile_range(const KvCache &C, const KvBatch &B, c
                                            const Item &it, int first_row, int32_t *status) {
     Tile T;
     T.tokens = min(A.tokens, it.count - first_row);
-    const int64_t len = __builtin_amdgcn_readfirstlane(B.lengths[it.seq]);
+    const int64_t len = it.length;
     T.pos0 = len - it.count + first_row;
     int64_t end = A.causal ? T.pos0 + T.tokens : len;
     const int64_t held = (int64_t)B.width << C.block_shift;
@@ -129,25 +129,15 @@ __device__ __forceinline__ float v_operand(uint32_t byte, uint32_t top) {
     return u2f(byte == 255u ? 255u << 23 : (uint32_t)max(e, 0) << 23);
 }
 
-constexpr int NARROW_WG = 256;
-constexpr int NARROW_WAVES = NARROW_WG / WAVE;
-constexpr int NARROW_STEP = 32 * NARROW_WAVES;  // keys of a workgroup's step
-constexpr int NARROW_MAX_KEYS = 4096;           // keys of a split, at most
+constexpr int NARROW_PAGES = 256;  // pages under a workgroup's keys, at most
 
-// The pages under a workgroup's keys.
-constexpr int kPageSlots = NARROW_MAX_KEYS / 16 + 2;
-
-template <int D>
+template <int D, int WAVES>
 struct NarrowShared {
-    union {
-        struct {
-            int page[kPageSlots];
-            uint32_t k_scale[kPageSlots], v_scale[kPageSlots];  // E8M0 bytes
-            uint32_t v_top;  // the largest of v_scale but NaN
-        };
-        float o[NARROW_WAVES][16][D + 4];
-    };
-    float m[NARROW_WAVES][16], l[NARROW_WAVES][16];
+    int page[NARROW_PAGES];
+    uint8_t k_scale[NARROW_PAGES], v_scale[NARROW_PAGES];
+    uint32_t v_top;  // the largest of v_scale but NaN
+    float m[WAVES][16], l[WAVES][16];
+    float o[WAVES][16][D + 4];
 };
 
 // A lane's values of one token: D / 16 consecutive dimensions.
@@ -184,8 +174,8 @@ struct Step {
 // Row tiles of up to 16 query rows (tokens x the query heads of one kv head):
 // single tokens, drafts, short chunks.
 //
-// A workgroup has one row tile, one kv head and one range of keys; its four
-// waves take 32 keys at a time in turn.  Scores are computed transposed,
+// A workgroup has one row tile, one kv head and one range of keys; its waves
+// take 32 keys at a time in turn.  Scores are computed transposed,
 // S^T = K Q^T, so that a lane's scores are those of one row (lane % 16) and its
 // keys, 4 (lane / 16) + i, are the ones the second product wants from this
 // lane: probabilities go from the first product to the second without leaving
@@ -194,17 +184,19 @@ struct Step {
 // free too, so a lane loads D / 16 consecutive bytes of eight value rows and
 // transposes them by byte permutes.  Nothing of keys or values goes through
 // LDS: each byte is used by one lane.
-template <int D, bool F32>
-__global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache C, KvBatch B,
-                                                                        AttnArgs A,
-                                                                        int32_t *status) {
+template <int D, bool F32, int WAVES>
+__global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow_kernel(
+    KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
+    constexpr int STEP = 32 * WAVES;  // keys of a workgroup's step
     constexpr int CH = D / 64, NT = D / 16;
     constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;  // terms of a query and a probability
     // values of the next step are loaded a step ahead where registers allow
     constexpr bool V_AHEAD = D <= 128;
-    __shared__ NarrowShared<D> sh;
+    __shared__ NarrowShared<D, WAVES> sh;
     const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
     const int r = lane & 15, g = lane >> 4;
+    if (threadIdx.x == 0) sh.v_top = 0;
+    __syncthreads();
     const Item it = find_item(B, (int)blockIdx.x, A.tokens, A.tokens > 1 ? 1 : 0);
     const int row0 = it.piece * A.tokens;
     if (it.count <= 0 || row0 >= it.count) {
@@ -269,39 +261,21 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
             }
     }
 
-    // the pages under [k0, k1)
+    // The pages under [k0, k1), k0 a page's first.  A wave looks its first step's
+    // up by itself, so that the step's codes are on their way while the
+    // workgroup's pages and their scales are.
     const int64_t b0 = k0 >> C.block_shift;
-    const int pages = keys > 0 ? (int)(((k1 - 1) >> C.block_shift) - b0) + 1 : 0;
-    bool missing = false;
-    if (threadIdx.x == 0) sh.v_top = 0;
-    __syncthreads();
-    uint32_t v_top = 0;
-    for (int i = threadIdx.x; i < pages; i += NARROW_WG) {
-        const int page = find_page(B, C, it.seq, b0 + i);
-        const int64_t at = (int64_t)max(page, 0) * C.heads + head;
-        sh.page[i] = page;
-        const uint32_t ks = page < 0 ? 0u : C.k_scales[at], vs = page < 0 ? 0u : C.v_scales[at];
-        sh.k_scale[i] = ks;
-        sh.v_scale[i] = vs;
-        if (vs != 255u) v_top = max(v_top, vs);
-        missing |= page < 0;
-    }
-    if (v_top > 0) atomicMax(&sh.v_top, v_top);
-    if (missing) flag(status, FLAG_CACHE_INDEX);
-    __syncthreads();
-    v_top = __builtin_amdgcn_readfirstlane(sh.v_top);
-
+    const int pages = (keys + C.block - 1) >> C.block_shift;
     const uint32_t k_lane = (uint32_t)(r * D + 16 * g);
     const uint32_t v_lane = (uint32_t)(4 * g * D + r * (D / 16));
-    auto page_at = [&](int j) {  // of the keys from j on, relative to k0; clamped to the last
+    auto page_at = [&](int j) {  // of the keys from j on; clamped to the last
         return __builtin_amdgcn_readfirstlane(min(j >> C.block_shift, pages - 1));
     };
-    auto load = [&](int j, Step<D> &s, bool keys_too, bool values_too) {
+    auto load = [&](int j, Step<D> &s, const int(&page)[2], bool keys_too, bool values_too) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int jj = j + 16 * half;
-            const int page = max(__builtin_amdgcn_readfirstlane(sh.page[page_at(jj)]), 0);
-            const int64_t at = page_offset(C, page, head) + (jj & (C.block - 1)) * D;
+            const int64_t at = page_offset(C, max(page[half], 0), head) +
+                               ((j + 16 * half) & (C.block - 1)) * D;
             const uint8_t *kp = C.k_codes + at, *vp = C.v_codes + at;
             if (keys_too)
 #pragma unroll
@@ -311,6 +285,38 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
                 for (int i = 0; i < 4; ++i) s.v[half][i] = load_v<D>(vp + v_lane + i * D);
         }
     };
+    auto load_held = [&](int j, Step<D> &s, bool keys_too, bool values_too) {
+        const int page[2] = {__builtin_amdgcn_readfirstlane(sh.page[page_at(j)]),
+                             __builtin_amdgcn_readfirstlane(sh.page[page_at(j + 16)])};
+        load(j, s, page, keys_too, values_too);
+    };
+    Step<D> now, next;
+    // a window may start inside its first page
+    int j = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / STEP * STEP + 32 * wave;
+    {
+        int page = -1, first_pages[2] = {-1, -1};
+        if ((int)threadIdx.x < pages) page = find_page(B, C, it.seq, b0 + threadIdx.x);
+        if (j < keys) {
+            first_pages[0] = __builtin_amdgcn_readfirstlane(find_page(B, C, it.seq, b0 + page_at(j)));
+            first_pages[1] =
+                __builtin_amdgcn_readfirstlane(find_page(B, C, it.seq, b0 + page_at(j + 16)));
+            load(j, now, first_pages, true, V_AHEAD);
+        }
+        uint32_t v_top = 0;
+        auto hold = [&](int i, int page) {
+            const int64_t at = (int64_t)max(page, 0) * C.heads + head;
+            const uint32_t ks = page < 0 ? 0u : C.k_scales[at], vs = page < 0 ? 0u : C.v_scales[at];
+            sh.page[i] = page;
+            sh.k_scale[i] = (uint8_t)ks;
+            sh.v_scale[i] = (uint8_t)vs;
+            if (vs != 255u) v_top = max(v_top, vs);
+            if (page < 0) flag(status, FLAG_CACHE_INDEX);
+        };
+        if ((int)threadIdx.x < pages) hold(threadIdx.x, page);
+        if (v_top > 0) atomicMax(&sh.v_top, v_top);
+    }
+    __syncthreads();
+    const uint32_t v_top = __builtin_amdgcn_readfirstlane(sh.v_top);
 
     f32x4_t o[NT];
 #pragma unroll
@@ -460,14 +466,10 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
         }
     };
 
-    Step<D> now, next;
-    // a window may start inside its first page
-    int j = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / NARROW_STEP * NARROW_STEP + 32 * wave;
-    if (j < keys) load(j, now, true, V_AHEAD);
     while (j < keys) {
-        const int after = j + NARROW_STEP;
-        if (!V_AHEAD) load(j, now, false, true);
-        if (after < keys) load(after, next, true, V_AHEAD);
+        const int after = j + STEP;
+        if (!V_AHEAD) load_held(j, now, false, true);
+        if (after < keys) load_held(after, next, true, V_AHEAD);
         compute(j, now);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -480,10 +482,9 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
         j = after;
     }
 
-    // join the four waves
+    // join the waves
     l += __shfl_xor(l, 16, WAVE);
     l += __shfl_xor(l, 32, WAVE);
-    __syncthreads();  // the pages are done with
     if (g == 0) {
         sh.m[wave][r] = m;
         sh.l[wave][r] = l;
@@ -491,7 +492,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     __syncthreads();
     float top = sh.m[0][r];
 #pragma unroll
-    for (int w = 1; w < NARROW_WAVES; ++w) top = __builtin_fmaxf(top, sh.m[w][r]);
+    for (int w = 1; w < WAVES; ++w) top = __builtin_fmaxf(top, sh.m[w][r]);
     const float own = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -505,14 +506,15 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     }
     __syncthreads();
     // 16 lanes a row, four dimensions at a time
+    if (threadIdx.x >= 256) return;
     const int rr = threadIdx.x >> 4, part = threadIdx.x & 15;
     const int ti = rr / hn, th = rr - ti * hn;
     if (ti >= T.tokens) return;
     float m_all = sh.m[0][rr], l_all = 0.0f;
 #pragma unroll
-    for (int w = 1; w < NARROW_WAVES; ++w) m_all = __builtin_fmaxf(m_all, sh.m[w][rr]);
+    for (int w = 1; w < WAVES; ++w) m_all = __builtin_fmaxf(m_all, sh.m[w][rr]);
 #pragma unroll
-    for (int w = 0; w < NARROW_WAVES; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         const float mw = sh.m[w][rr];
         l_all = __builtin_fmaf(sh.l[w][rr],
                                mw == m_all ? 1.0f : __builtin_amdgcn_exp2f(mw - m_all), l_all);
@@ -525,7 +527,7 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
         const int d = 64 * c + 4 * part;
         f32x4_t y = *(const f32x4_t *)&sh.o[0][rr][d];
 #pragma unroll
-        for (int w = 1; w < NARROW_WAVES; ++w) y += *(const f32x4_t *)&sh.o[w][rr][d];
+        for (int w = 1; w < WAVES; ++w) y += *(const f32x4_t *)&sh.o[w][rr][d];
         y *= inv;
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = __builtin_ldexpf(y[i], back);
@@ -550,45 +552,68 @@ __global__ __launch_bounds__(NARROW_WG, 2) void attention_narrow_kernel(KvCache 
     }
 }
 
-// Joins the splits of rows that have more than one, in order: a wave a row.  A
-// split's output is normalised by its own sum, so its weight is that sum.
+// Joins the splits of rows that have more than one: a workgroup a row.  A
+// split's output is normalised by its own sum, so its weight is that sum.  D / 4
+// lanes have four dimensions each; the groups of lanes take every GROUPS-th split
+// and are added in order.
+constexpr int JOIN_WG = 256;
+
 template <int D, bool F32>
-__global__ __launch_bounds__(256) void attention_join_kernel(KvCache C, KvBatch B, AttnArgs A) {
-    constexpr int N = D / WAVE;
-    const int lane = threadIdx.x & (WAVE - 1);
-    const int token = blockIdx.x, hq = blockIdx.y * 4 + threadIdx.x / WAVE;
-    if (hq >= A.heads) return;
-    const int64_t row = (int64_t)token * A.heads + hq;
-    const Item it = find_item(B, token, 1, 0);
+__global__ __launch_bounds__(JOIN_WG) void attention_join_kernel(KvCache C, KvBatch B, AttnArgs A) {
+    constexpr int LANES = D / 4, GROUPS = JOIN_WG / LANES;
+    __shared__ float tops[JOIN_WG / WAVE], sums[GROUPS];
+    __shared__ f32x4_t outs[GROUPS][LANES];
+    const int64_t row = (int64_t)blockIdx.x * A.heads + blockIdx.y;
+    const Item it = find_item(B, (int)blockIdx.x, 1, 0);
     if (it.count <= 0 || it.seq >= B.seqs || it.piece >= it.count) return;
     const Tile T = tile_range(C, B, A, it, it.piece / A.tokens * A.tokens, nullptr);
     const int n = (int)((T.end - T.base + A.split_keys - 1) / A.split_keys);
     if (n <= 1) return;
     const float2 *ml = A.part_ml + row * A.splits;
     float top = -__builtin_inff();
-    for (int i = lane; i < n; i += WAVE) top = __builtin_fmaxf(top, ml[i].x);
+    for (int i = threadIdx.x; i < n; i += JOIN_WG) top = __builtin_fmaxf(top, ml[i].x);
     for (int off = 32; off >= 1; off >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, off, WAVE));
-    float l = 0.0f, o[N];
+    if ((threadIdx.x & (WAVE - 1)) == 0) tops[threadIdx.x / WAVE] = top;
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = 0.0f;
-    const float *po = A.part_o + row * A.splits * D + N * lane;
-    for (int i = 0; i < n; ++i) {
-        const float2 w = ml[i];
-        const float f = w.y * (w.x == top ? 1.0f : __builtin_amdgcn_exp2f(w.x - top));
-        l += f;
+    for (int w = 0; w < JOIN_WG / WAVE; ++w) top = __builtin_fmaxf(top, tops[w]);
+    const int g = threadIdx.x / LANES, lane = threadIdx.x - g * LANES;
+    float l = 0.0f;
+    f32x4_t o = {0, 0, 0, 0};
+    if (g < GROUPS) {
+        const f32x4_t *po = (const f32x4_t *)(A.part_o + row * A.splits * D) + lane;
+#pragma unroll 4
+        for (int i = g; i < n; i += GROUPS) {
+            const float2 w = ml[i];
+            const float f = w.y * (w.x == top ? 1.0f : __builtin_amdgcn_exp2f(w.x - top));
+            const f32x4_t x = po[(int64_t)i * LANES];
+            l += f;
 #pragma unroll
-        for (int k = 0; k < N; ++k) o[k] = __builtin_fmaf(po[(int64_t)i * D + k], f, o[k]);
+            for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(x[k], f, o[k]);
+        }
+        outs[g][lane] = o;
+        if (lane == 0) sums[g] = l;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __syncthreads();
+    if (threadIdx.x >= LANES) return;
+    l = sums[0];
+    o = outs[0][lane];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int64_t at = row * D + N * lane + k;
-        if constexpr (F32)
-            ((float *)A.out)[at] = o[k] * inv;
-        else
-            ((__bf16 *)A.out)[at] = (__bf16)(o[k] * inv);
+    for (int k = 1; k < GROUPS; ++k) {
+        l += sums[k];
+        o += outs[k][lane];
     }
-    if (A.lse != nullptr && lane == 0)
+    o *= l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = row * D + 4 * lane;
+    if constexpr (F32) {
+        *(f32x4_t *)((float *)A.out + at) = o;
+    } else {
+        const f32x2_t lo = {o.x, o.y}, hi = {o.z, o.w};
+        *(uint2 *)((uint16_t *)A.out + at) =
+            make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
+                       __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
+    }
+    if (A.lse != nullptr && threadIdx.x == 0)
         A.lse[row] = l == 0.0f ? -__builtin_inff()
                                : ((top == -__builtin_inff() ? 0.0f : top) +
                                   __builtin_amdgcn_logf(l)) * kLn2;
@@ -811,6 +836,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         f32x16_t s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) s[u] = f32x16_t{};
+        __builtin_amdgcn_s_setprio(1);
         const u32x4_t *kp = &sh.k[buf][64 * part * 2 * KC];
 #pragma unroll
         for (int c = 0; c < KC; ++c)
@@ -819,6 +845,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
                 const u32x4_t w = kp[(32 * u + r) * 2 * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
                 s[u] = mfma32(__builtin_bit_cast(bf16x8_t, w), q[c], s[u]);
             }
+        __builtin_amdgcn_s_setprio(0);
         // LDS reads stay AHEAD products ahead of the one that takes them
         constexpr int AHEAD = 6;
         __builtin_amdgcn_sched_group_barrier(SCHED_LDS_READ, AHEAD, 0);
@@ -1022,10 +1049,13 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
 // How a call is laid out: from its shapes alone, which the workspace's size
 // needs too.
 struct Plan {
-    int wide;  // waves of a wide workgroup, 0 for narrow tiles
+    int wide;   // waves of a wide workgroup, 0 for narrow tiles
+    int waves;  // of a narrow workgroup
     int sub, sub_heads, tokens, splits, split_keys;
     int64_t items;
 };
+
+constexpr int CUS = 256;
 
 Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool bf16) {
     Plan P;
@@ -1040,18 +1070,22 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     int64_t extent = (int64_t)B.width << C.block_shift;
     if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + P.tokens + C.block);
     const int64_t tiles = std::max<int64_t>(1, B.tokens / P.tokens) * C.heads * P.sub;
+    int64_t keys;
+    P.waves = 0;
     if (P.wide) {
-        const int64_t want = std::max<int64_t>(1, 512 / tiles);
-        int64_t keys = (extent + want - 1) / want;
+        const int64_t want = std::max<int64_t>(1, 2 * CUS / tiles);
+        keys = (extent + want - 1) / want;
         keys = (keys + WIDE_SEGMENT - 1) / WIDE_SEGMENT * WIDE_SEGMENT;
-        P.split_keys = (int)keys;
-        P.splits = (int)((extent + keys - 1) / keys);
-        return P;
+    } else {
+        // few tiles: workgroups of 8 waves, one a CU; else of 4, two a CU
+        P.waves = tiles <= CUS ? 8 : 4;
+        const int64_t slots = P.waves == 8 ? CUS : 2 * CUS;
+        const int64_t want = tiles <= slots ? slots / tiles : (3 * slots + tiles - 1) / tiles;
+        keys = (extent + want - 1) / want;
+        if (extent <= 6 * 32 * P.waves) keys = extent;
+        keys = (keys + 255) / 256 * 256;  // whole pages
+        keys = std::min<int64_t>(keys, std::min<int64_t>(NARROW_PAGES * C.block, 16384));
     }
-    const int64_t want = std::max<int64_t>(1, 2048 / tiles);
-    int64_t keys = (extent + want - 1) / want;
-    keys = (keys + 2 * NARROW_STEP - 1) / (2 * NARROW_STEP) * (2 * NARROW_STEP);  // whole pages
-    keys = std::min<int64_t>(keys, NARROW_MAX_KEYS);
     P.split_keys = (int)keys;
     P.splits = (int)((extent + keys - 1) / keys);
     return P;
@@ -1081,19 +1115,20 @@ static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, co
             hipLaunchKernelGGL((attention_wide_kernel<D, 8>),
                                dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)),
                                dim3(P.wide * WAVE), 0, s, C, B, A, status);
-    } else if (bf16) {
-        hipLaunchKernelGGL((attention_narrow_kernel<D, false>), grid, dim3(NARROW_WG), 0, s, C, B,
-                           A, status);
     } else {
-        hipLaunchKernelGGL((attention_narrow_kernel<D, true>), grid, dim3(NARROW_WG), 0, s, C, B, A,
-                           status);
+        void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) =
+            bf16 ? (P.waves == 8 ? attention_narrow_kernel<D, false, 8>
+                                 : attention_narrow_kernel<D, false, 4>)
+                 : (P.waves == 8 ? attention_narrow_kernel<D, true, 8>
+                                 : attention_narrow_kernel<D, true, 4>);
+        hipLaunchKernelGGL(kernel, grid, dim3(P.waves * WAVE), 0, s, C, B, A, status);
     }
     if (P.splits <= 1) return;
-    const dim3 join((uint32_t)B.tokens, (A.heads + 3) / 4);
+    const dim3 join((uint32_t)B.tokens, A.heads);
     if (bf16)
-        hipLaunchKernelGGL((attention_join_kernel<D, false>), join, dim3(256), 0, s, C, B, A);
+        hipLaunchKernelGGL((attention_join_kernel<D, false>), join, dim3(JOIN_WG), 0, s, C, B, A);
     else
-        hipLaunchKernelGGL((attention_join_kernel<D, true>), join, dim3(256), 0, s, C, B, A);
+        hipLaunchKernelGGL((attention_join_kernel<D, true>), join, dim3(JOIN_WG), 0, s, C, B, A);
 }
 
 hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, int64_t q_token,

@@ -37,15 +37,16 @@ __device__ __forceinline__ int64_t page_offset(const KvCache &C, int page, int h
 // floor difference + 1 pieces (extra 1), from inside a unit one more (extra
 // 2).  Items past a sequence's pieces end at once.  Sequence `seqs` stands for
 // the rows past cu[seqs].  The search reads 64 candidates at a time, one per
-// lane: one step up to 64 sequences, two up to 4096.
+// lane: one step up to 62 sequences, two up to some 4000.
 struct Item {
     int seq, piece, base, count;  // base, count: the sequence's rows [base, base + count)
+    int length;                   // the sequence's tokens
 };
 
 __device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit, int extra) {
     const int lane = threadIdx.x & (WAVE - 1);
     int lo = 0, n = B.seqs + 1;
-    while (n > 1) {
+    while (n >= WAVE) {
         const int step = (n + WAVE - 1) / WAVE;
         const int i = lo + lane * step;
         const bool at = lane * step < n && B.cu[i] / unit + extra * i <= item;
@@ -54,12 +55,17 @@ __device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit, 
         lo += k * step;
         n = min(step, n - k * step);
     }
-    lo = __builtin_amdgcn_readfirstlane(lo);
+    // the last step's lanes also hold what comes with the sequence found
+    const int i = min(lo + lane, B.seqs);
+    const int cu = B.cu[i], len = B.lengths[min(i, B.seqs - 1)];
+    const uint64_t b = __ballot(lane < n && cu / unit + extra * i <= item);
+    const int k = b ? 63 - __builtin_clzll(b) : 0;
     Item it;
-    it.seq = lo;
-    it.base = __builtin_amdgcn_readfirstlane(B.cu[lo]);
-    it.piece = item - (it.base / unit + extra * lo);
-    it.count = (lo < B.seqs ? __builtin_amdgcn_readfirstlane(B.cu[lo + 1]) : B.tokens) - it.base;
+    it.seq = __builtin_amdgcn_readfirstlane(lo + k);
+    it.base = __builtin_amdgcn_readlane(cu, k);
+    it.length = __builtin_amdgcn_readlane(len, k);
+    it.piece = item - (it.base / unit + extra * it.seq);
+    it.count = (it.seq < B.seqs ? __builtin_amdgcn_readlane(cu, k + 1) : B.tokens) - it.base;
     // a cu that is no prefix sum of at most `tokens` rows gives no piece
     if (it.base < 0 || it.count < 0 || it.base > B.tokens || it.count > B.tokens - it.base ||
         it.piece < 0)

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
     }
-    const int64_t len = B.lengths[it.seq], start = len - it.count;
+    const int64_t len = it.length, start = len - it.count;
     const int64_t b = (start < 0 ? 0 : start >> C.block_shift) + it.piece;
     const int64_t p0 = max(max(b << C.block_shift, start), (int64_t)0);
     const int64_t p1 = min((b + 1) << C.block_shift, len);
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvCache C, KvBatch B, void
     // rows past the last sequence, positions before 0 and pages that do not
     // exist read as zero
     const bool none = it.seq >= B.seqs;
-    const int64_t len = none ? it.count : B.lengths[it.seq], start = len - it.count;
+    const int64_t len = none ? it.count : it.length, start = len - it.count;
     const int64_t b = (start >> C.block_shift) + it.piece;
     const int64_t p0 = max(b << C.block_shift, start);
     const int64_t p1 = min((b + 1) << C.block_shift, len);
