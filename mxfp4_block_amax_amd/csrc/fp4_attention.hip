@@ -292,7 +292,9 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
     };
     Step<D> now, next;
     // a window may start inside its first page
-    int j = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / STEP * STEP + 32 * wave;
+    const int start = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / STEP * STEP;
+    int j = start + 32 * wave;
+    const int busy = min(max((keys - start + 31) / 32, 1), WAVES);  // waves that have a step
     {
         int page = -1, first_pages[2] = {-1, -1};
         if ((int)threadIdx.x < pages) page = find_page(B, C, it.seq, b0 + threadIdx.x);
@@ -490,66 +492,77 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
         sh.l[wave][r] = l;
     }
     __syncthreads();
-    float top = sh.m[0][r];
+    // `count` waves: all, as a constant, or those that had a step
+    auto join = [&](auto count) {
+        if (wave < count) {
+            float top = sh.m[0][r];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) top = __builtin_fmaxf(top, sh.m[w][r]);
-    const float own = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+            for (int w = 1; w < count; ++w) top = __builtin_fmaxf(top, sh.m[w][r]);
+            const float own = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float *to = &sh.o[wave][r][NT * (4 * g + i)];
+            for (int i = 0; i < 4; ++i) {
+                float *to = &sh.o[wave][r][NT * (4 * g + i)];
 #pragma unroll
-        for (int n = 0; n < NT; n += 4) {
-            f32x4_t y = {o[n][i], o[n + 1][i], o[n + 2][i], o[n + 3][i]};
-            y *= own;
-            *(f32x4_t *)(to + n) = y;
+                for (int n = 0; n < NT; n += 4) {
+                    f32x4_t y = {o[n][i], o[n + 1][i], o[n + 2][i], o[n + 3][i]};
+                    y *= own;
+                    *(f32x4_t *)(to + n) = y;
+                }
+            }
         }
-    }
-    __syncthreads();
-    // 16 lanes a row, four dimensions at a time
-    if (threadIdx.x >= 256) return;
-    const int rr = threadIdx.x >> 4, part = threadIdx.x & 15;
-    const int ti = rr / hn, th = rr - ti * hn;
-    if (ti >= T.tokens) return;
-    float m_all = sh.m[0][rr], l_all = 0.0f;
+        __syncthreads();
+        // 16 lanes a row, four dimensions at a time
+        if (threadIdx.x >= 256) return;
+        const int rr = threadIdx.x >> 4, part = threadIdx.x & 15;
+        const int ti = rr / hn, th = rr - ti * hn;
+        if (ti >= T.tokens) return;
+        float m_all = sh.m[0][rr], l_all = 0.0f;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) m_all = __builtin_fmaxf(m_all, sh.m[w][rr]);
+        for (int w = 1; w < count; ++w) m_all = __builtin_fmaxf(m_all, sh.m[w][rr]);
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        const float mw = sh.m[w][rr];
-        l_all = __builtin_fmaf(sh.l[w][rr],
-                               mw == m_all ? 1.0f : __builtin_amdgcn_exp2f(mw - m_all), l_all);
-    }
-    const int64_t row = (it.base + row0 + ti) * (int64_t)A.heads + head * A.group + h0 + th;
-    const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
-    const int back = (int)v_top - (int)E8M0_ONE - kVBias;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int d = 64 * c + 4 * part;
-        f32x4_t y = *(const f32x4_t *)&sh.o[0][rr][d];
-#pragma unroll
-        for (int w = 1; w < WAVES; ++w) y += *(const f32x4_t *)&sh.o[w][rr][d];
-        y *= inv;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_ldexpf(y[i], back);
-        if (!whole) {
-            *(f32x4_t *)(A.part_o + (row * A.splits + split) * D + d) = y;
-        } else if constexpr (!F32) {
-            const f32x2_t lo = {y.x, y.y}, hi = {y.z, y.w};
-            *(uint2 *)((uint16_t *)A.out + row * D + d) =
-                make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
-                           __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
-        } else {
-            *(f32x4_t *)((float *)A.out + row * D + d) = y;
+        for (int w = 0; w < count; ++w) {
+            const float mw = sh.m[w][rr];
+            l_all = __builtin_fmaf(sh.l[w][rr],
+                                   mw == m_all ? 1.0f : __builtin_amdgcn_exp2f(mw - m_all), l_all);
         }
-    }
-    if (part == 0) {
-        if (!whole)
-            A.part_ml[row * A.splits + split] = make_float2(m_all, l_all);
-        else if (A.lse != nullptr)
-            A.lse[row] = l_all == 0.0f ? -__builtin_inff()
-                                       : ((m_all == -__builtin_inff() ? 0.0f : m_all) +
-                                          __builtin_amdgcn_logf(l_all)) * kLn2;
-    }
+        const int64_t row = (it.base + row0 + ti) * (int64_t)A.heads + head * A.group + h0 + th;
+        const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+        const int back = (int)v_top - (int)E8M0_ONE - kVBias;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int d = 64 * c + 4 * part;
+            f32x4_t y = *(const f32x4_t *)&sh.o[0][rr][d];
+#pragma unroll
+            for (int w = 1; w < count; ++w) y += *(const f32x4_t *)&sh.o[w][rr][d];
+            y *= inv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = __builtin_ldexpf(y[i], back);
+            if (!whole) {
+                *(f32x4_t *)(A.part_o + (row * A.splits + split) * D + d) = y;
+            } else if constexpr (!F32) {
+                const f32x2_t lo = {y.x, y.y}, hi = {y.z, y.w};
+                *(uint2 *)((uint16_t *)A.out + row * D + d) =
+                    make_uint2(__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t)),
+                               __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t)));
+            } else {
+                *(f32x4_t *)((float *)A.out + row * D + d) = y;
+            }
+        }
+        if (part == 0) {
+            if (!whole)
+                A.part_ml[row * A.splits + split] = make_float2(m_all, l_all);
+            else if (A.lse != nullptr)
+                A.lse[row] = l_all == 0.0f ? -__builtin_inff()
+                                           : ((m_all == -__builtin_inff() ? 0.0f : m_all) +
+                                              __builtin_amdgcn_logf(l_all)) * kLn2;
+        }
+    };
+    if (busy == WAVES)
+        join(std::integral_constant<int, WAVES>{});
+    else if (busy == 1)
+        join(std::integral_constant<int, 1>{});
+    else
+        join(busy);
 }
 
 // Joins the splits of rows that have more than one: a workgroup a row.  A
@@ -1056,12 +1069,16 @@ struct Plan {
 };
 
 constexpr int CUS = 256;
+constexpr int WIDE_MIN_KEYS = 1024;
 
 Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool bf16) {
     Plan P;
     const int group = heads / C.heads;
     const int64_t per = (B.tokens + B.seqs - 1) / B.seqs;  // new tokens of a sequence, on average
-    P.wide = bf16 && per * group > 64 && C.dim <= 128 ? 8 : 0;
+    // FORCE
+    P.wide = 0;
+    if (bf16 && per * group > (C.dim <= 128 ? 24 : 48))
+        P.wide = C.dim <= 128 && per * group >= 256 && B.tokens * heads >= 2 * CUS * 256 ? 8 : 4;
     const int rows = P.wide ? 32 * P.wide : 16;
     P.sub = (group + rows - 1) / rows;
     P.sub_heads = (group + P.sub - 1) / P.sub;
@@ -1069,21 +1086,23 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     P.items = P.tokens > 1 ? item_count(B.tokens, B.seqs, P.tokens, 1) : B.tokens;
     int64_t extent = (int64_t)B.width << C.block_shift;
     if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + P.tokens + C.block);
-    const int64_t tiles = std::max<int64_t>(1, B.tokens / P.tokens) * C.heads * P.sub;
+    const int64_t tiles = (per + P.tokens - 1) / P.tokens * B.seqs * C.heads * P.sub;
     int64_t keys;
     P.waves = 0;
     if (P.wide) {
-        const int64_t want = std::max<int64_t>(1, 2 * CUS / tiles);
-        keys = (extent + want - 1) / want;
-        keys = (keys + WIDE_SEGMENT - 1) / WIDE_SEGMENT * WIDE_SEGMENT;
+        const int64_t slots = P.wide == 8 ? CUS : 2 * CUS;
+        const int64_t want = std::max<int64_t>(1, slots / tiles);
+        keys = std::max<int64_t>((extent + want - 1) / want, WIDE_MIN_KEYS);
+        keys = (keys + 255) / 256 * 256;  // whole pages and steps
     } else {
-        // few tiles: workgroups of 8 waves, one a CU; else of 4, two a CU
-        P.waves = tiles <= CUS ? 8 : 4;
-        const int64_t slots = P.waves == 8 ? CUS : 2 * CUS;
+        // few tiles: workgroups of 8 waves, one a CU (of 16 where 64 dimensions
+        // take half the registers); else of 4, two a CU
+        P.waves = tiles > CUS ? 4 : C.dim == 64 ? 16 : 8;
+        const int64_t slots = P.waves > 4 ? CUS : 2 * CUS;
         const int64_t want = tiles <= slots ? slots / tiles : (3 * slots + tiles - 1) / tiles;
         keys = (extent + want - 1) / want;
         if (extent <= 6 * 32 * P.waves) keys = extent;
-        keys = (keys + 255) / 256 * 256;  // whole pages
+        keys = (keys + 255) / 256 * 256;  // whole pages and steps
         keys = std::min<int64_t>(keys, std::min<int64_t>(NARROW_PAGES * C.block, 16384));
     }
     P.split_keys = (int)keys;
@@ -1111,16 +1130,18 @@ static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, co
                        bool bf16, int32_t *status, hipStream_t s) {
     const dim3 grid((uint32_t)P.items, C.heads * P.sub, P.splits);
     if (P.wide) {
+        void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) = attention_wide_kernel<D, 4>;
         if constexpr (D <= 128)
-            hipLaunchKernelGGL((attention_wide_kernel<D, 8>),
-                               dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)),
-                               dim3(P.wide * WAVE), 0, s, C, B, A, status);
+            if (P.wide == 8) kernel = attention_wide_kernel<D, 8>;
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)),
+                           dim3(P.wide * WAVE), 0, s, C, B, A, status);
     } else {
+        constexpr int MANY = D == 64 ? 16 : 8;
         void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) =
-            bf16 ? (P.waves == 8 ? attention_narrow_kernel<D, false, 8>
-                                 : attention_narrow_kernel<D, false, 4>)
-                 : (P.waves == 8 ? attention_narrow_kernel<D, true, 8>
-                                 : attention_narrow_kernel<D, true, 4>);
+            bf16 ? (P.waves == 4 ? attention_narrow_kernel<D, false, 4>
+                                 : attention_narrow_kernel<D, false, MANY>)
+                 : (P.waves == 4 ? attention_narrow_kernel<D, true, 4>
+                                 : attention_narrow_kernel<D, true, MANY>);
         hipLaunchKernelGGL(kernel, grid, dim3(P.waves * WAVE), 0, s, C, B, A, status);
     }
     if (P.splits <= 1) return;
