@@ -643,9 +643,6 @@ __device__ __forceinline__ f32x16_t mfma32(f16x8_t a, f16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// kinds of instructions for the scheduler's groups
-constexpr int SCHED_MFMA = 8, SCHED_LDS_READ = 256;
-
 constexpr int WIDE_SEGMENT = 2048;  // keys whose pages are held in LDS
 // a segment's pages, and those a step that ends past it may ask for
 constexpr int WIDE_PAGES = (WIDE_SEGMENT + 128) / 16;
@@ -851,23 +848,23 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         for (int u = 0; u < 2; ++u) s[u] = f32x16_t{};
         __builtin_amdgcn_s_setprio(1);
         const u32x4_t *kp = &sh.k[buf][64 * part * 2 * KC];
-#pragma unroll
-        for (int c = 0; c < KC; ++c)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const u32x4_t w = kp[(32 * u + r) * 2 * KC + ((2 * c + h) ^ key_swizzle<D>(r))];
-                s[u] = mfma32(__builtin_bit_cast(bf16x8_t, w), q[c], s[u]);
-            }
-        __builtin_amdgcn_s_setprio(0);
-        // LDS reads stay AHEAD products ahead of the one that takes them
+        // product i: dimensions 16 (i / 2) .., keys 32 (i & 1) ..; its keys are read
+        // AHEAD products before it
         constexpr int AHEAD = 6;
-        __builtin_amdgcn_sched_group_barrier(SCHED_LDS_READ, AHEAD, 0);
+        auto key = [&](int i) {
+            return kp[(32 * (i & 1) + r) * 2 * KC + ((2 * (i / 2) + h) ^ key_swizzle<D>(r))];
+        };
+        u32x4_t kf[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 2 * KC - AHEAD; ++i) {
-            __builtin_amdgcn_sched_group_barrier(SCHED_MFMA, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(SCHED_LDS_READ, 1, 0);
+        for (int i = 0; i < AHEAD; ++i) kf[i] = key(i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2 * KC; ++i) {
+            s[i & 1] = mfma32(__builtin_bit_cast(bf16x8_t, kf[i % AHEAD]), q[i / 2], s[i & 1]);
+            if (i + AHEAD < 2 * KC) kf[i % AHEAD] = key(i + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_group_barrier(SCHED_MFMA, AHEAD, 0);
+        __builtin_amdgcn_s_setprio(0);
         // the base-2 scores are s c2
         float c2 = A.scale2;
         const bool clean = j >= first_r && j + 63 <= last_r && !special;
