@@ -800,38 +800,36 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
             }
         }
     };
-    auto store = [&](int buf, int j) {
-#pragma unroll
-        for (int i = 0; i < KL; ++i) {
+    // A step's way into LDS, in PIECES pieces that a caller puts between products.
+    constexpr int PIECES = 2 * KL + 2 * (2 * W4 + W2);
+    auto store = [&](int buf, int j, int piece) {
+        if (piece < 2 * KL) {  // half a chunk of a key
+            const int i = piece / 2, e = piece & 1;
             const int c = threadIdx.x + i * WG;
             const int key = c / KC;
-            const int at = 2 * (c - key * KC), swz = key_swizzle<D>(key);
-            sh.k[buf][key * 2 * KC + (at ^ swz)] =
-                __builtin_bit_cast(u32x4_t, widen_codes(kr[i].x, kr[i].y, k_scale[i]));
-            sh.k[buf][key * 2 * KC + ((at + 1) ^ swz)] =
-                __builtin_bit_cast(u32x4_t, widen_codes(kr[i].z, kr[i].w, k_scale[i]));
+            sh.k[buf][key * 2 * KC + ((2 * (c - key * KC) + e) ^ key_swizzle<D>(key))] =
+                __builtin_bit_cast(u32x4_t, e ? widen_codes(kr[i].z, kr[i].w, k_scale[i])
+                                              : widen_codes(kr[i].x, kr[i].y, k_scale[i]));
+            return;
         }
-        if (any_nan) sh.nan[buf] = j + STEP;
+        // a dimension of eight values: of dimensions n and n + 1 the bytes of two
+        // keys lie in a half word each
+        const int at = piece - 2 * KL, w = at / 4, n = at & 3;
+        const uint32_t sel = n & 2 ? 0x07030602u : 0x05010400u;
+        u32x4_t a;
 #pragma unroll
-        for (int w = 0; w < W4 + W2; ++w) {
-            u32x4_t *to = &sh.v[buf][((vt * NT + 4 * w) * 2 + h) * 32 + r];
-#pragma unroll
-            for (int n = 0; n < (w < W4 ? 4 : 2); n += 2) {
-                // bytes of dimensions n and n + 1, two keys to a half word
-                const uint32_t sel = n ? 0x07030602u : 0x05010400u;
-                u32x4_t a, b;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t x = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], sel);
-                    a[k] = __builtin_bit_cast(
-                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, v_scale, false));
-                    b[k] = __builtin_bit_cast(
-                        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, v_scale, true));
-                }
-                to[n * 64] = a;
-                to[n * 64 + 64] = b;
-            }
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x = __builtin_amdgcn_perm(vr[w][2 * k + 1], vr[w][2 * k], sel);
+            a[k] = __builtin_bit_cast(uint32_t,
+                                      n & 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, v_scale, true)
+                                            : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, v_scale, false));
         }
+        sh.v[buf][((vt * NT + 4 * w + n) * 2 + h) * 32 + r] = a;
+        if (at == 0 && any_nan) sh.nan[buf] = j + STEP;
+    };
+    auto store_all = [&](int buf, int j) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) store(buf, j, i);
     };
 
     f32x16_t o[NT];
@@ -841,7 +839,8 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
     uint32_t v_top = 0;
 
     // 64 keys, part `part` of the step at j0
-    auto compute = [&](int buf, int j0, int part, int seg) {
+    // `between(i)` runs after product i of the scores
+    auto compute = [&](int buf, int j0, int part, int seg, auto between) {
         const int j = j0 + 64 * part;
         f32x16_t s[2];
 #pragma unroll
@@ -862,6 +861,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         for (int i = 0; i < 2 * KC; ++i) {
             s[i & 1] = mfma32(__builtin_bit_cast(bf16x8_t, kf[i % AHEAD]), q[i / 2], s[i & 1]);
             if (i + AHEAD < 2 * KC) kf[i % AHEAD] = key(i + AHEAD);
+            between(i);
             __builtin_amdgcn_sched_barrier(0);
         }
         __builtin_amdgcn_s_setprio(0);
@@ -1004,17 +1004,31 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         __syncthreads();
         int buf = 0, j = max(seg, start);
         load(j, seg);
-        store(0, j);
+        store_all(0, j);
         __syncthreads();
         for (; j < seg_end; j += STEP) {
             const bool more = j + STEP < seg_end;
             if (more) load(j + STEP, seg);
 #pragma unroll 1
-            for (int part = 0; part < STEP / 64; ++part)
+            for (int part = 0; part < STEP / 64 - 1; ++part)
                 if (j + 64 * part <= wave_last && j + 64 * part + 63 >= wave_first)
-                    compute(buf, j, part, seg);
+                    compute(buf, j, part, seg, [](int) {});
+            // the next step is stored between the products of the last part
+            const int part = STEP / 64 - 1;
+            if (j + 64 * part <= wave_last && j + 64 * part + 63 >= wave_first) {
+                if (more)
+                    compute(buf, j, part, seg, [&](int i) {
+                        constexpr int EACH = (PIECES + 2 * KC - 1) / (2 * KC);
+#pragma unroll
+                        for (int e = EACH * i; e < EACH * (i + 1); ++e)
+                            if (e < PIECES) store(buf ^ 1, j + STEP, e);
+                    });
+                else
+                    compute(buf, j, part, seg, [](int) {});
+            } else if (more) {
+                store_all(buf ^ 1, j + STEP);
+            }
             if (sh.nan[buf] == j + STEP) mark_nan(j, seg);
-            if (more) store(buf ^ 1, j + STEP);
             __syncthreads();
             buf ^= 1;
         }
