@@ -653,10 +653,14 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
  *   lse    [tokens, heads] fp32 or NULL: the logarithm of the sum of the
  *          exponentials of a row's scores
  * A row that sees nothing gets zeros and lse = -inf.  Keys that raise
- * FP4_FLAG_CACHE_INDEX are not seen.  Scores, their maxima and sums and the output
- * sums are fp32; bf16 queries use products of bf16 operands (cache values are
- * exact in bf16; probabilities are rounded to bf16), fp32 queries products
- * split over several bf16 operands, to fp32 precision.
+ * FP4_FLAG_CACHE_INDEX are not seen.  A NaN key makes the rows that see it NaN, a
+ * NaN value its dimension of the rows that see it; neither reaches other rows.
+ * Scores, their maxima and sums and the output sums are fp32.  Keys are exact in
+ * bf16; values are exact in fp16 relative to the largest value scale among a
+ * workgroup's pages, down to pages 2^-21 of it; probabilities are rounded to
+ * fp16 (relative 2^-11).  fp32 queries and their probabilities are split over
+ * several such operands, to fp32 precision.  Scale bytes above 246 can stand for
+ * values beyond fp32: what such values give is unspecified.
  *   workspace  fp4_kv_attention_workspace_bytes(...) bytes of scratch, 16-byte
  *          aligned (NULL when that is 0); calls that share one must be ordered
  * How the keys are split over workgroups depends on the arguments given here

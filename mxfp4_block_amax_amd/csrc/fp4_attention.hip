@@ -16,8 +16,8 @@
 // or more, so what is lost below fp16's range is under 2^-32 of it), for fp32
 // queries two fp16 terms (22 bits).  Values are E4M3(c) 2^(e - E + 6) with E
 // the largest scale exponent among the workgroup's pages: at most 28672, and
-// exact for pages within 2^-12 of the largest.  The sums take 2^(E - 6) back
-// at the end.
+// exact (fp16's subnormals are multiplied as they are) for pages down to 2^-21
+// of the largest.  The sums take 2^(E - 6) back at the end.
 #include <algorithm>
 #include <type_traits>
 
@@ -774,7 +774,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
             const int at = (8 * (i / 4) + (i & 3)) * D;  // keys 4 h + 0..3, 8 + 4 h + 0..3
 #pragma unroll
             for (int w = 0; w < W4; ++w) vr[w][i] = ((const uint32_t *)(vp + at + 128 * w))[r];
-            if (W2) vr[W4][i] = ((const uint16_t *)(vp + at + 128 * W4))[r];
+            if constexpr (W2 > 0) vr[W4][i] = ((const uint16_t *)(vp + at + 128 * W4))[r];
         }
         any_nan = 0;
         if (special || j < tile_first || j + STEP - 1 > tile_last) {
@@ -1137,15 +1137,17 @@ size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, 
 }
 
 template <int D>
-static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, const Plan &P,
+static hipError_t launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, const Plan &P,
                        bool bf16, int32_t *status, hipStream_t s) {
     const dim3 grid((uint32_t)P.items, C.heads * P.sub, P.splits);
     if (P.wide) {
         void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) = attention_wide_kernel<D, 4>;
         if constexpr (D <= 128)
             if (P.wide == 8) kernel = attention_wide_kernel<D, 8>;
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)(P.items * C.heads * P.sub * P.splits)),
-                           dim3(P.wide * WAVE), 0, s, C, B, A, status);
+        const int64_t groups = P.items * C.heads * P.sub * P.splits;
+        if (groups * P.wide * WAVE > UINT32_MAX) return hipErrorInvalidConfiguration;
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)groups), dim3(P.wide * WAVE), 0, s, C, B, A,
+                           status);
     } else {
         constexpr int MANY = D == 64 ? 16 : 8;
         void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) =
@@ -1155,12 +1157,10 @@ static void launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, co
                                  : attention_narrow_kernel<D, true, MANY>);
         hipLaunchKernelGGL(kernel, grid, dim3(P.waves * WAVE), 0, s, C, B, A, status);
     }
-    if (P.splits <= 1) return;
-    const dim3 join((uint32_t)B.tokens, A.heads);
-    if (bf16)
-        hipLaunchKernelGGL((attention_join_kernel<D, false>), join, dim3(JOIN_WG), 0, s, C, B, A);
-    else
-        hipLaunchKernelGGL((attention_join_kernel<D, true>), join, dim3(JOIN_WG), 0, s, C, B, A);
+    if (P.splits > 1)
+        hipLaunchKernelGGL((bf16 ? attention_join_kernel<D, false> : attention_join_kernel<D, true>),
+                           dim3((uint32_t)B.tokens, A.heads), dim3(JOIN_WG), 0, s, C, B, A);
+    return hipGetLastError();
 }
 
 hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, int64_t q_token,
@@ -1178,12 +1178,11 @@ hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, i
     A.scale2 = (scale < 0.0f ? -scale : scale) * kLog2e;
     A.q_sign = scale < 0.0f ? (bf16 ? 0x80008000u : 0x80000000u) : 0u;
     switch (C.dim) {
-        case 64: launch_dim<64>(C, B, A, P, bf16, status, s); break;
-        case 128: launch_dim<128>(C, B, A, P, bf16, status, s); break;
-        case 192: launch_dim<192>(C, B, A, P, bf16, status, s); break;
-        default: launch_dim<256>(C, B, A, P, bf16, status, s); break;
+        case 64: return launch_dim<64>(C, B, A, P, bf16, status, s);
+        case 128: return launch_dim<128>(C, B, A, P, bf16, status, s);
+        case 192: return launch_dim<192>(C, B, A, P, bf16, status, s);
+        default: return launch_dim<256>(C, B, A, P, bf16, status, s);
     }
-    return hipGetLastError();
 }
 
 }  // namespace fp4dev

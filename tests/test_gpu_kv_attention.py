@@ -179,6 +179,24 @@ def test_extreme_scales():
     assert (np.abs(got.double().cpu().numpy() - want) <= bound + 41 * 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("new,dtype", [(1, "bf16"), (1, "fp32"), (40, "bf16")])
+@pytest.mark.parametrize("apart", [1, 12, 21])
+def test_pages_of_far_apart_scales(new, dtype, apart):
+    """Values 2^-apart of another page's, which nothing weighs: as exact as ever."""
+    cu, lengths, table, pages = _kv.layout([new], [32], 16)
+    ref = _kv.Cache(pages, 1, 16, 64)
+    g = np.random.default_rng(0)
+    k, v = (g.standard_normal((32 + new, 1, 64)) for _ in range(2))
+    k[:16, :, 0], k[16:, :, 0] = -25, 25
+    v[16:] *= 2.0 ** -apart
+    ref.write((k, v), [0, 32 + new], [32 + new], table)
+    q = queries(new, 4, 64, dtype, 12) * 0.25
+    q[:, :, 0] = 12
+    announce(f"kv attention, pages 2^-{apart} apart, {new} new, {dtype}")
+    # the large page's probabilities are below 2^-100: not a part of any bound
+    check(ref, ref.device(fp4), q, cu, lengths, table)
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_keys_out_of_bounds(new):
     """A page id the cache does not have: flagged, its keys are not seen."""
