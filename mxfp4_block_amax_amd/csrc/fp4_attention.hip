@@ -29,6 +29,7 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
@@ -87,16 +88,16 @@ struct Parts {
 
 // x as N terms of a narrower type: each the nearest to what the ones before
 // left, an exact difference.
-template <typename V, int N>
-__device__ __forceinline__ Parts<V, N> split_parts(const float (&x)[8]) {
+template <typename V, int N, int COUNT>
+__device__ __forceinline__ Parts<V, N> split_parts(const float (&x)[COUNT]) {
     Parts<V, N> r;
-    float rest[8];
+    float rest[COUNT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rest[i] = x[i];
+    for (int i = 0; i < COUNT; ++i) rest[i] = x[i];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < COUNT; ++i) {
             r.p[k][i] = rest[i];
             if (k + 1 < N) rest[i] = rest[i] - (float)r.p[k][i];
         }
@@ -120,6 +121,9 @@ __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 }
 __device__ __forceinline__ f32x4_t mfma16(f16x8_t a, f16x8_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(f16x4_t a, f16x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, c, 0, 0, 0);
 }
 
 // The converter's scale operand for a value page of scale byte `byte` where
@@ -164,11 +168,18 @@ __device__ __forceinline__ VBytes<D> load_v(const uint8_t *p) {
     return r;
 }
 
-// The codes of one step (32 keys): a lane's keys and values.
+// 16-key halves of a wave's step: two, or one where a step of more dimensions
+// would leave no registers to load the next one into (24 sequences x 5 tokens
+// over 1024 keys of 256 dimensions, the values of 32 keys loaded as they are
+// needed: 33 us, against the figure below).
+template <int D>
+constexpr int kHalves = D <= 128 ? 2 : 1;
+
+// The codes of one step: a lane's keys and values.
 template <int D>
 struct Step {
-    uint4 k[2][D / 64];  // key lane % 16 of either half, dimensions 64 c + 16 (lane / 16) ..
-    VBytes<D> v[2][4];   // keys 4 (lane / 16) + i of either half, dimensions D / 16 (lane % 16) ..
+    uint4 k[kHalves<D>][D / 64];  // key lane % 16 of a half, dimensions 64 c + 16 (lane / 16) ..
+    VBytes<D> v[kHalves<D>][4];   // keys 4 (lane / 16) + i of a half, dimensions D / 16 (lane % 16) ..
 };
 
 // Row tiles of up to 16 query rows (tokens x the query heads of one kv head):
@@ -187,11 +198,11 @@ struct Step {
 template <int D, bool F32, int WAVES>
 __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow_kernel(
     KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
-    constexpr int STEP = 32 * WAVES;  // keys of a workgroup's step
+    constexpr int HALVES = kHalves<D>, KEYS = 16 * HALVES, N = 4 * HALVES;  // keys of a wave, of a lane
+    constexpr int STEP = KEYS * WAVES;                                     // of a workgroup
+    using Values = std::conditional_t<HALVES == 2, f16x8_t, f16x4_t>;
     constexpr int CH = D / 64, NT = D / 16;
     constexpr int QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;  // terms of a query and a probability
-    // values of the next step are loaded a step ahead where registers allow
-    constexpr bool V_AHEAD = D <= 128;
     __shared__ NarrowShared<D, WAVES> sh;
     const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
     const int r = lane & 15, g = lane >> 4;
@@ -271,38 +282,39 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
     auto page_at = [&](int j) {  // of the keys from j on; clamped to the last
         return __builtin_amdgcn_readfirstlane(min(j >> C.block_shift, pages - 1));
     };
-    auto load = [&](int j, Step<D> &s, const int(&page)[2], bool keys_too, bool values_too) {
+    auto load = [&](int j, Step<D> &s, const int(&page)[HALVES]) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < HALVES; ++half) {
             const int64_t at = page_offset(C, max(page[half], 0), head) +
                                ((j + 16 * half) & (C.block - 1)) * D;
             const uint8_t *kp = C.k_codes + at, *vp = C.v_codes + at;
-            if (keys_too)
 #pragma unroll
-                for (int c = 0; c < CH; ++c) s.k[half][c] = *(const uint4 *)(kp + k_lane + 64 * c);
-            if (values_too)
+            for (int c = 0; c < CH; ++c) s.k[half][c] = *(const uint4 *)(kp + k_lane + 64 * c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s.v[half][i] = load_v<D>(vp + v_lane + i * D);
+            for (int i = 0; i < 4; ++i) s.v[half][i] = load_v<D>(vp + v_lane + i * D);
         }
     };
-    auto load_held = [&](int j, Step<D> &s, bool keys_too, bool values_too) {
-        const int page[2] = {__builtin_amdgcn_readfirstlane(sh.page[page_at(j)]),
-                             __builtin_amdgcn_readfirstlane(sh.page[page_at(j + 16)])};
-        load(j, s, page, keys_too, values_too);
+    auto load_held = [&](int j, Step<D> &s) {
+        int page[HALVES];
+#pragma unroll
+        for (int half = 0; half < HALVES; ++half)
+            page[half] = __builtin_amdgcn_readfirstlane(sh.page[page_at(j + 16 * half)]);
+        load(j, s, page);
     };
     Step<D> now, next;
     // a window may start inside its first page
     const int start = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / STEP * STEP;
-    int j = start + 32 * wave;
-    const int busy = min(max((keys - start + 31) / 32, 1), WAVES);  // waves that have a step
+    int j = start + KEYS * wave;
+    const int busy = min(max((keys - start + KEYS - 1) / KEYS, 1), WAVES);  // waves that have a step
     {
-        int page = -1, first_pages[2] = {-1, -1};
+        int page = -1, first_pages[HALVES];
         if ((int)threadIdx.x < pages) page = find_page(B, C, it.seq, b0 + threadIdx.x);
         if (j < keys) {
-            first_pages[0] = __builtin_amdgcn_readfirstlane(find_page(B, C, it.seq, b0 + page_at(j)));
-            first_pages[1] =
-                __builtin_amdgcn_readfirstlane(find_page(B, C, it.seq, b0 + page_at(j + 16)));
-            load(j, now, first_pages, true, V_AHEAD);
+#pragma unroll
+            for (int half = 0; half < HALVES; ++half)
+                first_pages[half] = __builtin_amdgcn_readfirstlane(
+                    find_page(B, C, it.seq, b0 + page_at(j + 16 * half)));
+            load(j, now, first_pages);
         }
         uint32_t v_top = 0;
         auto hold = [&](int i, int page) {
@@ -326,13 +338,14 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
     float m = -__builtin_inff(), l = 0.0f;
 
     auto compute = [&](int j, Step<D> &st) {
-        f32x4_t s[2];
-        float vs[2];
-        bool held[2];
+        f32x4_t s[HALVES];
+        float vs[HALVES];
+        bool held[HALVES], all_held = true;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < HALVES; ++half) {
             const int at = page_at(j + 16 * half);
             held[half] = sh.page[at] >= 0;
+            all_held = all_held && held[half];
             const float ks = e8m0_operand(__builtin_amdgcn_readfirstlane(sh.k_scale[at]));
             vs[half] = v_operand(__builtin_amdgcn_readfirstlane(sh.v_scale[at]), v_top);
             s[half] = f32x4_t{0, 0, 0, 0};
@@ -347,17 +360,17 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
                 }
             }
         }
-        float x[8];  // base-2 scores: keys 4 g + i, then 16 + 4 g + i
+        float x[N];  // base-2 scores: keys 4 g + i, then 16 + 4 g + i
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i & 3] * A.scale2;
+        for (int i = 0; i < N; ++i) x[i] = s[i / 4][i & 3] * A.scale2;
         // a step that some row does not see whole
-        const bool clean = j >= first_r && j + 31 <= last_r;
-        const bool edge = __ballot(!clean) != 0 || !held[0] || !held[1];
+        const bool clean = j >= first_r && j + KEYS - 1 <= last_r;
+        const bool edge = __ballot(!clean) != 0 || !all_held;
         bool fix = false;
         if (edge) {
-            const int top = min(keys, j + 32);
+            const int top = min(keys, j + KEYS);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < N; ++i) {
                 const int key = j + 16 * (i / 4) + 4 * g + (i & 3);
                 if (key < first_r || key > last_r || !held[i / 4]) x[i] = -__builtin_inff();
                 // values nothing sees are zeros, whatever the page holds there
@@ -368,7 +381,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
             // NaN values that only some rows see
             uint32_t nan = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     uint32_t &w = st.v[i / 4][i & 3].w[c];
@@ -380,7 +393,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
         }
         float top = x[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i]);
+        for (int i = 1; i < N; ++i) top = __builtin_fmaxf(top, x[i]);
         if (__ballot(top > m + kRaiseAbove) != 0) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 16, WAVE));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32, WAVE));
@@ -392,38 +405,38 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
             for (int n = 0; n < NT; ++n) o[n] *= keep;
         }
         const float ref = m == -__builtin_inff() ? 0.0f : m;
-        float p[8];
+        float p[N];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < N; ++i) {
             p[i] = __builtin_amdgcn_exp2f(x[i] - ref);
             l += p[i];
         }
-        const Parts<f16x8_t, PP> pb = split_parts<f16x8_t, PP>(p);
+        const Parts<Values, PP> pb = split_parts<Values, PP>(p);
         // values: tile n has dimensions NT row + n; words of two keys interleaved
-        auto codes_of = [&](auto &&word, int n, uint32_t(&w)[4]) {
-            // bytes of dimension n, keys 0..7, two to each half word
+        auto codes_of = [&](auto &&word, int n, uint32_t(&w)[N / 2]) {
+            // bytes of dimension n, a lane's keys, two to each half word
             const int c = n / 4;
             const uint32_t sel = (n & 2) ? 0x07030602u : 0x05010400u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < N / 2; ++k)
                 w[k] = __builtin_amdgcn_perm(word(2 * k + 1, c), word(2 * k, c), sel);
         };
-        auto pair = [&](const uint32_t(&w)[4], bool hi, float s0, float s1) {
-            f16x2_t t[4];
+        auto pair = [&](const uint32_t(&w)[N / 2], bool hi, const float(&scale)[HALVES]) {
+            f16x2_t t[N / 2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                t[k] = hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k], k < 2 ? s0 : s1, true)
-                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k], k < 2 ? s0 : s1, false);
-            f16x8_t v;
+            for (int k = 0; k < N / 2; ++k)
+                t[k] = hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k], scale[k / 2], true)
+                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[k], scale[k / 2], false);
+            Values v;
             __builtin_memcpy(&v, t, sizeof(v));
             return v;
         };
         if (!fix) {
 #pragma unroll
             for (int n = 0; n < NT; n += 2) {
-                uint32_t w[4];
+                uint32_t w[N / 2];
                 codes_of([&](int i, int c) { return st.v[i / 4][i & 3].w[c]; }, n, w);
-                const f16x8_t va = pair(w, false, vs[0], vs[1]), vb = pair(w, true, vs[0], vs[1]);
+                const Values va = pair(w, false, vs), vb = pair(w, true, vs);
 #pragma unroll
                 for (int k = PP - 1; k >= 0; --k) {
                     o[n] = mfma16(va, pb.p[k], o[n]);
@@ -433,32 +446,36 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
         } else {
             // The sums without the NaN values, then NaN where a row sees one:
             // a product of where they are with who sees them counts it.
-            float see[8];
+            float see[N];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) see[i] = x[i] == -__builtin_inff() ? 0.0f : 1.0f;
-            const f16x8_t sb = split_parts<f16x8_t, 1>(see).p[0];
-            const float s0 = f2u(vs[0]) == 0x7F800000u ? 1.0f : vs[0];
-            const float s1 = f2u(vs[1]) == 0x7F800000u ? 1.0f : vs[1];
+            for (int i = 0; i < N; ++i) see[i] = x[i] == -__builtin_inff() ? 0.0f : 1.0f;
+            const Values sb = split_parts<Values, 1>(see).p[0];
+            float finite[HALVES], one[HALVES];  // scales: of values that are not NaN; of marks
+#pragma unroll
+            for (int half = 0; half < HALVES; ++half) {
+                finite[half] = f2u(vs[half]) == 0x7F800000u ? 1.0f : vs[half];
+                one[half] = 1.0f;
+            }
             auto nans = [&](int i, int c) {  // 0x80 in the bytes that are NaN
                 return ((st.v[i / 4][i & 3].w[c] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
             };
 #pragma unroll
             for (int n = 0; n < NT; n += 2) {
-                uint32_t w[4], z[4];
+                uint32_t w[N / 2], z[N / 2];
                 codes_of([&](int i, int c) {
                     const uint32_t b = nans(i, c);
                     return st.v[i / 4][i & 3].w[c] & ~((b >> 7) * 0xFFu);
                 }, n, w);
                 codes_of([&](int i, int c) { return (nans(i, c) >> 7) * 0x38u; }, n, z);
-                const f16x8_t va = pair(w, false, s0, s1), vb = pair(w, true, s0, s1);
+                const Values va = pair(w, false, finite), vb = pair(w, true, finite);
 #pragma unroll
                 for (int k = PP - 1; k >= 0; --k) {
                     o[n] = mfma16(va, pb.p[k], o[n]);
                     o[n + 1] = mfma16(vb, pb.p[k], o[n + 1]);
                 }
                 const f32x4_t zero = {0, 0, 0, 0};
-                const f32x4_t ca = mfma16(pair(z, false, 1.0f, 1.0f), sb, zero);
-                const f32x4_t cb = mfma16(pair(z, true, 1.0f, 1.0f), sb, zero);
+                const f32x4_t ca = mfma16(pair(z, false, one), sb, zero);
+                const f32x4_t cb = mfma16(pair(z, true, one), sb, zero);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (ca[i] > 0.0f) o[n][i] = __builtin_nanf("");
@@ -470,17 +487,9 @@ __global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow
 
     while (j < keys) {
         const int after = j + STEP;
-        if (!V_AHEAD) load_held(j, now, false, true);
-        if (after < keys) load_held(after, next, true, V_AHEAD);
+        if (after < keys) load_held(after, next);
         compute(j, now);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) now.k[half][c] = next.k[half][c];
-            if (V_AHEAD)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) now.v[half][i] = next.v[half][i];
-        }
+        now = next;
         j = after;
     }
 
