@@ -175,6 +175,13 @@ __device__ __forceinline__ VBytes<D> load_v(const uint8_t *p) {
 template <int D>
 constexpr int kHalves = D <= 128 ? 2 : 1;
 
+// Waves of a SIMD, by registers, and waves of a workgroup that has a CU for
+// itself.  The three terms of an fp32 query of 256 dimensions take 96 registers.
+template <int D, bool F32>
+constexpr int kNarrowOccupancy = D == 64 ? 4 : F32 && D == 256 ? 1 : 2;
+template <int D, bool F32>
+constexpr int kNarrowMany = 4 * kNarrowOccupancy<D, F32>;
+
 // The codes of one step: a lane's keys and values.
 template <int D>
 struct Step {
@@ -196,7 +203,7 @@ struct Step {
 // transposes them by byte permutes.  Nothing of keys or values goes through
 // LDS: each byte is used by one lane.
 template <int D, bool F32, int WAVES>
-__global__ __launch_bounds__(WAVES *WAVE, D == 64 ? 4 : 2) void attention_narrow_kernel(
+__global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void attention_narrow_kernel(
     KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
     constexpr int HALVES = kHalves<D>, KEYS = 16 * HALVES, N = 4 * HALVES;  // keys of a wave, of a lane
     constexpr int STEP = KEYS * WAVES;                                     // of a workgroup
@@ -1117,8 +1124,8 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     } else {
         // few tiles: workgroups of 8 waves, one a CU (of 16 where 64 dimensions
         // take half the registers); else of 4, two a CU
-        P.waves = tiles > CUS ? 4 : C.dim == 64 ? 16 : 8;
-        const int64_t slots = P.waves > 4 ? CUS : 2 * CUS;
+        P.waves = tiles > CUS || (!bf16 && C.dim == 256) ? 4 : C.dim == 64 ? 16 : 8;
+        const int64_t slots = tiles > CUS && (bf16 || C.dim < 256) ? 2 * CUS : CUS;
         const int64_t want = tiles <= slots ? slots / tiles : (3 * slots + tiles - 1) / tiles;
         keys = (extent + want - 1) / want;
         if (extent <= 6 * 32 * P.waves) keys = extent;
@@ -1158,12 +1165,11 @@ static hipError_t launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs 
         hipLaunchKernelGGL(kernel, dim3((uint32_t)groups), dim3(P.wide * WAVE), 0, s, C, B, A,
                            status);
     } else {
-        constexpr int MANY = D == 64 ? 16 : 8;
         void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) =
             bf16 ? (P.waves == 4 ? attention_narrow_kernel<D, false, 4>
-                                 : attention_narrow_kernel<D, false, MANY>)
+                                 : attention_narrow_kernel<D, false, kNarrowMany<D, false>>)
                  : (P.waves == 4 ? attention_narrow_kernel<D, true, 4>
-                                 : attention_narrow_kernel<D, true, MANY>);
+                                 : attention_narrow_kernel<D, true, kNarrowMany<D, true>>);
         hipLaunchKernelGGL(kernel, grid, dim3(P.waves * WAVE), 0, s, C, B, A, status);
     }
     if (P.splits > 1)
