@@ -171,7 +171,7 @@ __device__ __forceinline__ VBytes<D> load_v(const uint8_t *p) {
 // 16-key halves of a wave's step: two, or one where a step of more dimensions
 // would leave no registers to load the next one into (24 sequences x 5 tokens
 // over 1024 keys of 256 dimensions, the values of 32 keys loaded as they are
-// needed: 33 us, against the figure below).
+// needed: 33 us; with halves 25).
 template <int D>
 constexpr int kHalves = D <= 128 ? 2 : 1;
 
@@ -1102,7 +1102,12 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     Plan P;
     const int group = heads / C.heads;
     const int64_t per = (B.tokens + B.seqs - 1) / B.seqs;  // new tokens of a sequence, on average
-    // FORCE
+    // Which kernel, by the rows a sequence has for one kv head (8 query heads for
+    // each of 8 kv heads, 8 sequences, narrow against wide): 32 rows 51 and 42 us,
+    // 64 rows 73 and 50.  Of 256 dimensions: 20 rows 38 and 78, 40 rows 76 and 77,
+    // 120 rows 160 and 87.  Tiles of 256 rows once there are two for each CU (4
+    // chunks of 1024 tokens: 984 us with tiles of 128, 922; 8 of 64 tokens, one
+    // tile for each four CUs: 130, 187).  fp32 queries have no wide kernel.
     P.wide = 0;
     if (bf16 && per * group > (C.dim <= 128 ? 24 : 48))
         P.wide = C.dim <= 128 && per * group >= 256 && B.tokens * heads >= 2 * CUS * 256 ? 8 : 4;
@@ -1123,7 +1128,11 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
         keys = (keys + 255) / 256 * 256;  // whole pages and steps
     } else {
         // few tiles: workgroups of 8 waves, one a CU (of 16 where 64 dimensions
-        // take half the registers); else of 4, two a CU
+        // take half the registers); else of 4, two a CU.  Many tiles are split until
+        // three workgroups wait for each place: sequences differ in length.  Splits
+        // are as long as that leaves them, up to 16384 keys (64 sequences x 20000
+        // keys of 256 dimensions: 494 us; up to 8192 514, up to 4096 539); six steps
+        // of a workgroup are not split.
         P.waves = tiles > CUS || (!bf16 && C.dim == 256) ? 4 : C.dim == 64 ? 16 : 8;
         const int64_t slots = tiles > CUS && (bf16 || C.dim < 256) ? 2 * CUS : CUS;
         const int64_t want = tiles <= slots ? slots / tiles : (3 * slots + tiles - 1) / tiles;
