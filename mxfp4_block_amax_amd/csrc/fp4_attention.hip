@@ -770,14 +770,20 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
     const int vt = threadIdx.x >> 6;  // this thread's values: keys of group vt, half h, lane r
     const int slots = C.block - 1;
     bool special = false;
+    // key and chunk of it that this thread's load i is
+    auto key_of = [&](int i) {
+        return WG % KC == 0 ? (int)threadIdx.x / KC + i * (WG / KC) : ((int)threadIdx.x + i * WG) / KC;
+    };
+    auto chunk_of = [&](int i) {
+        return WG % KC == 0 ? (int)threadIdx.x % KC : ((int)threadIdx.x + i * WG) % KC;
+    };
     auto load = [&](int j, int seg) {
 #pragma unroll
         for (int i = 0; i < KL; ++i) {
-            const int c = threadIdx.x + i * WG;
-            const int key = c / KC;
+            const int key = key_of(i);
             const int page = (j - seg + key) >> C.block_shift;
             const uint8_t *p = C.k_codes + sh.offset[page] +
-                               (uint32_t)(((j + key) & slots) * D + 16 * (c - key * KC));
+                               (uint32_t)(((j + key) & slots) * D + 16 * chunk_of(i));
             k_scale[i] = sh.k_operand[page];
             kr[i] = *(const u32x4_t *)p;
         }
@@ -793,26 +799,28 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
             if constexpr (W2 > 0) vr[W4][i] = ((const uint16_t *)(vp + at + 128 * W4))[r];
         }
         any_nan = 0;
-        if (special || j < tile_first || j + STEP - 1 > tile_last) {
-            // Values nothing sees are zeros, whatever the page holds there.  NaN
-            // values of a step that not every row sees whole would reach rows
-            // that do not see them (0 times NaN): they are taken out here and
-            // marked afterwards.  Where every row sees them the sums do it by
-            // themselves.
-            const uint32_t bad = sh.bad[page];
-            const uint32_t every = bad & PAGE_NAN ? 0x01010101u : 0u;
+    };
+    // a step some of whose keys some row does not see
+    auto edge = [&](int j) { return special || j < tile_first || j + STEP - 1 > tile_last; };
+    auto clean = [&](int j, int seg) {
+        // Values nothing sees are zeros, whatever the page holds there.  NaN
+        // values of a step that not every row sees whole would reach rows
+        // that do not see them (0 times NaN): they are taken out here and
+        // marked afterwards.  Where every row sees them the sums do it by
+        // themselves.
+        const uint32_t bad = sh.bad[(j - seg + 16 * vt) >> C.block_shift];
+        const uint32_t every = bad & PAGE_NAN ? 0x01010101u : 0u;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int key = j + 16 * vt + 4 * h + 8 * (i / 4) + (i & 3);
-                const bool none = key >= keys || (bad & PAGE_MISSING);
+        for (int i = 0; i < 8; ++i) {
+            const int key = j + 16 * vt + 4 * h + 8 * (i / 4) + (i & 3);
+            const bool none = key >= keys || (bad & PAGE_MISSING);
 #pragma unroll
-                for (int w = 0; w < W4 + W2; ++w) {
-                    const uint32_t x = vr[w][i];
-                    uint32_t z = ((((x & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | every;
-                    if (none) z = 0;
-                    vr[w][i] = none ? 0u : x & ~(z * 0xFFu);
-                    any_nan |= z;
-                }
+            for (int w = 0; w < W4 + W2; ++w) {
+                const uint32_t x = vr[w][i];
+                uint32_t z = ((((x & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) | every;
+                if (none) z = 0;
+                vr[w][i] = none ? 0u : x & ~(z * 0xFFu);
+                any_nan |= z;
             }
         }
     };
@@ -821,9 +829,8 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
     auto store = [&](int buf, int j, int piece) {
         if (piece < 2 * KL) {  // half a chunk of a key
             const int i = piece / 2, e = piece & 1;
-            const int c = threadIdx.x + i * WG;
-            const int key = c / KC;
-            sh.k[buf][key * 2 * KC + ((2 * (c - key * KC) + e) ^ key_swizzle<D>(key))] =
+            const int at = ((2 * chunk_of(i)) ^ key_swizzle<D>(key_of(i))) ^ e;
+            sh.k[buf][key_of(i) * 2 * KC + at] =
                 __builtin_bit_cast(u32x4_t, e ? widen_codes(kr[i].z, kr[i].w, k_scale[i])
                                               : widen_codes(kr[i].x, kr[i].y, k_scale[i]));
             return;
@@ -862,12 +869,20 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
 #pragma unroll
         for (int u = 0; u < 2; ++u) s[u] = f32x16_t{};
         __builtin_amdgcn_s_setprio(1);
-        const u32x4_t *kp = &sh.k[buf][64 * part * 2 * KC];
         // product i: dimensions 16 (i / 2) .., keys 32 (i & 1) ..; its keys are read
-        // AHEAD products before it
+        // AHEAD products before it.  Their addresses differ in the swizzled bits:
+        // computed here, as all of them over the loop take more registers than
+        // there are (256 dimensions).
         constexpr int AHEAD = 6;
+        constexpr int SPAN = D % 128 == 0 ? 8 : 4;  // products of one row whose addresses differ
+        uint32_t k_bits = (uint32_t)(h ^ key_swizzle<D>(r)) * 16;
+        const uint32_t k_row = (uint32_t)((buf * STEP + 64 * part + r) * 2 * D);
+        asm volatile("" : "+v"(k_bits));
         auto key = [&](int i) {
-            return kp[(32 * (i & 1) + r) * 2 * KC + ((2 * (i / 2) + h) ^ key_swizzle<D>(r))];
+            const int c = i / 2;
+            const uint32_t at = (k_bits ^ (uint32_t)(c % SPAN * 32)) + k_row;
+            return *(const u32x4_t *)((const char *)sh.k + at + c / SPAN * SPAN * 32 +
+                                      (i & 1) * 32 * 2 * D);
         };
         u32x4_t kf[AHEAD];
 #pragma unroll
@@ -1020,16 +1035,20 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         __syncthreads();
         int buf = 0, j = max(seg, start);
         load(j, seg);
+        if (edge(j)) clean(j, seg);
         store_all(0, j);
+        if (j + STEP < seg_end) load(j + STEP, seg);
         __syncthreads();
         for (; j < seg_end; j += STEP) {
-            const bool more = j + STEP < seg_end;
-            if (more) load(j + STEP, seg);
+            // The next step's codes are in registers.  They are stored between the
+            // products of the last part; then the step after it is on its way, and
+            // has until the next step's last part.
+            const bool more = j + STEP < seg_end, load_more = j + 2 * STEP < seg_end;
+            if (more && edge(j + STEP)) clean(j + STEP, seg);
 #pragma unroll 1
             for (int part = 0; part < STEP / 64 - 1; ++part)
                 if (j + 64 * part <= wave_last && j + 64 * part + 63 >= wave_first)
                     compute(buf, j, part, seg, [](int) {});
-            // the next step is stored between the products of the last part
             const int part = STEP / 64 - 1;
             if (j + 64 * part <= wave_last && j + 64 * part + 63 >= wave_first) {
                 if (more)
@@ -1038,11 +1057,14 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
 #pragma unroll
                         for (int e = EACH * i; e < EACH * (i + 1); ++e)
                             if (e < PIECES) store(buf ^ 1, j + STEP, e);
+                        if (i == (PIECES + EACH - 1) / EACH - 1 && load_more)
+                            load(j + 2 * STEP, seg);
                     });
                 else
                     compute(buf, j, part, seg, [](int) {});
             } else if (more) {
                 store_all(buf ^ 1, j + STEP);
+                if (load_more) load(j + 2 * STEP, seg);
             }
             if (sh.nan[buf] == j + STEP) mark_nan(j, seg);
             __syncthreads();
