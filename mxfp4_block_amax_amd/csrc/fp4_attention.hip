@@ -1118,7 +1118,6 @@ struct Plan {
 };
 
 constexpr int CUS = 256;
-constexpr int WIDE_MIN_KEYS = 1024;
 
 Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool bf16) {
     Plan P;
@@ -1144,9 +1143,18 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     int64_t keys;
     P.waves = 0;
     if (P.wide) {
-        const int64_t slots = P.wide == 8 ? CUS : 2 * CUS;
-        const int64_t want = std::max<int64_t>(1, slots / tiles);
-        keys = std::max<int64_t>((extent + want - 1) / want, WIDE_MIN_KEYS);
+        auto split = [&](int64_t slots, int64_t least) {
+            const int64_t want = std::max<int64_t>(1, slots / tiles);
+            return std::max<int64_t>((extent + want - 1) / want, least);
+        };
+        // One workgroup a CU down to splits of 512 keys (3 chunks of 116 tokens, 8
+        // heads, 1212 keys: 31 us; not below 1024 39, nor below 256 29, but 2 of 285
+        // tokens then 30 against 25).  Two a CU, where they fit, down to 1024 (8 x 4
+        // tokens x 4096 keys: 41 us, of 512 keys 47).  Those of four waves fit to 128
+        // dimensions (4 chunks of 100 tokens of 192 dimensions over 4096 keys, split
+        // as if they fitted: 109 us, 82).
+        keys = split(CUS, 512);
+        if (P.wide == 4 && C.dim <= 128) keys = std::min(keys, split(2 * CUS, 1024));
         keys = (keys + 255) / 256 * 256;  // whole pages and steps
     } else {
         // few tiles: workgroups of 8 waves, one a CU (of 16 where 64 dimensions
