@@ -133,6 +133,11 @@ __device__ __forceinline__ float v_operand(uint32_t byte, uint32_t top) {
     return u2f(byte == 255u ? 255u << 23 : (uint32_t)max(e, 0) << 23);
 }
 
+// Launch order: heads, then row tiles, then splits, so that the tiles that read
+// the same keys are near each other in time and, for 8 heads, on the same XCD and
+// its L2 (8 sequences x 30 tokens over 4096 keys of 8 heads, 256 dimensions: 99
+// us, row tiles first 215).  More row tiles than a grid's y go first.
+constexpr int NARROW_GRID_Y = 65535;
 constexpr int NARROW_PAGES = 256;  // pages under a workgroup's keys, at most
 
 template <int D, int WAVES>
@@ -176,9 +181,11 @@ template <int D>
 constexpr int kHalves = D <= 128 ? 2 : 1;
 
 // Waves of a SIMD, by registers, and waves of a workgroup that has a CU for
-// itself.  The three terms of an fp32 query of 256 dimensions take 96 registers.
+// itself.  The three terms of an fp32 query of 256 dimensions take 96 registers;
+// those of 64 spill with four waves (16 sequences x 2048 keys, 16 heads: 31 us,
+// with three 25).
 template <int D, bool F32>
-constexpr int kNarrowOccupancy = D == 64 ? 4 : F32 && D == 256 ? 1 : 2;
+constexpr int kNarrowOccupancy = D == 64 ? (F32 ? 3 : 4) : F32 && D == 256 ? 1 : 2;
 template <int D, bool F32>
 constexpr int kNarrowMany = 4 * kNarrowOccupancy<D, F32>;
 
@@ -215,13 +222,18 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
     const int r = lane & 15, g = lane >> 4;
     if (threadIdx.x == 0) sh.v_top = 0;
     __syncthreads();
-    const Item it = find_item(B, (int)blockIdx.x, A.tokens, A.tokens > 1 ? 1 : 0);
+    const bool heads_first = A.items <= NARROW_GRID_Y;
+    const int headsub = heads_first ? blockIdx.x : blockIdx.y;
+    const int item = heads_first ? blockIdx.y : blockIdx.x;
+    const Item it = A.tokens > 1 && B.seqs < TILE_SEQS
+                        ? find_tile(B, item, A.tokens, status)
+                        : find_item(B, item, A.tokens, A.tokens > 1 ? 1 : 0);
     const int row0 = it.piece * A.tokens;
     if (it.count <= 0 || row0 >= it.count) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
     }
-    const int head = blockIdx.y / A.sub, sub = blockIdx.y - head * A.sub;
+    const int head = headsub / A.sub, sub = headsub - head * A.sub;
     const int split = blockIdx.z;
     const bool none = it.seq >= B.seqs;
     Tile T;
@@ -709,7 +721,9 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
     const uint32_t rest = blockIdx.x / hs;
     const int split = rest / (uint32_t)A.items;
     const int item = A.items - 1 - (int)(rest - (uint32_t)split * A.items);
-    const Item it = find_item(B, item, A.tokens, A.tokens > 1 ? 1 : 0);
+    const Item it = A.tokens > 1 && B.seqs < TILE_SEQS
+                        ? find_tile(B, item, A.tokens, status)
+                        : find_item(B, item, A.tokens, A.tokens > 1 ? 1 : 0);
     const int row0 = it.piece * A.tokens;
     if (it.count <= 0 || row0 >= it.count) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
@@ -1123,21 +1137,27 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     Plan P;
     const int group = heads / C.heads;
     const int64_t per = (B.tokens + B.seqs - 1) / B.seqs;  // new tokens of a sequence, on average
-    // Which kernel, by the rows a sequence has for one kv head (8 query heads for
-    // each of 8 kv heads, 8 sequences, narrow against wide): 32 rows 51 and 42 us,
-    // 64 rows 73 and 50.  Of 256 dimensions: 20 rows 38 and 78, 40 rows 76 and 77,
-    // 120 rows 160 and 87.  Tiles of 256 rows once there are two for each CU (4
-    // chunks of 1024 tokens: 984 us with tiles of 128, 922; 8 of 64 tokens, one
-    // tile for each four CUs: 130, 187).  fp32 queries have no wide kernel.
+    int64_t extent = (int64_t)B.width << C.block_shift;
+    if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + per + C.block);
+    // Which kernel: narrow tiles for few rows of a sequence and kv head (narrow
+    // against wide; of 64 dimensions 96 rows 112 and 156 us, 160 rows 158 and 136;
+    // of 128 64 rows 45 and 55, 160 rows 307 and 188; of 256 56 rows 58 and 115, 120
+    // rows 191 and 144), and where a CU has up to two of them and 2048 of their keys
+    // (2 prompts of 433 tokens, 4 heads: 13 us and 21; 3 chunks of 116 tokens, 8
+    // heads, over 1212 keys: 20 and 31; but 119 tokens, 16 x 7 heads, four for each
+    // CU: 29 and 18).  Tiles of 256 rows once there are two for
+    // each CU (4 chunks of 1024 tokens: 984 us with tiles of 128, 922; 8 of 64 tokens,
+    // one tile for each four CUs: 130, 187).  fp32 queries have no wide kernel.
+    const int64_t narrow_tiles = (per * group + 15) / 16 * B.seqs * C.heads;
     P.wide = 0;
-    if (bf16 && per * group > (C.dim <= 128 ? 24 : 48))
+    if (bf16 && per * group > (C.dim == 64 ? 128 : C.dim == 128 ? 64 : 96) &&
+        (narrow_tiles > 2 * CUS || narrow_tiles * extent > 2048 * CUS))
         P.wide = C.dim <= 128 && per * group >= 256 && B.tokens * heads >= 2 * CUS * 256 ? 8 : 4;
     const int rows = P.wide ? 32 * P.wide : 16;
     P.sub = (group + rows - 1) / rows;
     P.sub_heads = (group + P.sub - 1) / P.sub;
     P.tokens = (int)std::min<int64_t>(rows / P.sub_heads, per);
     P.items = P.tokens > 1 ? item_count(B.tokens, B.seqs, P.tokens, 1) : B.tokens;
-    int64_t extent = (int64_t)B.width << C.block_shift;
     if (window > 0) extent = std::min<int64_t>(extent, (int64_t)window + P.tokens + C.block);
     const int64_t tiles = (per + P.tokens - 1) / P.tokens * B.seqs * C.heads * P.sub;
     int64_t keys;
@@ -1163,7 +1183,7 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
         // are as long as that leaves them, up to 16384 keys (64 sequences x 20000
         // keys of 256 dimensions: 494 us; up to 8192 514, up to 4096 539); six steps
         // of a workgroup are not split.
-        P.waves = tiles > CUS || (!bf16 && C.dim == 256) ? 4 : C.dim == 64 ? 16 : 8;
+        P.waves = tiles > CUS || (!bf16 && C.dim == 256) ? 4 : C.dim == 64 ? (bf16 ? 16 : 12) : 8;
         const int64_t slots = tiles > CUS && (bf16 || C.dim < 256) ? 2 * CUS : CUS;
         const int64_t want = tiles <= slots ? slots / tiles : (3 * slots + tiles - 1) / tiles;
         keys = (extent + want - 1) / want;
@@ -1194,7 +1214,6 @@ size_t attention_workspace_bytes(const KvCache &C, const KvBatch &B, int heads, 
 template <int D>
 static hipError_t launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, const Plan &P,
                        bool bf16, int32_t *status, hipStream_t s) {
-    const dim3 grid((uint32_t)P.items, C.heads * P.sub, P.splits);
     if (P.wide) {
         void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) = attention_wide_kernel<D, 4>;
         if constexpr (D <= 128)
@@ -1209,7 +1228,9 @@ static hipError_t launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs 
                                  : attention_narrow_kernel<D, false, kNarrowMany<D, false>>)
                  : (P.waves == 4 ? attention_narrow_kernel<D, true, 4>
                                  : attention_narrow_kernel<D, true, kNarrowMany<D, true>>);
-        hipLaunchKernelGGL(kernel, grid, dim3(P.waves * WAVE), 0, s, C, B, A, status);
+        const uint32_t hs = C.heads * P.sub, items = (uint32_t)P.items;
+        hipLaunchKernelGGL(kernel, (items <= NARROW_GRID_Y ? dim3(hs, items, P.splits) : dim3(items, hs, P.splits)),
+                           dim3(P.waves * WAVE), 0, s, C, B, A, status);
     }
     if (P.splits > 1)
         hipLaunchKernelGGL((bf16 ? attention_join_kernel<D, false> : attention_join_kernel<D, true>),
