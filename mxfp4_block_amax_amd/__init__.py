@@ -816,7 +816,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
     bf16, slices allowed), over the cache; scale defaults to head_dim ** -0.5.
     Returns out, or (out, lse [tokens, heads] fp32).  The work is laid out for
     sequences as long as the table is wide: pass a table (or table[:, :width])
-    no wider than the longest one needs."""
+    no wider than the longest one needs; and of the average number of new
+    tokens: long chunks and single tokens are faster in calls of their own."""
     rows = _kv_rows(q, cache, "q")
     tokens, heads, dim = q.shape
     dtype = _KV_DTYPES.get(q.dtype)
