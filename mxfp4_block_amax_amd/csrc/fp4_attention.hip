@@ -209,6 +209,11 @@ struct Step {
 // free too, so a lane loads D / 16 consecutive bytes of eight value rows and
 // transposes them by byte permutes.  Nothing of keys or values goes through
 // LDS: each byte is used by one lane.
+//
+// Long decoding is bound by HBM: 64 tokens over about 8192 keys each, 8 x 8 heads
+// of 128, read 1084 MB in 205 us (5.3 TB/s; 185 at equal lengths), one over 200001
+// 410 MB in 76 us (5.4 TB/s).  Short calls are bound by latency, some 2 us a step
+// where a CU has one workgroup: a token over 1000 keys takes 13.7 us.
 template <int D, bool F32, int WAVES>
 __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void attention_narrow_kernel(
     KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
@@ -701,9 +706,15 @@ __device__ __forceinline__ int key_swizzle(int row) {
 //
 // As above, but the waves share the keys and have 32 rows each: scores
 // S^T = K Q^T and sums out^T = V^T P^T on 32 x 32 tiles, probabilities staying
-// in their lanes.  A step of 16 WAVES keys is loaded a step ahead as codes and
-// widened once for all waves on its way into LDS, keys to bf16, values
-// transposed (eight keys of a dimension side by side) to fp16.
+// in their lanes.  A step of 16 WAVES keys is widened once for all waves on its
+// way into LDS, keys to bf16, values transposed (eight keys of a dimension side by
+// side) to fp16; its codes were loaded during the step before that.
+//
+// Bound by MFMA and vector issue of the two waves of a SIMD, and by the power they
+// draw: 4 chunks of about 1024 tokens over 6000, 8 x 8 heads of 128, 898 us (937
+// TFLOP/s, MFMA busy for 42% of the cycles at a clock that falls to about 1.9
+// GHz); a prompt of 4096, 8 x 4 heads, 149 us (922 TFLOP/s).  With the codes of a
+// step loaded and stored in the same step: 930 and 155.
 template <int D, int WAVES>
 __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_kernel(
     KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
