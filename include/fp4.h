@@ -656,11 +656,14 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
  * FP4_FLAG_CACHE_INDEX are not seen.  A NaN key makes the rows that see it NaN, a
  * NaN value its dimension of the rows that see it; neither reaches other rows.
  * Scores, their maxima and sums and the output sums are fp32.  Keys are exact in
- * bf16; values are exact in fp16 relative to the largest value scale among a
- * workgroup's pages, down to pages 2^-21 of it; probabilities are rounded to
- * fp16 (relative 2^-11).  fp32 queries and their probabilities are split over
- * several such operands, to fp32 precision.  Scale bytes above 246 can stand for
- * values beyond fp32: what such values give is unspecified.
+ * bf16 and values in fp16; probabilities, times their value page's scale, are
+ * rounded to fp16 (relative 2^-11; what is below 2^-31 of a row's largest loses
+ * bits, to none in the end).  fp32 queries and their probabilities are split over
+ * several such operands, to fp32 precision but for that end.  So a row's result
+ * is that of the keys it sees, whatever the scales of other pages, with one
+ * limit: values of pages below 2^-101 of the largest value scale among a
+ * workgroup's keys lose bits.  Scale bytes above 246 can stand for values beyond
+ * fp32: what such values give is unspecified.
  *   workspace  fp4_kv_attention_workspace_bytes(...) bytes of scratch, 16-byte
  *          aligned (NULL when that is 0); calls that share one must be ordered
  * How the keys are split over workgroups depends on the arguments given here

@@ -4,9 +4,14 @@
 //   out_r = sum_j exp(S_rj) v_j / sum_j exp(S_rj).
 //
 // One pass over the keys with a running reference m_r and sum per row, both
-// fp32: probabilities are p = 2^(S log2 e - m).  The reference is raised (and
-// the sums rescaled) only when some score passes it by more than 15, to 7 below
-// that score: most steps then need no rescaling and no exchange between lanes.
+// fp32: weights are p = 2^(S log2 e - d - m), d the exponent by which the scale
+// of the key's value page is below E, the largest among the workgroup's pages.
+// So a weight carries its page's scale: what a row's sums lose is relative to
+// its own largest weight, not to pages that other rows see.  Pages of one scale
+// have d = 0.  The reference is raised (and the sums rescaled) only when some
+// weight passes it by more than 2^15, to 2^-7 of that weight: most steps then need
+// no rescaling and no exchange between lanes.  The sum of the probabilities takes
+// p 2^d.  d ends at 80, which keeps that sum below 2^122; the values take the rest.
 //
 // First product, on the bf16 MFMA: keys E4M3(c) 2^e are exact in bf16 (the
 // converter applies the scale) and bf16 queries multiply as they are; fp32
@@ -14,10 +19,10 @@
 // Second product, on the fp16 MFMA: p is at most 2^15 and rounded to fp16
 // (relative 2^-11, an eighth of what bf16 would lose; a row's largest p is 2^7
 // or more, so what is lost below fp16's range is under 2^-32 of it), for fp32
-// queries two fp16 terms (22 bits).  Values are E4M3(c) 2^(e - E + 6) with E
-// the largest scale exponent among the workgroup's pages: at most 28672, and
-// exact (fp16's subnormals are multiplied as they are) for pages down to 2^-21
-// of the largest.  The sums take 2^(E - 6) back at the end.
+// queries two fp16 terms (22 bits).  Values are E4M3(c) 2^6: at most 28672, and
+// from d = 80 on down to fp16's end: exact (its subnormals are multiplied as they
+// are) for pages down to 2^-101 of the largest.  The sums take 2^(E - 6) back at
+// the end.
 #include <algorithm>
 #include <type_traits>
 
@@ -35,9 +40,10 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kRaiseAbove = 15.0f;  // a score this far over its reference raises it ..
-constexpr float kRaiseTo = 7.0f;      // .. to this far below that score
-constexpr int kVBias = 6;             // values are scaled by 2^kVBias over the largest page scale
+constexpr float kRaiseAbove = 15.0f;  // a weight this far over its reference raises it ..
+constexpr float kRaiseTo = 7.0f;      // .. to this far below that weight
+constexpr int kVBias = 6;             // values are scaled by 2^kVBias
+constexpr int kCarry = 80;            // the most of a page's distance from E that weights carry
 
 struct AttnArgs {
     const void *q;
@@ -126,11 +132,24 @@ __device__ __forceinline__ f32x4_t mfma16(f16x4_t a, f16x4_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, c, 0, 0, 0);
 }
 
-// The converter's scale operand for a value page of scale byte `byte` where
-// the largest is `top` (255, a NaN page, stays NaN).
+// d of a value page of scale byte `byte` where the largest is `top`, the factor
+// 2^d, and the converter's scale operand (255, a NaN page, stays NaN).
+__device__ __forceinline__ int v_below(uint32_t byte, uint32_t top) {
+    return byte == 255u ? 0 : min((int)top - (int)byte, kCarry);
+}
+__device__ __forceinline__ float v_lift(int below) {
+    return u2f((E8M0_ONE + (uint32_t)below) << 23);
+}
 __device__ __forceinline__ float v_operand(uint32_t byte, uint32_t top) {
-    const int e = (int)byte - (int)top + kVBias + (int)E8M0_ONE;
+    const int e = kVBias + (int)E8M0_ONE - max((int)top - (int)byte - kCarry, 0);
     return u2f(byte == 255u ? 255u << 23 : (uint32_t)max(e, 0) << 23);
+}
+
+// A split's reference and sum for the join: the sum's exponent goes into the
+// reference, so that products of weights and outputs stay in range.
+__device__ __forceinline__ float2 split_weight(float m, float l) {
+    const int e = __builtin_amdgcn_frexp_expf(l);
+    return make_float2(m + (float)e, __builtin_ldexpf(l, -e));
 }
 
 // Launch order: heads, then row tiles, then splits, so that the tiles that read
@@ -366,7 +385,7 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
 
     auto compute = [&](int j, Step<D> &st) {
         f32x4_t s[HALVES];
-        float vs[HALVES];
+        float vs[HALVES], below[HALVES], lift[HALVES];
         bool held[HALVES], all_held = true;
 #pragma unroll
         for (int half = 0; half < HALVES; ++half) {
@@ -374,7 +393,10 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
             held[half] = sh.page[at] >= 0;
             all_held = all_held && held[half];
             const float ks = e8m0_operand(__builtin_amdgcn_readfirstlane(sh.k_scale[at]));
-            vs[half] = v_operand(__builtin_amdgcn_readfirstlane(sh.v_scale[at]), v_top);
+            const uint32_t vb = __builtin_amdgcn_readfirstlane(sh.v_scale[at]);
+            vs[half] = v_operand(vb, v_top);
+            below[half] = (float)v_below(vb, v_top);
+            lift[half] = v_lift(v_below(vb, v_top));
             s[half] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -421,7 +443,10 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < N; ++i) top = __builtin_fmaxf(top, x[i]);
-        if (__ballot(top > m + kRaiseAbove) != 0) {
+        if (__ballot(top > m + kRaiseAbove) != 0) {  // some weight may (d is not negative)
+            top = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < N; ++i) top = __builtin_fmaxf(top, x[i] - below[i / 4]);
             top = __builtin_fmaxf(top, __shfl_xor(top, 16, WAVE));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32, WAVE));
             const float next = __builtin_fmaxf(m, top - kRaiseTo);
@@ -435,8 +460,8 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
         float p[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(x[i] - ref);
-            l += p[i];
+            p[i] = __builtin_amdgcn_exp2f(x[i] - (ref + below[i / 4]));
+            l = __builtin_fmaf(p[i], lift[i / 4], l);
         }
         const Parts<Values, PP> pb = split_parts<Values, PP>(p);
         // values: tile n has dimensions NT row + n; words of two keys interleaved
@@ -586,7 +611,7 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
         }
         if (part == 0) {
             if (!whole)
-                A.part_ml[row * A.splits + split] = make_float2(m_all, l_all);
+                A.part_ml[row * A.splits + split] = split_weight(m_all, l_all);
             else if (A.lse != nullptr)
                 A.lse[row] = l_all == 0.0f ? -__builtin_inff()
                                            : ((m_all == -__builtin_inff() ? 0.0f : m_all) +
@@ -690,6 +715,7 @@ struct WideShared {
     u32x4_t v[2][STEP * D / 8];  // fp16: [16 keys t][tile n][half h][lane m]: 8 keys of a dimension
     int64_t offset[WIDE_PAGES];        // a page's codes
     float k_operand[WIDE_PAGES], v_operand[WIDE_PAGES];
+    float2 v_below[WIDE_PAGES];        // d and 2^d
     uint8_t bad[WIDE_PAGES];           // PAGE_*
     uint32_t v_top, special;           // special: some page of the segment is bad
     int nan[2];                        // the last step (its end) with NaN values taken out
@@ -715,7 +741,11 @@ __device__ __forceinline__ int key_swizzle(int row) {
 // TFLOP/s, MFMA busy for 42% of the cycles at a clock that falls to about 1.9
 // GHz); a prompt of 4096, 8 x 4 heads, 149 us (922 TFLOP/s).  With the codes of a
 // step loaded and stored in the same step: 930 and 155.
-template <int D, int WAVES>
+//
+// PAGES is how many pages 64 keys may have, 1 (of 64 tokens and more) or 4: four
+// distances d cost the same two calls 2.3% over values that carry all of d
+// themselves, one 1%.
+template <int D, int WAVES, int PAGES>
 __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_kernel(
     KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
     constexpr int WG = WAVES * WAVE;
@@ -887,7 +917,6 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
 #pragma unroll
     for (int n = 0; n < NT; ++n) o[n] = f32x16_t{};
     float m = -__builtin_inff(), l = 0.0f;
-    uint32_t v_top = 0;
 
     // 64 keys, part `part` of the step at j0
     // `between(i)` runs after product i of the scores
@@ -947,13 +976,23 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         u32x4_t vf[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) vf[n] = vp[n * 64];
+        float2 below[PAGES];
+#pragma unroll
+        for (int t = 0; t < PAGES; ++t)
+            below[t] = sh.v_below[(j - seg + 64 / PAGES * t) >> C.block_shift];
         float top = s[0][0];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[u][i]);
-        top *= c2;
-        if (__ballot(top > m + kRaiseAbove) != 0) {
+        if (__ballot(top * c2 > m + kRaiseAbove) != 0) {  // some weight may (d is not negative)
+            top = -__builtin_inff();
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    top = __builtin_fmaxf(
+                        top, __builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -below[t * PAGES / 4].x));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32, WAVE));
             const float next = __builtin_fmaxf(m, top - kRaiseTo);
             const float keep = m == next ? 1.0f : __builtin_amdgcn_exp2f(m - next);
@@ -968,8 +1007,9 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         // has taken its own.
         float p[8];
         auto probability = [&](int t, int i) {
-            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -ref));
-            l += p[i];
+            p[i] = __builtin_amdgcn_exp2f(
+                __builtin_fmaf(s[t / 2][8 * (t & 1) + i], c2, -(ref + below[t * PAGES / 4].x)));
+            l = __builtin_fmaf(p[i], below[t * PAGES / 4].y, l);
         };
 #pragma unroll
         for (int i = 0; i < 8; ++i) probability(0, i);
@@ -1022,6 +1062,22 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         }
     };
 
+    // the largest value scale (of one segment it is found with its pages)
+    uint32_t v_top = 0;
+    if (keys > WIDE_SEGMENT) {
+        if (threadIdx.x == 0) sh.v_top = 0;
+        __syncthreads();
+        const int pages = (keys + slots) >> C.block_shift;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < pages; i += WG) {
+            const int page = find_page(B, C, it.seq, (k0 >> C.block_shift) + i);
+            const uint32_t vb = page < 0 ? 0u : C.v_scales[(int64_t)page * C.heads + head];
+            if (vb != 255u) v_top = max(v_top, vb);
+        }
+        if (v_top > 0) atomicMax(&sh.v_top, v_top);
+        __syncthreads();
+        v_top = __builtin_amdgcn_readfirstlane(sh.v_top);
+    }
     // a window may start inside its first page
     const int start = (int)max(min(T.first - k0, (int64_t)keys), (int64_t)0) / STEP * STEP;
     for (int seg = start / WIDE_SEGMENT * WIDE_SEGMENT; seg < keys; seg += WIDE_SEGMENT) {
@@ -1051,15 +1107,13 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
             if (vb > v_top) atomicMax(&sh.v_top, vb);
         }
         __syncthreads();
-        const uint32_t v_next = __builtin_amdgcn_readfirstlane(sh.v_top);
+        v_top = __builtin_amdgcn_readfirstlane(sh.v_top);
         special = __builtin_amdgcn_readfirstlane(sh.special) != 0;
-        if (v_next > v_top) {
-            const float down = e8m0_value(E8M0_ONE - min(v_next - v_top, E8M0_ONE));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) o[n] *= down;
-            v_top = v_next;
+        if (threadIdx.x < WIDE_PAGES) {
+            const int below = v_below(vb, v_top);
+            sh.v_operand[threadIdx.x] = v_operand(vb, v_top);
+            sh.v_below[threadIdx.x] = make_float2((float)below, v_lift(below));
         }
-        if (threadIdx.x < WIDE_PAGES) sh.v_operand[threadIdx.x] = v_operand(vb, v_top);
         __syncthreads();
         int buf = 0, j = max(seg, start);
         load(j, seg);
@@ -1129,7 +1183,7 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
         }
     if (h == 0) {
         if (!whole)
-            A.part_ml[to * A.splits + split] = make_float2(m, l);
+            A.part_ml[to * A.splits + split] = split_weight(m, l);
         else if (A.lse != nullptr)
             A.lse[to] = l == 0.0f ? -__builtin_inff()
                                   : ((m == -__builtin_inff() ? 0.0f : m) + __builtin_amdgcn_logf(l)) * kLn2;
@@ -1229,9 +1283,11 @@ template <int D>
 static hipError_t launch_dim(const KvCache &C, const KvBatch &B, const AttnArgs &A, const Plan &P,
                        bool bf16, int32_t *status, hipStream_t s) {
     if (P.wide) {
-        void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) = attention_wide_kernel<D, 4>;
+        void (*kernel)(KvCache, KvBatch, AttnArgs, int32_t *) =
+            C.block >= 64 ? attention_wide_kernel<D, 4, 1> : attention_wide_kernel<D, 4, 4>;
         if constexpr (D <= 128)
-            if (P.wide == 8) kernel = attention_wide_kernel<D, 8>;
+            if (P.wide == 8)
+                kernel = C.block >= 64 ? attention_wide_kernel<D, 8, 1> : attention_wide_kernel<D, 8, 4>;
         const int64_t groups = P.items * C.heads * P.sub * P.splits;
         if (groups * P.wide * WAVE > UINT32_MAX) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL(kernel, dim3((uint32_t)groups), dim3(P.wide * WAVE), 0, s, C, B, A,
