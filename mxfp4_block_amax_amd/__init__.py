@@ -758,7 +758,12 @@ def _kv_rows(x: torch.Tensor, cache: KVCache, what: str):
 
 def _kv_call(fn, cache, batch, args, check, status):
     """One cache call on the current stream; with check, its flags raise."""
-    if check and status is None:
+    if status is not None:
+        if status.dtype is not torch.int32:
+            raise TypeError("status must be an int32 tensor")
+        if status.device != cache.k_codes.device or status.numel() == 0:
+            raise ValueError("status must have an element, on the cache's device")
+    elif check:
         status = torch.zeros(1, dtype=torch.int32, device=cache.k_codes.device)
     code = fn(cache._c, batch, *args, None if status is None else status.data_ptr(),
               _raw_stream(cache._device))

@@ -1,0 +1,76 @@
+"""CPU tests of what the Python cache calls hand to the library: a recording
+stand-in for the library, host tensors in the place of device ones."""
+import pytest
+import torch
+
+import mxfp4_block_amax_amd as fp4
+
+
+class Library:
+    """Records the entry points' arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def _call(self, *args):
+        self.calls.append(args)
+        return 0
+
+    fp4_kv_cache_write = fp4_kv_cache_read = fp4_kv_attention = _call
+
+    def fp4_kv_attention_workspace_bytes(self, *args):
+        self.calls.append(args)
+        return 64
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(fp4, "_lib", lib)
+    monkeypatch.setattr(fp4, "_raw_stream", lambda device: 0)
+    return lib
+
+
+def host_cache(monkeypatch):
+    """A cache of host tensors: the constructor takes device ones."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    u8 = torch.uint8
+    return fp4.KVCache(torch.zeros(4, 2, 16, 64, dtype=u8), torch.zeros(4, 2, dtype=u8),
+                       torch.zeros(4, 2, 16, 64, dtype=u8), torch.zeros(4, 2, dtype=u8))
+
+
+@pytest.fixture
+def cache(library, monkeypatch):
+    return host_cache(monkeypatch)
+
+
+BATCH = [torch.tensor(a, dtype=torch.int32) for a in ([0, 3], [3], [[1]])]
+K = torch.zeros(3, 2, 64)
+Q = torch.zeros(3, 4, 64)
+
+
+def write(cache, **how):
+    fp4.kv_cache_write(cache, K, K, *BATCH, **how)
+
+
+def read(cache, **how):
+    fp4.kv_cache_read(cache, *BATCH, 3, **how)
+
+
+def attend(cache, **how):
+    fp4.kv_attention(Q, cache, *BATCH, **how)
+
+
+@pytest.mark.parametrize("call", [write, read, attend])
+@pytest.mark.parametrize("check", [False, True])
+def test_status_of_another_kind(call, check, cache, library):
+    """The kernels write 4 bytes through its pointer."""
+    for bad in (torch.zeros(1, dtype=torch.int32, device="meta"),  # another device's
+                torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int64),
+                torch.zeros(1)):
+        with pytest.raises((TypeError, ValueError)):
+            call(cache, check=check, status=bad)
+    assert not [c for c in library.calls if len(c) > 5]  # none reached a launch
+    call(cache, check=check, status=torch.zeros(1, dtype=torch.int32))
+    call(cache, check=False)
+    assert len([c for c in library.calls if len(c) > 5]) == 2
