@@ -842,7 +842,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
         need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, window, dtype)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    space, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    space, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
     _kv_call(L.fp4_kv_attention, cache, batch,
              (*rows, dtype, heads, dim ** -0.5 if scale is None else scale, 1 if causal else 0,
               window, out.data_ptr(), None if lse is None else lse.data_ptr(), space, size),

@@ -74,3 +74,19 @@ def test_status_of_another_kind(call, check, cache, library):
     call(cache, check=check, status=torch.zeros(1, dtype=torch.int32))
     call(cache, check=False)
     assert len([c for c in library.calls if len(c) > 5]) == 2
+
+
+def test_workspace_of_another_kind(cache, library):
+    """The kernels write its bytes in one piece."""
+    for bad in (torch.zeros(64, dtype=torch.uint8, device="meta"),
+                torch.zeros(64, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError):
+            attend(cache, check=False, workspace=bad)
+    assert not library.calls
+
+
+def test_workspace_size_in_bytes(cache, library):
+    for space in (torch.zeros(64, dtype=torch.uint8), torch.zeros(4, 4)):
+        attend(cache, check=False, workspace=space)
+        pointer, size = library.calls[-1][12:14]
+        assert (pointer, size) == (space.data_ptr(), 64)
