@@ -837,7 +837,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     lse = torch.empty(tokens, heads, dtype=torch.float32, device=device) if return_lse else None
     L = _lib or lib()
-    window = int(window)
+    window = max(-1, min(int(window), 2 ** 31 - 1))  # the library takes 32 bits
     if workspace is None:
         need = L.fp4_kv_attention_workspace_bytes(cache._c, batch, heads, window, dtype)
         if need:

@@ -1,5 +1,7 @@
 """CPU tests of what the Python cache calls hand to the library: a recording
 stand-in for the library, host tensors in the place of device ones."""
+import ctypes
+
 import pytest
 import torch
 
@@ -90,3 +92,13 @@ def test_workspace_size_in_bytes(cache, library):
         attend(cache, check=False, workspace=space)
         pointer, size = library.calls[-1][12:14]
         assert (pointer, size) == (space.data_ptr(), 64)
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 80])
+def test_windows_past_32_bits(window, cache, library):
+    """The library takes 32 bits: a window longer than any sequence stays one."""
+    attend(cache, check=False, window=window)
+    for at, call in ((9, library.calls[-1]), (3, library.calls[-2])):  # attention; its workspace
+        assert ctypes.c_int32(call[at]).value >= 2 ** 27
+    attend(cache, check=False, window=-window)
+    assert ctypes.c_int32(library.calls[-1][9]).value < 0  # for the library to refuse
