@@ -689,9 +689,10 @@ _KV_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 class KVCache:
     """An 8-bit key/value cache: k_codes, v_codes [pages, kv_heads, block,
     head_dim] and k_scales, v_scales [pages, kv_heads], contiguous uint8 tensors
-    on one device (include/fp4.h, fp4_kv_cache)."""
+    on one device (include/fp4.h, fp4_kv_cache).  It keeps these tensors, whose
+    addresses the calls use: other tensors make another KVCache."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "_shape", "_device", "_c")
+    __slots__ = ("_tensors", "_shape", "_device", "_c")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales):
         shape = k_codes.shape
@@ -710,11 +711,13 @@ class KVCache:
                 and k_codes.is_contiguous() and k_scales.is_contiguous()
                 and v_codes.is_contiguous() and v_scales.is_contiguous()):
             raise ValueError("a cache's tensors must be contiguous, on one device")
-        self.k_codes, self.k_scales = k_codes, k_scales
-        self.v_codes, self.v_scales = v_codes, v_scales
+        self._tensors = k_codes, k_scales, v_codes, v_scales
         self._shape, self._device = shape, device
         self._c = _pack_kv_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                  v_scales.data_ptr(), *shape)
+
+    k_codes, k_scales, v_codes, v_scales = (
+        property(lambda self, i=i: self._tensors[i]) for i in range(4))
 
 
 def new_kv_cache(pages: int, kv_heads: int, block: int, head_dim: int, device) -> KVCache:

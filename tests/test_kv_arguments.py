@@ -102,3 +102,12 @@ def test_windows_past_32_bits(window, cache, library):
         assert ctypes.c_int32(call[at]).value >= 2 ** 27
     attend(cache, check=False, window=-window)
     assert ctypes.c_int32(library.calls[-1][9]).value < 0  # for the library to refuse
+
+
+def test_a_cache_keeps_its_tensors(cache):
+    """The calls use their addresses: another tensor makes another cache."""
+    for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        held = getattr(cache, name)
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros_like(held))
+        assert getattr(cache, name) is held
