@@ -599,8 +599,11 @@ typedef struct {
  *              cu_tokens[seqs] belong to no sequence: outputs get zeros there
  *   seqs       1 .. 2^20
  * What the kernels find outside these bounds they skip and flag
- * (FP4_FLAG_CACHE_INDEX): a position below 0 or past the table, a page id
- * outside 0 .. pages - 1, prefix sums outside 0 .. tokens.
+ * (FP4_FLAG_CACHE_INDEX): a position below 0 (in attention its row just sees
+ * nothing) or past the table, a page id outside 0 .. pages - 1, prefix sums that
+ * do not start at 0, descend, or pass `tokens`.  With such prefix sums nothing
+ * out of bounds is read or written, but which rows of k, v and out belong to
+ * whom is not known: some may be left as they were.
  */
 typedef struct {
     const int32_t *cu_tokens, *lengths, *table;
@@ -633,8 +636,9 @@ fp4_status fp4_kv_cache_write(const fp4_kv_cache *cache, const fp4_kv_batch *bat
  * Reads the batch's rows (those fp4_kv_cache_write would write; with
  * cu_tokens the prefix sums of lengths, whole sequences) back as k and v
  * [tokens, kv_heads, head_dim] of fp32 or bf16, 16-byte aligned.  Exact in fp32,
- * and in bf16 for scale bytes 8 .. 246.  Rows of no sequence and entries that
- * raise FP4_FLAG_CACHE_INDEX read as zero.  One launch.  Deterministic.
+ * and in bf16 for scale bytes 8 .. 246.  Rows of no sequence, and positions and
+ * pages that raise FP4_FLAG_CACHE_INDEX, read as zero.  One launch.
+ * Deterministic.
  */
 fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batch, void *k,
                              void *v, fp4_dtype yt, int32_t *status, void *stream);

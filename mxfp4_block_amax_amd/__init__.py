@@ -681,7 +681,10 @@ def padded_storage_bytes(fmt: int, rows: int, cols: int) -> int:
 
 # The cache calls below run once or more a layer of every decoding step, where
 # the host's own time counts: checks read each property once, pointers go to
-# ctypes as integers, and the stream is the raw handle.
+# ctypes as integers, and the stream is the raw handle.  With check, what the
+# kernels flag raises ValueError after the call; without, it is in `status` alone,
+# and after row counts that are no prefix sums rows of the outputs may hold
+# whatever was in their memory (include/fp4.h, fp4_kv_batch).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _KV_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 

@@ -254,7 +254,8 @@ __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void atten
                      : A.tokens > 1 ? gridDim.y - 1 - blockIdx.y : blockIdx.y;
     const Item it = A.tokens > 1 && B.seqs < TILE_SEQS
                         ? find_tile(B, item, A.tokens, status)
-                        : find_item(B, item, A.tokens, A.tokens > 1 ? 1 : 0);
+                        : find_item(B, item, A.items, A.tokens, A.tokens > 1 ? 1 : 0,
+                                    headsub == 0 && blockIdx.z == 0, status);
     const int row0 = it.piece * A.tokens;
     if (it.count <= 0 || row0 >= it.count) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
@@ -638,7 +639,7 @@ __global__ __launch_bounds__(JOIN_WG) void attention_join_kernel(KvCache C, KvBa
     __shared__ float tops[JOIN_WG / WAVE], sums[GROUPS];
     __shared__ f32x4_t outs[GROUPS][LANES];
     const int64_t row = (int64_t)blockIdx.x * A.heads + blockIdx.y;
-    const Item it = find_item(B, (int)blockIdx.x, 1, 0);
+    const Item it = search_item(B, (int)blockIdx.x, 1, 0);
     if (it.count <= 0 || it.seq >= B.seqs || it.piece >= it.count) return;
     const Tile T = tile_range(C, B, A, it, it.piece / A.tokens * A.tokens, nullptr);
     const int n = (int)((T.end - T.base + A.split_keys - 1) / A.split_keys);
@@ -767,7 +768,8 @@ __global__ __launch_bounds__(WAVES *WAVE, D <= 128 ? 2 : 1) void attention_wide_
     const int item = A.items - 1 - (int)(rest - (uint32_t)split * A.items);
     const Item it = A.tokens > 1 && B.seqs < TILE_SEQS
                         ? find_tile(B, item, A.tokens, status)
-                        : find_item(B, item, A.tokens, A.tokens > 1 ? 1 : 0);
+                        : find_item(B, item, A.items, A.tokens, A.tokens > 1 ? 1 : 0,
+                                    headsub == 0 && split == 0, status);
     const int row0 = it.piece * A.tokens;
     if (it.count <= 0 || row0 >= it.count) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);

@@ -47,7 +47,26 @@ struct Item {
     int length;                   // the sequence's tokens
 };
 
-__device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit, int extra) {
+// cu is prefix sums from 0 to at most `tokens`: item i of `items` looks at its
+// entries from 64 i on, one a lane, and at those a multiple of 64 items further.
+// The search reads only some of them, so of others it would not know.  The
+// entries come with the search's first ones; `leader`, one workgroup an item,
+// flags.
+struct RowsSeen {
+    int at, base, next;
+};
+
+__device__ __forceinline__ RowsSeen load_rows(const KvBatch &B, int64_t at) {
+    const int i = (int)min(at, (int64_t)B.seqs);
+    return {i, B.cu[i], B.cu[min(i + 1, B.seqs)]};
+}
+
+__device__ __forceinline__ bool rows_bad(const KvBatch &B, const RowsSeen &r) {
+    return r.at == 0 ? r.base != 0 || r.next < 0 || r.next > B.tokens
+                     : r.base < 0 || r.next < r.base || r.next > B.tokens;
+}
+
+__device__ __forceinline__ Item search_item(const KvBatch &B, int item, int unit, int extra) {
     const int lane = threadIdx.x & (WAVE - 1);
     int lo = 0, n = B.seqs + 1;
     while (n >= WAVE) {
@@ -77,6 +96,20 @@ __device__ __forceinline__ Item find_item(const KvBatch &B, int item, int unit, 
     return it;
 }
 
+__device__ __forceinline__ Item find_item(const KvBatch &B, int item, int64_t items, int unit,
+                                          int extra, bool leader, int32_t *status) {
+    const int64_t first = (int64_t)item * WAVE + (threadIdx.x & (WAVE - 1));
+    const RowsSeen seen = load_rows(B, first);
+    const Item it = search_item(B, item, unit, extra);
+    if (leader && status != nullptr && threadIdx.x < WAVE) {
+        bool bad = rows_bad(B, seen);
+        for (int64_t i = first + items * WAVE; i <= B.seqs; i += items * WAVE)
+            bad = bad || rows_bad(B, load_rows(B, i));
+        if (__ballot(bad) != 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
+    }
+    return it;
+}
+
 // The same launch's items without gaps: item i is the i-th piece there is, and
 // what has none comes last.  A lane counts the pieces of up to TILE_SEQS / 64
 // sequences, and the wave adds them up.  Items that own nothing end at once, but
@@ -98,7 +131,8 @@ __device__ __forceinline__ Item find_tile(const KvBatch &B, int item, int unit, 
             base[k] = B.cu[s];
             length[k] = B.lengths[min(s, B.seqs - 1)];
             const int next = s < B.seqs ? B.cu[s + 1] : B.tokens;
-            if (base[k] < 0 || next < base[k] || next > B.tokens) {
+            if (s == 0 ? base[k] != 0 || next < 0 || next > B.tokens
+                       : base[k] < 0 || next < base[k] || next > B.tokens) {
                 if (item == 0 && threadIdx.x < WAVE) flag(status, FLAG_CACHE_INDEX);
             } else {
                 count[k] = next - base[k];

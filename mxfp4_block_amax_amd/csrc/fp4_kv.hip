@@ -83,7 +83,10 @@ __device__ __forceinline__ uint2 chunk_codes(const Chunk<BF16> &c, float inv) {
 // written: 49 us, against 57 us with the pages of a head side by side).
 constexpr int KV_GRID_Y = 32768;
 
-__device__ __forceinline__ int grid_item() { return (int)(blockIdx.z * KV_GRID_Y + blockIdx.y); }
+__device__ __forceinline__ Item grid_item(const KvCache &C, const KvBatch &B, int32_t *status) {
+    return find_item(B, (int)(blockIdx.z * KV_GRID_Y + blockIdx.y),
+                     (int64_t)gridDim.y * gridDim.z, C.block, 2, blockIdx.x == 0, status);
+}
 
 dim3 kv_grid(const KvCache &C, const KvBatch &B) {
     const int64_t items = item_count(B.tokens, B.seqs, C.block, 2);
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
                                                        const void *v, int64_t v_token,
                                                        int64_t v_head, int32_t *status) {
     __shared__ uint32_t part[2][256 / WAVE];
-    const Item it = find_item(B, grid_item(), C.block, 2);
+    const Item it = grid_item(C, B, status);
     if (it.seq >= B.seqs || it.count <= 0) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
@@ -215,7 +218,7 @@ constexpr int KV_READ = 2;  // such pieces of keys, and of values, a lane has in
 template <bool BF16>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvCache C, KvBatch B, void *k, void *v,
                                                       int32_t *status) {
-    const Item it = find_item(B, grid_item(), C.block, 2);
+    const Item it = grid_item(C, B, status);
     if (it.count <= 0) {
         if (it.count < 0 && threadIdx.x == 0) flag(status, FLAG_CACHE_INDEX);
         return;
