@@ -15,6 +15,7 @@
 // batch's prefix sums, then the table, then the page: three loads that wait for
 // each other) is gone once for both.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4_kernels.h"
 #include "fp4_kv.h"
@@ -30,13 +31,14 @@ struct Chunk {
     u32x4_t w[BF16 ? 1 : 2];
 };
 
-template <bool BF16>
+// ONCE: streamed, nothing reads it again.
+template <bool BF16, bool ONCE>
 __device__ __forceinline__ Chunk<BF16> load_chunk(const void *x, int64_t at) {
     Chunk<BF16> c;
     const u32x4_t *p = BF16 ? (const u32x4_t *)((const uint16_t *)x + at)
                             : (const u32x4_t *)((const float *)x + at);
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 1 : 2); ++i) c.w[i] = __builtin_nontemporal_load(p + i);
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) c.w[i] = ONCE ? __builtin_nontemporal_load(p + i) : p[i];
     return c;
 }
 
@@ -137,10 +139,12 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
     const int per = C.dim >> 3;  // chunks of a token: 8, 16, 24 or 32
     const int chunks = n * per;
     const bool held = chunks <= KV_HELD * (int)blockDim.x;
-    auto fetch = [&](const Half &f, int c) {
+    auto fetch = [&](auto stream, const Half &f, int c) {
         const int t = c / per;
-        return load_chunk<BF16>(f.x, f.x0 + t * f.token + 8 * (c - t * per));
+        return load_chunk<BF16, stream>(f.x, f.x0 + t * f.token + 8 * (c - t * per));
     };
+    constexpr std::true_type once{};
+    constexpr std::false_type again{};
     Chunk<BF16> x[2][KV_HELD];
     float amax[2] = {0.0f, 0.0f};
     bool bad = false;
@@ -150,7 +154,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
 #pragma unroll
             for (int i = 0; i < KV_HELD; ++i) {
                 const int c = threadIdx.x + i * blockDim.x;
-                if (c < chunks) x[s][i] = fetch(half[s], c);
+                if (c < chunks) x[s][i] = fetch(once, half[s], c);
             }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -158,10 +162,13 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
             for (int i = 0; i < KV_HELD; ++i)
                 if (threadIdx.x + i * blockDim.x < (uint32_t)chunks)
                     bad |= chunk_amax<BF16>(x[s][i], amax[s]);
-    } else {  // read again below, from a cache
+    } else {
+        // Too many to hold: read again below, for which these loads are ordinary
+        // ones (8 x 4096 tokens of 8 heads of 128 in pages of 128, fp32: 109 us,
+        // streamed 138; bf16 73 and 74; in pages of 256, bf16: 70 and 68).
         for (int c = threadIdx.x; c < chunks; c += blockDim.x)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) bad |= chunk_amax<BF16>(fetch(half[s], c), amax[s]);
+            for (int s = 0; s < 2; ++s) bad |= chunk_amax<BF16>(fetch(again, half[s], c), amax[s]);
     }
     // non-negative floats order as their bits
     uint32_t top[2] = {wave_max_u32(f2u(amax[0])), wave_max_u32(f2u(amax[1]))};
@@ -190,7 +197,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvCache C, KvBatch B, con
             }
         } else {
             for (int c = threadIdx.x; c < chunks; c += blockDim.x)
-                *(uint2 *)(codes + 8 * c) = chunk_codes<BF16>(fetch(f, c), inv);
+                *(uint2 *)(codes + 8 * c) = chunk_codes<BF16>(fetch(once, f, c), inv);
         }
         if (byte > before[s] && slot0 > 0) {
             // 448 2^-20 rounds to zero, and so does all below
