@@ -154,8 +154,9 @@ __device__ __forceinline__ float2 split_weight(float m, float l) {
 
 // Launch order: heads, then row tiles, then splits, so that the tiles that read
 // the same keys are near each other in time and, for 8 heads, on the same XCD and
-// its L2 (8 sequences x 30 tokens over 4096 keys of 8 heads, 256 dimensions: 99
-// us, row tiles first 215).  More row tiles than a grid's y go first.
+// its L2 (8 sequences x 20 tokens over 4096 keys, 8 x 4 heads of 256: 97 us, row
+// tiles first 112; 4 tokens, 8 x 8 heads of 128: 32 and 52).  More row tiles than a
+// grid's y go first.
 constexpr int NARROW_GRID_Y = 65535;
 constexpr int NARROW_PAGES = 256;  // pages under a workgroup's keys, at most
 
@@ -201,8 +202,8 @@ constexpr int kHalves = D <= 128 ? 2 : 1;
 
 // Waves of a SIMD, by registers, and waves of a workgroup that has a CU for
 // itself.  The three terms of an fp32 query of 256 dimensions take 96 registers;
-// those of 64 spill with four waves (16 sequences x 2048 keys, 16 heads: 31 us,
-// with three 25).
+// those of 64 spill with four waves (16 sequences x 2048 keys, 16 heads: 27 us,
+// with three 22).
 template <int D, bool F32>
 constexpr int kNarrowOccupancy = D == 64 ? (F32 ? 3 : 4) : F32 && D == 256 ? 1 : 2;
 template <int D, bool F32>
@@ -219,20 +220,21 @@ struct Step {
 // single tokens, drafts, short chunks.
 //
 // A workgroup has one row tile, one kv head and one range of keys; its waves
-// take 32 keys at a time in turn.  Scores are computed transposed,
+// take 32 keys at a time in turn (16 of more than 128 dimensions).  Scores are
+// computed transposed,
 // S^T = K Q^T, so that a lane's scores are those of one row (lane % 16) and its
 // keys, 4 (lane / 16) + i, are the ones the second product wants from this
 // lane: probabilities go from the first product to the second without leaving
 // their lane.  Out^T = V^T P^T; which keys are which of a product's 32 terms is
 // free as long as V follows P, and which dimension is which row of a tile is
-// free too, so a lane loads D / 16 consecutive bytes of eight value rows and
-// transposes them by byte permutes.  Nothing of keys or values goes through
+// free too, so a lane loads D / 16 consecutive bytes of eight (four) value rows
+// and transposes them by byte permutes.  Nothing of keys or values goes through
 // LDS: each byte is used by one lane.
 //
 // Long decoding is bound by HBM: 64 tokens over about 8192 keys each, 8 x 8 heads
-// of 128, read 1084 MB in 205 us (5.3 TB/s; 185 at equal lengths), one over 200001
+// of 128, read 1084 MB in 206 us (5.3 TB/s; 190 at equal lengths), one over 200001
 // 410 MB in 76 us (5.4 TB/s).  Short calls are bound by latency, some 2 us a step
-// where a CU has one workgroup: a token over 1000 keys takes 13.7 us.
+// where a CU has one workgroup: a token over 1000 keys takes 14.1 us.
 template <int D, bool F32, int WAVES>
 __global__ __launch_bounds__(WAVES *WAVE, (kNarrowOccupancy<D, F32>)) void attention_narrow_kernel(
     KvCache C, KvBatch B, AttnArgs A, int32_t *status) {
@@ -738,10 +740,13 @@ __device__ __forceinline__ int key_swizzle(int row) {
 // side) to fp16; its codes were loaded during the step before that.
 //
 // Bound by MFMA and vector issue of the two waves of a SIMD, and by the power they
-// draw: 4 chunks of about 1024 tokens over 6000, 8 x 8 heads of 128, 898 us (937
-// TFLOP/s, MFMA busy for 42% of the cycles at a clock that falls to about 1.9
-// GHz); a prompt of 4096, 8 x 4 heads, 149 us (922 TFLOP/s).  With the codes of a
-// step loaded and stored in the same step: 930 and 155.
+// draw: 4 chunks of about 1024 tokens over 6000, 8 x 8 heads of 128, 905 us (930
+// TFLOP/s, MFMA busy for 41% of the cycles and vector instructions for 46%, LDS for
+// 30%, at a clock that falls to 1.94 GHz); a prompt of 4096, 8 x 4 heads, 151 us
+// (910 TFLOP/s).  With the codes of a step loaded and stored in the same step 3 to
+// 4% more.  Of 192 and 256 dimensions one wave a SIMD holds the sums in accumulation
+// registers, and nothing covers what it waits for; of 256 it also spills 18 of its
+// 512 registers.
 //
 // PAGES is how many pages 64 keys may have, 1 (of 64 tokens and more) or 4: four
 // distances d cost the same two calls 2.3% over values that carry all of d
@@ -1216,7 +1221,7 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
     // (2 prompts of 433 tokens, 4 heads: 13 us and 21; 3 chunks of 116 tokens, 8
     // heads, over 1212 keys: 20 and 31; but 119 tokens, 16 x 7 heads, four for each
     // CU: 29 and 18).  Tiles of 256 rows once there are two for
-    // each CU (4 chunks of 1024 tokens: 984 us with tiles of 128, 922; 8 of 64 tokens,
+    // each CU (4 chunks of 1024 tokens: 980 us with tiles of 128, 911; 8 of 64 tokens,
     // one tile for each four CUs: 130, 187).  fp32 queries have no wide kernel.
     const int64_t narrow_tiles = (per * group + 15) / 16 * B.seqs * C.heads;
     P.wide = 0;
@@ -1252,7 +1257,7 @@ Plan make_plan(const KvCache &C, const KvBatch &B, int heads, int window, bool b
         // three workgroups wait for each place: sequences differ in length.  Splits
         // are as long as that leaves them, up to 16384 keys (64 sequences x 20000
         // keys of 256 dimensions: 494 us; up to 8192 514, up to 4096 539); six steps
-        // of a workgroup are not split.
+        // of a workgroup are not split (1000 keys: 14.1 us, in four 14.8).
         P.waves = tiles > CUS || (!bf16 && C.dim == 256) ? 4 : C.dim == 64 ? (bf16 ? 16 : 12) : 8;
         const int64_t slots = tiles > CUS && (bf16 || C.dim < 256) ? 2 * CUS : CUS;
         const int64_t want = tiles <= slots ? slots / tiles : (3 * slots + tiles - 1) / tiles;

@@ -114,7 +114,7 @@ __device__ __forceinline__ Item find_item(const KvBatch &B, int item, int64_t it
 // what has none comes last.  A lane counts the pieces of up to TILE_SEQS / 64
 // sequences, and the wave adds them up.  Items that own nothing end at once, but
 // between others they leave shader engines, which get workgroups in turn, with
-// less to do: attention of 8 x 4 tokens over 4096 keys, 8 x 8 heads, 31 us, with
+// less to do: attention of 8 x 4 tokens over 4096 keys, 8 x 8 heads, 32 us, with
 // every second item empty 49.
 constexpr int TILE_SEQS = 256;  // with the rows past the last one
 
