@@ -504,6 +504,40 @@ fp4_status fp4_linear_mxfp4(const void *x, fp4_dtype xt, int64_t M, int64_t K,
                             int32_t *status, void *stream);
 
 /*
+ * Linear layer of few tokens with an FP4 weight and activations that keep
+ * their precision ("FP4, FP8 and INT8/INT4" page, section 5.1: weights stored in
+ * four bits and widened in the product): c = x Bt^T with
+ *   c_mn = s_g sum_b s_nb sum_{k in b} E2M1(code_nk) x_mk   (s_g = 1: MXFP4).
+ *   fmt        FP4_MXFP4 or FP4_NVFP4
+ *   x          [M, K] fp32 or bf16, 16-byte aligned, finite or not
+ *   bt_codes, bt_scales, bt_global_scale   the weight Bt [N, K] as its
+ *              quantizer gives it; codes 16-byte aligned; the tensor scale
+ *              (device float) for NVFP4, ignored for MXFP4
+ *   c          [M, N] fp32 or bf16 (nearest, ties to even, of the fp32 sum
+ *              times s_g)
+ * Products are exact: a weight's value fits bf16 (MXFP4 for scale bytes up to
+ * 252), fp32 activations count with all their bits.  Sums are fp32, their order
+ * is fixed: deterministic.  A NaN scale byte makes its row's outputs NaN.  K is
+ * a multiple of the block (32 or 16); any M and N.  The weight is read once
+ * for every 64 tokens, which bounds the time: for long prompts the W4A4
+ * layers are faster.  One launch.
+ */
+fp4_status fp4_linear_w4(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
+                         const uint8_t *bt_codes, const uint8_t *bt_scales,
+                         const float *bt_global_scale, int64_t N, void *c, fp4_dtype ct,
+                         void *stream);
+
+/*
+ * The same on a weight in MFMA operand order, Bt [N, K] packed by
+ * fp4_pack_mxfp4_operand or fp4_pack_nvfp4_operand: the buffer that a W4A4
+ * layer multiplies prompts with serves single tokens too.  bt_packed is
+ * 16-byte aligned; K is a multiple of 512.
+ */
+fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
+                                const uint8_t *bt_packed, const float *bt_global_scale, int64_t N,
+                                void *c, fp4_dtype ct, void *stream);
+
+/*
  * Row-padded layout ("NVFP4 / MXFP4 format" page, section 8): each row of a
  * [rows, cols] matrix is padded with zeros to whole blocks (32 for MXFP4, 16
  * for NVFP4), pcols = ceil(cols / block) * block, and the padded matrix is

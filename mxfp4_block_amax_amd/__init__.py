@@ -59,6 +59,7 @@ EXPORTS = ("fp4_quantize_mxfp4", "fp4_quantize_mxfp4_rule", "fp4_quantize_nvfp4"
            "fp4_gemm_mxfp4_packed", "fp4_quantize_mxfp4_packed", "fp4_linear_mxfp4_packed",
            "fp4_nv_packed_operand_bytes", "fp4_pack_nvfp4_operand", "fp4_gemm_nvfp4_packed",
            "fp4_quantize_nvfp4_packed", "fp4_linear_nvfp4_packed",
+           "fp4_linear_w4", "fp4_linear_w4_packed",
            "fp4_quantize_nvfp4_noalloc", "fp4_workspace_bytes", "fp4_status_str",
            "fp4_kv_cache_write", "fp4_kv_cache_read", "fp4_kv_attention",
            "fp4_kv_attention_workspace_bytes")
@@ -124,6 +125,8 @@ def lib() -> ctypes.CDLL:
                                                 ctypes.c_uint32]
     L.fp4_debug_linear_mxfp4_spin.argtypes = [P, I, I64, I64, P, P, I64, P, P, P, I, I, P, S, P, P,
                                               ctypes.c_uint32]
+    L.fp4_linear_w4.argtypes = [I, P, I, I64, I64, P, P, P, I64, P, I, P]
+    L.fp4_linear_w4_packed.argtypes = [I, P, I, I64, I64, P, P, I64, P, I, P]
     KC = KB = ctypes.c_char_p
     L.fp4_kv_cache_write.argtypes = [KC, KB, P, I64, I64, P, I64, I64, I, P, P]
     L.fp4_kv_cache_read.argtypes = [KC, KB, P, P, I, P, P]
@@ -638,6 +641,87 @@ def linear_mxfp4(x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torch.Tenso
     return c, (a_codes, a_scales)
 
 
+# As the cache calls further down, the layers of a decoding step check each
+# property once and pass pointers as integers: the host's time counts there.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _on(x: torch.Tensor, fn, *args):
+    """fn(*args, stream) on x's device and its current stream."""
+    device = x.get_device()
+    if device == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, _raw_stream(device))
+    if code:
+        _ok(code)
+
+
+def _w4_output(fmt, x, K, N, global_scale, out_dtype, out):
+    """What both layouts of a four-bit weight check; (x's rows, its dtype's code,
+    the tensor scale's pointer, the output)."""
+    if fmt != MXFP4 and fmt != NVFP4:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    dtype, shape = x.dtype, x.shape
+    code = _DTYPES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    if len(shape) < 1 or shape[-1] != K:
+        raise ValueError(f"x must have {K} columns, as the weight")
+    if not x.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    if fmt == MXFP4:
+        s_g = None
+    else:
+        _check_global_scale(global_scale, "global_scale", x.device)
+        s_g = global_scale.data_ptr()
+    if out is None:
+        out = torch.empty(*shape[:-1], N, dtype=out_dtype or dtype, device=x.device)
+    elif (out.shape != (*shape[:-1], N) or out.device != x.device or not out.is_contiguous()
+          or (out_dtype is not None and out.dtype != out_dtype)):
+        raise ValueError("out must be a contiguous tensor of x's rows and N columns, of out_dtype")
+    return x.numel() // K, code, s_g, out
+
+
+def linear_w4(fmt: int, x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torch.Tensor,
+              global_scale=None, out_dtype=None, out=None) -> torch.Tensor:
+    """Linear layer of few tokens: x [.., K] (fp32 or bf16, not quantized) times
+    the FP4 weight Bt [N, K] (codes [N, K/2], scales [N, K/block], for NVFP4 its
+    tensor scale).  Returns [.., N] of x's dtype, or of out_dtype."""
+    if bt_codes.dim() != 2 or not x.is_cuda:
+        raise ValueError("expected device tensors, the weight's codes as [N, K/2]")
+    N, kh = bt_codes.shape
+    _check_u8(bt_codes, N * kh, "bt_codes", x.device)
+    _check_u8(bt_scales, N * (2 * kh) // (32 if fmt == MXFP4 else 16), "bt_scales", x.device)
+    M, code, s_g, out = _w4_output(fmt, x, 2 * kh, N, global_scale, out_dtype, out)
+    if M > 0:
+        _on(x, (_lib or lib()).fp4_linear_w4, fmt, x.data_ptr(), code, M, 2 * kh,
+            bt_codes.data_ptr(), bt_scales.data_ptr(), s_g, N, out.data_ptr(),
+            _dtype_code(out.dtype))
+    return out
+
+
+def linear_w4_packed(fmt: int, x: torch.Tensor, bt_packed: torch.Tensor, N: int,
+                     global_scale=None, out_dtype=None, out=None) -> torch.Tensor:
+    """linear_w4 with a weight of pack_mxfp4_operand or pack_nvfp4_operand."""
+    if not x.is_cuda:
+        raise TypeError("expected a device tensor")
+    K, N = x.shape[-1], int(N)
+    need = (packed_operand_bytes if fmt == MXFP4 else nv_packed_operand_bytes)(N, K)
+    if need == 0:
+        raise ValueError("the packed layout needs N >= 1 and K a positive multiple of 512")
+    if bt_packed.numel() < need:
+        raise ValueError("packed operand smaller than its shape")
+    _check_u8(bt_packed, bt_packed.numel(), "bt_packed", x.device)
+    M, code, s_g, out = _w4_output(fmt, x, K, N, global_scale, out_dtype, out)
+    if M > 0:
+        _on(x, (_lib or lib()).fp4_linear_w4_packed, fmt, x.data_ptr(), code, M, K,
+            bt_packed.data_ptr(), s_g, N, out.data_ptr(), _dtype_code(out.dtype))
+    return out
+
+
 def _padded_cols(cols: int, fmt: int) -> int:
     block = 32 if fmt == MXFP4 else 16
     return (cols + block - 1) // block * block
@@ -685,8 +769,6 @@ def padded_storage_bytes(fmt: int, rows: int, cols: int) -> int:
 # kernels flag raises ValueError after the call; without, it is in `status` alone,
 # and after row counts that are no prefix sums rows of the outputs may hold
 # whatever was in their memory (include/fp4.h, fp4_kv_batch).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_KV_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 class KVCache:
@@ -790,7 +872,7 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_tokens: 
         raise ValueError("k and v must have the same shape and dtype")
     if len(shape) != 3 or shape[1] != cache._shape[1]:
         raise ValueError("k and v must be [tokens, the cache's kv heads, head_dim]")
-    code = _KV_DTYPES.get(dtype)
+    code = _DTYPES.get(dtype)
     if code is None:
         code = _dtype_code(dtype)
     batch = _kv_batch(cache, cu_tokens, lengths, table, shape[0])
@@ -831,7 +913,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, cu_tokens: torch.Tensor, lengt
     tokens: long chunks and single tokens are faster in calls of their own."""
     rows = _kv_rows(q, cache, "q")
     tokens, heads, dim = q.shape
-    dtype = _KV_DTYPES.get(q.dtype)
+    dtype = _DTYPES.get(q.dtype)
     if dtype is None:
         dtype = _dtype_code(q.dtype)
     batch = _kv_batch(cache, cu_tokens, lengths, table, tokens)

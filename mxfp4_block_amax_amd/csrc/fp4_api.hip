@@ -492,6 +492,48 @@ fp4_status fp4_gemm_nvfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                               ct == FP4_BF16, (hipStream_t)stream));
 }
 
+// What both layouts of a four-bit weight's linear layer check.
+static fp4_status linear_w4_args(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
+                                 const float *bt_global_scale, int64_t N, const void *c,
+                                 fp4_dtype ct, int64_t k_unit) {
+    if (fmt != FP4_MXFP4 && fmt != FP4_NVFP4) return FP4_E_DTYPE;
+    if (!valid_dtype(xt) || !valid_dtype(ct)) return FP4_E_DTYPE;
+    if (!x || !c || (fmt == FP4_NVFP4 && !bt_global_scale)) return FP4_E_ARG;
+    if (M < 1 || N < 1 || K < 1 || K % k_unit) return FP4_E_SHAPE;
+    if (M > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2) return FP4_E_SHAPE;
+    if (M > kMaxElems / K || N > kMaxElems / K || !fp4dev::linear_w4_fits(M, N)) return FP4_E_SHAPE;
+    if (!aligned(x, 16) || !aligned(c, ct == FP4_BF16 ? 2 : 4)) return FP4_E_ALIGN;
+    if (fmt == FP4_NVFP4 && !aligned(bt_global_scale, 4)) return FP4_E_ALIGN;
+    return FP4_OK;
+}
+
+fp4_status fp4_linear_w4(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
+                         const uint8_t *bt_codes, const uint8_t *bt_scales,
+                         const float *bt_global_scale, int64_t N, void *c, fp4_dtype ct,
+                         void *stream) {
+    const fp4_status st = linear_w4_args(fmt, x, xt, M, K, bt_global_scale, N, c, ct,
+                                         fmt == FP4_MXFP4 ? 32 : 16);
+    if (st != FP4_OK) return st;
+    if (!bt_codes || !bt_scales) return FP4_E_ARG;
+    if (!aligned(bt_codes, 16)) return FP4_E_ALIGN;
+    return from_hip(fp4dev::launch_linear_w4((int)fmt, x, xt == FP4_BF16, M, K, bt_codes,
+                                             bt_scales, bt_global_scale, false, N, c,
+                                             ct == FP4_BF16, (hipStream_t)stream));
+}
+
+fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
+                                const uint8_t *bt_packed, const float *bt_global_scale, int64_t N,
+                                void *c, fp4_dtype ct, void *stream) {
+    const fp4_status st = linear_w4_args(fmt, x, xt, M, K, bt_global_scale, N, c, ct, 512);
+    if (st != FP4_OK) return st;
+    if (!bt_packed) return FP4_E_ARG;
+    if (!aligned(bt_packed, 16)) return FP4_E_ALIGN;
+    const uint8_t *scales = bt_packed + (N + 31) / 32 * 32 * (K / 2);
+    return from_hip(fp4dev::launch_linear_w4((int)fmt, x, xt == FP4_BF16, M, K, bt_packed, scales,
+                                             bt_global_scale, true, N, c, ct == FP4_BF16,
+                                             (hipStream_t)stream));
+}
+
 // fp4_linear_mxfp4 with the grid barrier's poll limit as an argument
 static fp4_status linear_mxfp4(const void *x, fp4_dtype xt, int64_t M, int64_t K,
                                const uint8_t *bt_codes, const uint8_t *bt_scales, int64_t N,
