@@ -87,6 +87,7 @@ typedef FP4_ENUM {
 #define FP4_FLAG_CACHE_INDEX 8     /* a cache call met a position, a token range or a
                                       page id outside what the batch and the cache
                                       hold; those entries were skipped           */
+#define FP4_FLAG_EXPERT_INDEX 16   /* an expert id outside -1 .. experts - 1; skipped  */
 
 typedef FP4_ENUM { FP4_F32 = 0, FP4_BF16 = 1 } fp4_dtype;
 typedef FP4_ENUM { FP4_MXFP4 = 0, FP4_NVFP4 = 1 } fp4_format;
@@ -536,6 +537,67 @@ fp4_status fp4_linear_w4(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M,
 fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
                                 const uint8_t *bt_packed, const float *bt_global_scale, int64_t N,
                                 void *c, fp4_dtype ct, void *stream);
+
+/*
+ * A mixture of experts for few tokens: the router's choice of experts, and their
+ * gated products with FP4 weights and activations that keep their precision
+ * (the operation of fp4_linear_w4, three times an expert).
+ *
+ * fp4_moe_route: l_te = sum_h x_th r_eh; chosen[t] = the top_k experts with the
+ * largest l_te, descending, the lower id of equal ones first; weights[t][j] =
+ * exp(l of chosen[t][j]) / sum exp(l_te) over the chosen ones (renormalize = 1)
+ * or over all experts (0).
+ *   x          [tokens, hidden] fp32 or bf16     router [experts, hidden] fp32 or bf16
+ *   chosen     [tokens, top_k] int32             weights [tokens, top_k] fp32
+ *   workspace  fp4_moe_route_workspace_bytes(...) bytes, scratch
+ * hidden is a multiple of 8; at most 1024 experts, 32 of a token, 2^21 tokens; x,
+ * router and workspace 16-byte aligned.  Sums are 64-bit, their order is fixed:
+ * deterministic.  A NaN logit is below every other.  Two launches.
+ */
+size_t fp4_moe_route_workspace_bytes(int64_t tokens, int64_t hidden, int32_t experts);
+fp4_status fp4_moe_route(const void *x, fp4_dtype xt, int64_t tokens, int64_t hidden,
+                         const void *router, fp4_dtype rt, int32_t experts, int32_t top_k,
+                         int32_t renormalize, int32_t *chosen, float *weights, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * The experts' weights, as the quantizers give them for row-major tensors:
+ *   up    [experts, 2 inner, hidden]  rows 0 .. inner - 1 of an expert its gate,
+ *         the others its up projection
+ *   down  [experts, hidden, inner]
+ * codes 16-byte aligned; hidden and inner multiples of the block.  NVFP4: tensor
+ * scales, one for all experts (global_scale_stride 0) or one each (1).
+ */
+typedef struct {
+    const uint8_t *up_codes, *up_scales, *down_codes, *down_scales;
+    const float *up_global_scale, *down_global_scale;
+    int64_t hidden, inner;
+    int32_t experts, global_scale_stride;
+} fp4_moe_weights;
+
+/*
+ * out_t = sum_j weights_tj Down_e (silu(Gate_e x_t) * (Up_e x_t)), e = experts_tj,
+ * silu(a) = a / (1 + exp(-a)).
+ *   x          [tokens, hidden] fp32 or bf16, 16-byte aligned
+ *   experts    [tokens, top_k] int32: ids, in any order, the same one twice (its
+ *              weights add up) or -1 (none: padding rows); others are skipped and
+ *              raise FP4_FLAG_EXPERT_INDEX
+ *   weights    [tokens, top_k] fp32
+ *   out        [tokens, hidden] fp32 or bf16; zeros for a token without experts
+ *   workspace  fp4_moe_experts_workspace_bytes(...) bytes, 16-byte aligned scratch
+ *              (calls that share one must be stream-ordered)
+ * Products are exact as in fp4_linear_w4, sums fp32 in a fixed order; the gated
+ * values go to the second product as two bf16 terms (17 bits) for bf16 x, three
+ * for fp32 x.  An expert's weights reach only the tokens that name it.  Those of
+ * each expert that some token names are read once for every 64 tokens.  Two
+ * launches.  Deterministic.
+ */
+size_t fp4_moe_experts_workspace_bytes(const fp4_moe_weights *w, fp4_format fmt, int64_t tokens,
+                                       int32_t top_k, fp4_dtype xt);
+fp4_status fp4_moe_experts(fp4_format fmt, const fp4_moe_weights *w, const void *x, fp4_dtype xt,
+                           int64_t tokens, const int32_t *experts, const float *weights,
+                           int32_t top_k, void *out, fp4_dtype ot, void *workspace,
+                           size_t workspace_bytes, int32_t *status, void *stream);
 
 /*
  * Row-padded layout ("NVFP4 / MXFP4 format" page, section 8): each row of a

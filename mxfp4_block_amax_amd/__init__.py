@@ -48,6 +48,7 @@ FLAG_NONFINITE = 1
 FLAG_SCALE_UNDERFLOW = 2
 FLAG_BARRIER_TIMEOUT = 4
 FLAG_CACHE_INDEX = 8
+FLAG_EXPERT_INDEX = 16
 
 EXPORTS = ("fp4_quantize_mxfp4", "fp4_quantize_mxfp4_rule", "fp4_quantize_nvfp4",
            "fp4_dequantize", "fp4_scale_search", "fp4_scale_search_exhaustive",
@@ -59,7 +60,9 @@ EXPORTS = ("fp4_quantize_mxfp4", "fp4_quantize_mxfp4_rule", "fp4_quantize_nvfp4"
            "fp4_gemm_mxfp4_packed", "fp4_quantize_mxfp4_packed", "fp4_linear_mxfp4_packed",
            "fp4_nv_packed_operand_bytes", "fp4_pack_nvfp4_operand", "fp4_gemm_nvfp4_packed",
            "fp4_quantize_nvfp4_packed", "fp4_linear_nvfp4_packed",
-           "fp4_linear_w4", "fp4_linear_w4_packed",
+           "fp4_linear_w4", "fp4_linear_w4_packed", "fp4_moe_route",
+           "fp4_moe_route_workspace_bytes", "fp4_moe_experts",
+           "fp4_moe_experts_workspace_bytes",
            "fp4_quantize_nvfp4_noalloc", "fp4_workspace_bytes", "fp4_status_str",
            "fp4_kv_cache_write", "fp4_kv_cache_read", "fp4_kv_attention",
            "fp4_kv_attention_workspace_bytes")
@@ -71,9 +74,10 @@ _lib = None
 
 
 # fp4_kv_cache and fp4_kv_batch as bytes (passed by pointer): packing one takes a
-# third of the time a ctypes.Structure takes to fill
+# third of the time a ctypes.Structure takes to fill; fp4_moe_weights alike
 _pack_kv_cache = struct.Struct("@PPPPqiii4x").pack
 _pack_kv_batch = struct.Struct("@PPPqqii").pack
+_pack_moe_weights = struct.Struct("@PPPPPPqqii").pack
 
 
 class Fp4Error(RuntimeError):
@@ -127,7 +131,13 @@ def lib() -> ctypes.CDLL:
                                               ctypes.c_uint32]
     L.fp4_linear_w4.argtypes = [I, P, I, I64, I64, P, P, P, I64, P, I, P]
     L.fp4_linear_w4_packed.argtypes = [I, P, I, I64, I64, P, P, I64, P, I, P]
-    KC = KB = ctypes.c_char_p
+    KC = KB = KM = ctypes.c_char_p
+    L.fp4_moe_route_workspace_bytes.argtypes = [I64, I64, I32]
+    L.fp4_moe_route_workspace_bytes.restype = S
+    L.fp4_moe_route.argtypes = [P, I, I64, I64, P, I, I32, I32, I32, P, P, P, S, P]
+    L.fp4_moe_experts_workspace_bytes.argtypes = [KM, I, I64, I32, I]
+    L.fp4_moe_experts_workspace_bytes.restype = S
+    L.fp4_moe_experts.argtypes = [I, KM, P, I, I64, P, P, I32, P, I, P, S, P, P]
     L.fp4_kv_cache_write.argtypes = [KC, KB, P, I64, I64, P, I64, I64, I, P, P]
     L.fp4_kv_cache_read.argtypes = [KC, KB, P, P, I, P, P]
     L.fp4_kv_attention.argtypes = [KC, KB, P, I64, I64, I, I32, F, I32, I32, P, P, P, S, P, P]
@@ -191,6 +201,8 @@ def _raise_flags(flags: int):
         raise ValueError("a nonzero scale rounded to zero (tensor, block scale or alpha underflow)")
     if flags & FLAG_CACHE_INDEX:
         raise ValueError("a cache position, token range or page id is out of bounds")
+    if flags & FLAG_EXPERT_INDEX:
+        raise ValueError("an expert id is neither -1 nor one of the layer's")
     # FLAG_BARRIER_TIMEOUT is information only: a workgroup took the grid
     # barrier's fallback and the outputs are exact
 
@@ -719,6 +731,141 @@ def linear_w4_packed(fmt: int, x: torch.Tensor, bt_packed: torch.Tensor, N: int,
     if M > 0:
         _on(x, (_lib or lib()).fp4_linear_w4_packed, fmt, x.data_ptr(), code, M, K,
             bt_packed.data_ptr(), s_g, N, out.data_ptr(), _dtype_code(out.dtype))
+    return out
+
+
+def _workspace(workspace, need: int, device):
+    """A scratch buffer of at least `need` bytes (its address and size)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    return workspace, workspace.data_ptr(), workspace.nbytes
+
+
+def _check_status(status, check: bool, device):
+    """The status tensor of a call: the caller's, a new one with check, or none."""
+    if status is not None:
+        if status.dtype is not torch.int32:
+            raise TypeError("status must be an int32 tensor")
+        if status.device != device or status.numel() == 0:
+            raise ValueError("status must have an element, on the call's device")
+    elif check:
+        status = torch.zeros(1, dtype=torch.int32, device=device)
+    return status
+
+
+def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int, renormalize: bool = True,
+              out=None, workspace=None):
+    """The top_k experts of each token and their weights: x [tokens, hidden] times
+    router [experts, hidden] (fp32 or bf16 each), softmax over the chosen experts
+    (renormalize) or over all.  Returns (experts int32, weights fp32), each
+    [tokens, top_k], descending; of equal logits the lower id comes first."""
+    if x.dim() != 2 or router.dim() != 2 or x.shape[1] != router.shape[1]:
+        raise ValueError("x must be [tokens, hidden], router [experts, hidden]")
+    if not x.is_cuda:
+        raise TypeError("expected device tensors")
+    device = x.device
+    if router.device != device or not x.is_contiguous() or not router.is_contiguous():
+        raise ValueError("x and router must be contiguous, on one device")
+    xt, rt = _dtype_code(x.dtype), _dtype_code(router.dtype)
+    (tokens, hidden), experts = x.shape, router.shape[0]
+    top_k = int(top_k)
+    if out is None:
+        if not 1 <= top_k <= experts:
+            raise ValueError("top_k must be from 1 to the number of experts")
+        chosen = torch.empty(tokens, top_k, dtype=torch.int32, device=device)
+        weights = torch.empty(tokens, top_k, dtype=torch.float32, device=device)
+    else:
+        chosen, weights = out
+        for t, dtype in ((chosen, torch.int32), (weights, torch.float32)):
+            if (t.shape != (tokens, top_k) or t.dtype != dtype or t.device != device
+                    or not t.is_contiguous()):
+                raise ValueError("out must be contiguous int32 and float32 [tokens, top_k]")
+    if tokens == 0:
+        return chosen, weights
+    L = _lib or lib()
+    need = L.fp4_moe_route_workspace_bytes(tokens, hidden, experts)
+    workspace, space, size = _workspace(workspace, need, device)
+    _on(x, L.fp4_moe_route, x.data_ptr(), xt, tokens, hidden, router.data_ptr(), rt, experts,
+        top_k, 1 if renormalize else 0, chosen.data_ptr(), weights.data_ptr(), space, size)
+    return chosen, weights
+
+
+def _moe_weights(fmt, up, down, device) -> bytes:
+    (uc, us), (dc, ds) = up[:2], down[:2]
+    if uc.dim() != 3 or dc.dim() != 3:
+        raise ValueError("codes must be [experts, 2 inner, hidden/2] and [experts, hidden, inner/2]")
+    experts, rows, hh = uc.shape
+    inner, hidden = rows // 2, 2 * hh
+    if rows % 2 or dc.shape != (experts, hidden, inner // 2) or inner % 2:
+        raise ValueError("codes must be [experts, 2 inner, hidden/2] and [experts, hidden, inner/2]")
+    block = 32 if fmt == MXFP4 else 16
+    _check_u8(uc, uc.numel(), "up codes", device)
+    _check_u8(dc, dc.numel(), "down codes", device)
+    _check_u8(us, experts * rows * (hidden // block), "up scales", device)
+    _check_u8(ds, experts * hidden * (inner // block), "down scales", device)
+    ug = dg = None
+    stride = 0
+    if fmt == NVFP4:
+        if len(up) < 3 or len(down) < 3:
+            raise ValueError("NVFP4 weights need their tensor scales")
+        ug, dg = up[2], down[2]
+        _check_global_scale(ug, "up's tensor scale", device)
+        _check_global_scale(dg, "down's tensor scale", device)
+        if ug.numel() != dg.numel() or ug.numel() not in (1, experts) or not (
+                ug.is_contiguous() and dg.is_contiguous()):
+            raise ValueError("tensor scales are one for all experts or one each, for up and down")
+        stride = 1 if ug.numel() > 1 else 0
+        ug, dg = ug.data_ptr(), dg.data_ptr()
+    return _pack_moe_weights(uc.data_ptr(), us.data_ptr(), dc.data_ptr(), ds.data_ptr(), ug or 0,
+                             dg or 0, hidden, inner, experts, stride)
+
+
+def moe_experts(fmt: int, x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, up, down,
+                out_dtype=None, out=None, workspace=None, check: bool = True,
+                status=None) -> torch.Tensor:
+    """The chosen experts' gated products: x [tokens, hidden] (fp32 or bf16),
+    experts int32 and weights fp32 [tokens, top_k] (moe_route's, or any; -1 for
+    none).  up and down are what the quantizer of fmt returns for [experts, 2
+    inner, hidden] (gate rows, then up rows) and [experts, hidden, inner]: (codes,
+    scales) or, of NVFP4, (codes, scales, tensor scale of 1 or `experts` elements).
+    Returns [tokens, hidden] of x's dtype, or of out_dtype."""
+    if fmt != MXFP4 and fmt != NVFP4:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    if x.dim() != 2 or experts.dim() != 2 or weights.shape != experts.shape:
+        raise ValueError("x must be [tokens, hidden], experts and weights [tokens, top_k]")
+    if not x.is_cuda:
+        raise TypeError("expected device tensors")
+    if experts.dtype is not torch.int32 or weights.dtype is not torch.float32:
+        raise TypeError("experts must be int32, weights float32")
+    device = x.device
+    if experts.device != device or weights.device != device or not (
+            x.is_contiguous() and experts.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("x, experts and weights must be contiguous, on one device")
+    tokens, hidden = x.shape
+    top_k = experts.shape[1]
+    if experts.shape[0] != tokens or down[0].dim() != 3 or down[0].shape[1] != hidden:
+        raise ValueError("experts and weights need x's tokens, the weights x's hidden size")
+    w = _moe_weights(fmt, up, down, device)
+    code = _dtype_code(x.dtype)
+    if out is None:
+        out = torch.empty(tokens, hidden, dtype=out_dtype or x.dtype, device=device)
+    elif (out.shape != x.shape or out.device != device or not out.is_contiguous()
+          or (out_dtype is not None and out.dtype != out_dtype)):
+        raise ValueError("out must be a contiguous tensor of x's shape, of out_dtype")
+    ot = _dtype_code(out.dtype)
+    status = _check_status(status, check, device)
+    if tokens == 0:
+        return out
+    L = _lib or lib()
+    need = L.fp4_moe_experts_workspace_bytes(w, fmt, tokens, top_k, code)
+    workspace, space, size = _workspace(workspace, need, device)
+    _on(x, L.fp4_moe_experts, fmt, w, x.data_ptr(), code, tokens, experts.data_ptr(),
+        weights.data_ptr(), top_k, out.data_ptr(), ot, space, size,
+        None if status is None else status.data_ptr())
+    if check:
+        _raise_flags(int(status.item()))
     return out
 
 

@@ -11,6 +11,7 @@
 #endif
 #include "fp4_kernels.h"
 #include "fp4_kv.h"
+#include "fp4_moe.h"
 
 // Device scratch of fp4_quantize_nvfp4_noalloc, for callers that cannot
 // allocate: the same workspace fp4_quantize_nvfp4 takes from its caller
@@ -78,6 +79,8 @@ hipError_t device_scratch(void **out) {
 constexpr int64_t kMaxTokens = (int64_t)1 << 23;    // rows of a batch
 constexpr int64_t kMaxPositions = (int64_t)1 << 27;  // positions of a sequence's table
 constexpr int32_t kMaxSeqs = 1 << 20;
+constexpr int64_t kMaxMoeTokens = (int64_t)1 << 21;
+static_assert(FP4_FLAG_EXPERT_INDEX == fp4dev::FLAG_EXPERT_INDEX, "the header states the flag");
 static_assert(FP4_FLAG_CACHE_INDEX == fp4dev::FLAG_CACHE_INDEX, "the header states the flag");
 
 // The kernels' forms of a cache and a batch, checked.  A batch without rows is
@@ -532,6 +535,75 @@ fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int
     return from_hip(fp4dev::launch_linear_w4((int)fmt, x, xt == FP4_BF16, M, K, bt_packed, scales,
                                              bt_global_scale, true, N, c, ct == FP4_BF16,
                                              (hipStream_t)stream));
+}
+
+size_t fp4_moe_route_workspace_bytes(int64_t tokens, int64_t hidden, int32_t experts) {
+    if (tokens < 1 || tokens > kMaxMoeTokens || hidden < 8 || hidden % 8 ||
+        hidden > INT32_MAX / 2 || experts < 1 || experts > fp4dev::MOE_EXPERTS)
+        return 0;
+    return fp4dev::route_workspace_bytes(tokens, hidden, experts);
+}
+
+fp4_status fp4_moe_route(const void *x, fp4_dtype xt, int64_t tokens, int64_t hidden,
+                         const void *router, fp4_dtype rt, int32_t experts, int32_t top_k,
+                         int32_t renormalize, int32_t *chosen, float *weights, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    if (!valid_dtype(xt) || !valid_dtype(rt)) return FP4_E_DTYPE;
+    if (renormalize != 0 && renormalize != 1) return FP4_E_ARG;
+    const size_t need = fp4_moe_route_workspace_bytes(tokens, hidden, experts);
+    if (need == 0 || top_k < 1 || top_k > experts || top_k > fp4dev::MOE_TOP_K) return FP4_E_SHAPE;
+    if (!x || !router || !chosen || !weights) return FP4_E_ARG;
+    if (!workspace || workspace_bytes < need) return FP4_E_WORKSPACE;
+    if (!aligned(x, 16) || !aligned(router, 16) || !aligned(chosen, 4) || !aligned(weights, 4) ||
+        !aligned(workspace, 16))
+        return FP4_E_ALIGN;
+    return from_hip(fp4dev::launch_route(x, xt == FP4_BF16, tokens, hidden, router, rt == FP4_BF16,
+                                         experts, top_k, renormalize == 1, chosen, weights,
+                                         workspace, (hipStream_t)stream));
+}
+
+// Sizes that the experts' calls take.
+static bool moe_fits(const fp4_moe_weights *w, fp4_format fmt, int64_t tokens, int32_t top_k) {
+    const int64_t block = fmt == FP4_MXFP4 ? 32 : 16;
+    if (tokens < 1 || tokens > kMaxMoeTokens || top_k < 1 || top_k > fp4dev::MOE_TOP_K) return false;
+    if (w->experts < 1 || w->experts > fp4dev::MOE_EXPERTS) return false;
+    if (w->hidden < 1 || w->hidden % block || w->hidden > INT32_MAX / 4) return false;
+    if (w->inner < 1 || w->inner % block || w->inner > INT32_MAX / 4) return false;
+    return w->hidden <= kMaxElems / 2 / w->inner / w->experts && w->inner <= kMaxElems / tokens / 128;
+}
+
+size_t fp4_moe_experts_workspace_bytes(const fp4_moe_weights *w, fp4_format fmt, int64_t tokens,
+                                       int32_t top_k, fp4_dtype xt) {
+    if (!w || (fmt != FP4_MXFP4 && fmt != FP4_NVFP4) || !valid_dtype(xt)) return 0;
+    if (!moe_fits(w, fmt, tokens, top_k)) return 0;
+    return fp4dev::experts_workspace_bytes(tokens, top_k, w->inner, xt == FP4_BF16);
+}
+
+fp4_status fp4_moe_experts(fp4_format fmt, const fp4_moe_weights *w, const void *x, fp4_dtype xt,
+                           int64_t tokens, const int32_t *experts, const float *weights,
+                           int32_t top_k, void *out, fp4_dtype ot, void *workspace,
+                           size_t workspace_bytes, int32_t *status, void *stream) {
+    if (fmt != FP4_MXFP4 && fmt != FP4_NVFP4) return FP4_E_DTYPE;
+    if (!valid_dtype(xt) || !valid_dtype(ot)) return FP4_E_DTYPE;
+    if (!w || !w->up_codes || !w->up_scales || !w->down_codes || !w->down_scales) return FP4_E_ARG;
+    if (fmt == FP4_NVFP4 && (!w->up_global_scale || !w->down_global_scale)) return FP4_E_ARG;
+    if (w->global_scale_stride != 0 && w->global_scale_stride != 1) return FP4_E_ARG;
+    if (!moe_fits(w, fmt, tokens, top_k)) return FP4_E_SHAPE;
+    if (!x || !experts || !weights || !out) return FP4_E_ARG;
+    const size_t need = fp4_moe_experts_workspace_bytes(w, fmt, tokens, top_k, xt);
+    if (!workspace || workspace_bytes < need) return FP4_E_WORKSPACE;
+    if (!aligned(w->up_codes, 16) || !aligned(w->down_codes, 16) || !aligned(x, 16) ||
+        !aligned(experts, 4) || !aligned(weights, 4) || !aligned(out, ot == FP4_BF16 ? 2 : 4) ||
+        !aligned(workspace, 16) || !aligned(status, 4))
+        return FP4_E_ALIGN;
+    if (fmt == FP4_NVFP4 && (!aligned(w->up_global_scale, 4) || !aligned(w->down_global_scale, 4)))
+        return FP4_E_ALIGN;
+    const fp4dev::MoeWeights W = {w->up_codes, w->up_scales, w->down_codes, w->down_scales,
+                                  w->up_global_scale, w->down_global_scale, w->hidden, w->inner,
+                                  w->experts, w->global_scale_stride};
+    return from_hip(fp4dev::launch_experts((int)fmt, W, x, xt == FP4_BF16, tokens, experts, weights,
+                                           top_k, out, ot == FP4_BF16, workspace, status,
+                                           (hipStream_t)stream));
 }
 
 // fp4_linear_mxfp4 with the grid barrier's poll limit as an argument

@@ -119,6 +119,18 @@ hipError_t launch_linear_w4(int fmt, const void *x, bool x_bf16, int64_t M, int6
                             const uint8_t *codes, const uint8_t *scales, const float *s_g,
                             bool packed, int64_t N, void *c, bool out_bf16, hipStream_t s);
 
+// Mixture of experts (fp4_moe.h): the router's choice, and the experts' products.
+struct MoeWeights;
+size_t route_workspace_bytes(int64_t tokens, int64_t hidden, int experts);
+hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidden,
+                        const void *router, bool router_bf16, int experts, int top_k,
+                        bool renormalize, int32_t *chosen, float *weights, void *workspace,
+                        hipStream_t s);
+size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t inner, bool x_bf16);
+hipError_t launch_experts(int fmt, const MoeWeights &W, const void *x, bool x_bf16, int64_t tokens,
+                          const int32_t *ids, const float *weights, int top_k, void *out,
+                          bool out_bf16, void *workspace, int32_t *status, hipStream_t s);
+
 // The 8-bit key/value cache (fp4_kv.h): the write of new tokens, the read of
 // the same rows, and attention over the cache.  Strides count elements.
 struct KvCache;

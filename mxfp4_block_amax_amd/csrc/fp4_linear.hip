@@ -73,41 +73,17 @@ __global__ __launch_bounds__(1024) void linear_w4_kernel(LinearArgs A) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) w[p] = w4_load_tail<FMT>(rows[p], u, g, A.K);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) top[p] = max(top[p], w[p].scale[h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bf16x8_t v[2] = {w4_decode<FMT>(w[0], h, i), w4_decode<FMT>(w[1], h, i)};
-                const int64_t k = u * W4_UNIT + 128 * h + 8 * i;
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    Terms<NT> b = {};
-                    if (real[t] && (PACKED || k + 32 * stretch < A.K)) b = load_terms(x[t] + k);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) acc[p][t] = mfma_w4(v[p], b.p[n], acc[p][t]);
-                }
-            }
-        }
+w4_multiply<FMT>(
+            w,
+            [&](int t, int k) {
+                Terms<NT> b = {};
+                if (real[t] && (PACKED || u * W4_UNIT + k + 32 * stretch < A.K))
+                    b = load_terms(x[t] + u * W4_UNIT + k);
+                return b;
+            },
+            acc, top);
     }
-    if constexpr (FMT == 0) {
-        // a scale byte of 255 makes its row NaN
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            uint64_t bad = __ballot(top[p] == 255u);
-            if (bad == 0) continue;
-            bad |= bad >> 32;
-            bad |= bad >> 16;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (bad >> (4 * g + i) & 1)
-#pragma unroll
-                    for (int t = 0; t < CT; ++t) acc[p][t][i] = __builtin_nanf("");
-        }
-    }
+    if constexpr (FMT == 0) w4_nan_rows(top, acc);
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll

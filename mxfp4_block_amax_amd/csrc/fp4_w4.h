@@ -233,4 +233,50 @@ __device__ __forceinline__ void w4_load_packed(const uint8_t *codes, const uint8
     }
 }
 
+// One unit: its products with X's activations are added to acc; top takes part in
+// w4_nan_rows.  x(t, k) gives the terms of values k .. k + 7 of the unit for the
+// lane's row of activation tile t.
+template <int FMT, int ROWS, int TILES, typename X>
+__device__ __forceinline__ void w4_multiply(const W4Unit<FMT> (&w)[ROWS], const X &x,
+                                            f32x4_t (&acc)[ROWS][TILES], uint32_t (&top)[ROWS]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int p = 0; p < ROWS; ++p) top[p] = max(top[p], w[p].scale[h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bf16x8_t v[ROWS];
+#pragma unroll
+            for (int p = 0; p < ROWS; ++p) v[p] = w4_decode<FMT>(w[p], h, i);
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                const auto b = x(t, 128 * h + 8 * i);
+#pragma unroll
+                for (auto &term : b.p)
+#pragma unroll
+                    for (int p = 0; p < ROWS; ++p) acc[p][t] = mfma_w4(v[p], term, acc[p][t]);
+            }
+        }
+    }
+}
+
+// A scale byte of 255 in any lane of a row makes the row's sums NaN (MXFP4).
+template <int ROWS, int TILES>
+__device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[ROWS],
+                                            f32x4_t (&acc)[ROWS][TILES]) {
+    const int g = (threadIdx.x & (WAVE - 1)) >> 4;
+#pragma unroll
+    for (int p = 0; p < ROWS; ++p) {
+        uint64_t bad = __ballot(top[p] == 255u);
+        if (bad == 0) continue;
+        bad |= bad >> 32;
+        bad |= bad >> 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bad >> (4 * g + i) & 1)
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) acc[p][t][i] = __builtin_nanf("");
+    }
+}
+
 }  // namespace fp4dev
