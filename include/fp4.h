@@ -708,6 +708,37 @@ typedef struct {
 } fp4_kv_batch;
 
 /*
+ * The norm and position rotation of a batch's new queries and keys, ahead of the
+ * cache and its attention.  For each token and head, with x its head_dim values:
+ *   z = x / sqrt(mean x^2 + eps) * weight      (z = x where weight is NULL)
+ *   (y_a, y_b) = (z_a cos - z_b sin, z_a sin + z_b cos) of position * frequencies[i]
+ * for the pairs i = 0 .. rotary/2 - 1, (a, b) = (i, i + rotary/2), or (2 i, 2 i + 1)
+ * if interleaved; y = z for the values from rotary on.
+ *   q, k        rows in and out (below), fp32 or bf16 (xt), with heads of their own
+ *   wt          the weights' type, fp32 or bf16
+ *   cu_tokens, lengths, seqs, tokens   as in fp4_kv_batch: they give the positions
+ *   frequencies [rotary/2] device doubles, radians per position
+ * head_dim is 64, 128, 192 or 256, rotary a multiple of 16 up to head_dim, eps >= 0.
+ * Sums and rotations are fp32 (rounded once), angles 64-bit.  Rows of no sequence
+ * come out as zeros; so do those at positions below 0, which raise
+ * FP4_FLAG_CACHE_INDEX, as prefix sums that are none do.  One launch.
+ * Deterministic.
+ */
+typedef struct {
+    const void *x;      /* element (t, h, d) at t * x_token_stride + h * x_head_stride + d */
+    void *y;            /* likewise; y == x with equal strides works in place, any other
+                           overlap does not.  Pointers and strides multiples of 16 bytes */
+    int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+    const void *weight; /* [head_dim], 16-byte aligned, or NULL */
+    int32_t heads;      /* 1 .. 65535 */
+} fp4_head_rows;
+fp4_status fp4_norm_rotate(const fp4_head_rows *q, const fp4_head_rows *k, fp4_dtype xt,
+                           fp4_dtype wt, int32_t head_dim, float eps, const int32_t *cu_tokens,
+                           const int32_t *lengths, int32_t seqs, int64_t tokens,
+                           const double *frequencies, int32_t rotary, int32_t interleaved,
+                           int32_t *status, void *stream);
+
+/*
  * Writes the batch's new tokens into the cache.
  *   k, v   fp32 or bf16, element (t, h, d) at t * token_stride + h *
  *          head_stride + d (strides in elements: slices of a fused projection's

@@ -65,7 +65,7 @@ EXPORTS = ("fp4_quantize_mxfp4", "fp4_quantize_mxfp4_rule", "fp4_quantize_nvfp4"
            "fp4_moe_experts_workspace_bytes",
            "fp4_quantize_nvfp4_noalloc", "fp4_workspace_bytes", "fp4_status_str",
            "fp4_kv_cache_write", "fp4_kv_cache_read", "fp4_kv_attention",
-           "fp4_kv_attention_workspace_bytes")
+           "fp4_kv_attention_workspace_bytes", "fp4_norm_rotate")
 
 # fp4_mx_rule: the MXFP4 block-exponent rules
 MX_RULES = {"ocp": 0, "ceil": 1, "mse": 2}
@@ -74,9 +74,11 @@ _lib = None
 
 
 # fp4_kv_cache and fp4_kv_batch as bytes (passed by pointer): packing one takes a
-# third of the time a ctypes.Structure takes to fill; fp4_moe_weights alike
+# third of the time a ctypes.Structure takes to fill; fp4_head_rows
+# and fp4_moe_weights alike
 _pack_kv_cache = struct.Struct("@PPPPqiii4x").pack
 _pack_kv_batch = struct.Struct("@PPPqqii").pack
+_pack_head_rows = struct.Struct("@PPqqqqPi4x").pack
 _pack_moe_weights = struct.Struct("@PPPPPPqqii").pack
 
 
@@ -143,6 +145,8 @@ def lib() -> ctypes.CDLL:
     L.fp4_kv_attention.argtypes = [KC, KB, P, I64, I64, I, I32, F, I32, I32, P, P, P, S, P, P]
     L.fp4_kv_attention_workspace_bytes.argtypes = [KC, KB, I32, I32, I]
     L.fp4_kv_attention_workspace_bytes.restype = S
+    KR = ctypes.c_char_p
+    L.fp4_norm_rotate.argtypes = [KR, KR, I, I, I32, F, P, P, I32, I64, P, I32, I32, P, P]
     L.fp4_workspace_bytes.argtypes = [I, I64, I64]
     L.fp4_workspace_bytes.restype = S
     L.fp4_status_str.argtypes = [I]
@@ -1006,6 +1010,74 @@ def _kv_call(fn, cache, batch, args, check, status):
         _ok(code)
     if check:
         _raise_flags(int(status.item()))
+
+
+def _head_rows(x, y, weight, dim, what):
+    """fp4_head_rows of rows x [tokens, heads, dim] and their output."""
+    if len(x.shape) != 3 or x.shape[2] != dim or y.shape != x.shape:
+        raise ValueError(f"{what} and its output must be [tokens, heads, {dim}]")
+    tokens, heads, _ = x.shape
+    xt, xh, xi = x.stride()
+    yt, yh, yi = y.stride()
+    if xi != 1 or yi != 1:
+        raise ValueError(f"{what} and its output must have a dense last dimension")
+    if tokens < 2:
+        xt = yt = 0
+    if heads < 2:
+        xh = yh = dim
+    return _pack_head_rows(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh,
+                           0 if weight is None else weight.data_ptr(), heads)
+
+
+def norm_rotate(q: torch.Tensor, k: torch.Tensor, cu_tokens: torch.Tensor, lengths: torch.Tensor,
+                frequencies: torch.Tensor, q_weight=None, k_weight=None, eps: float = 1e-6,
+                interleaved: bool = False, out=None, check: bool = True, status=None):
+    """The norm of each head (where a weight [head_dim] is given) and the rotation
+    by position of the batch's new queries and keys, ahead of kv_cache_write and
+    kv_attention.  q [tokens, heads, head_dim] and k [tokens, kv_heads, head_dim]
+    are fp32 or bf16, slices of a projection's rows allowed; cu_tokens [n + 1] and
+    lengths [n] (int32) are the batch's; frequencies float64 [rotary / 2], radians
+    per position.  Returns (q, k), new dense tensors or `out` (out=(q, k): in
+    place)."""
+    device, dtype = q.device, q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    if not q.is_cuda:
+        raise TypeError("expected device tensors")
+    if k.dtype is not dtype or len(q.shape) != 3 or len(k.shape) != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim] of one dtype")
+    if cu_tokens.dtype is not torch.int32 or lengths.dtype is not torch.int32:
+        raise TypeError("cu_tokens and lengths must be int32 tensors")
+    if frequencies.dtype is not torch.float64:
+        raise TypeError("frequencies must be a float64 tensor")
+    tokens, _, dim = q.shape
+    seqs = lengths.shape[0] if lengths.dim() == 1 else -1
+    if cu_tokens.shape != (seqs + 1,) or frequencies.dim() != 1 or k.shape[0] != tokens:
+        raise ValueError("lengths has n entries, cu_tokens n + 1; q and k have the same tokens")
+    out_q, out_k = (torch.empty(q.shape, dtype=dtype, device=device),
+                    torch.empty(k.shape, dtype=dtype, device=device)) if out is None else out
+    if out_q.dtype is not dtype or out_k.dtype is not dtype:
+        raise ValueError("out must have q's dtype")
+    weight = F32
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    for w in given:
+        if w.shape != (dim,) or w.dtype is not given[0].dtype:
+            raise ValueError("weights must be [head_dim], of one dtype")
+        weight = _dtype_code(w.dtype)
+    for t in (k, cu_tokens, lengths, frequencies, out_q, out_k, *given):
+        if t.device != device:
+            raise ValueError("all tensors must be on q's device")
+    if not all(t.is_contiguous() for t in (cu_tokens, lengths, frequencies, *given)):
+        raise ValueError("cu_tokens, lengths, frequencies and weights must be dense")
+    status = _check_status(status, check, device)
+    _on(q, (_lib or lib()).fp4_norm_rotate, _head_rows(q, out_q, q_weight, dim, "q"),
+        _head_rows(k, out_k, k_weight, dim, "k"), code, weight, dim, eps, cu_tokens.data_ptr(),
+        lengths.data_ptr(), seqs, tokens, frequencies.data_ptr(), 2 * frequencies.shape[0],
+        1 if interleaved else 0, None if status is None else status.data_ptr())
+    if check:
+        _raise_flags(int(status.item()))
+    return out_q, out_k
 
 
 def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor,

@@ -12,6 +12,7 @@
 #include "fp4_kernels.h"
 #include "fp4_kv.h"
 #include "fp4_moe.h"
+#include "fp4_rotate.h"
 
 // Device scratch of fp4_quantize_nvfp4_noalloc, for callers that cannot
 // allocate: the same workspace fp4_quantize_nvfp4 takes from its caller
@@ -726,6 +727,49 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(status, 4)) return FP4_E_ALIGN;
     return from_hip(fp4dev::launch_kv_read(C, B, k, v, yt == FP4_BF16, status,
                                            (hipStream_t)stream));
+}
+
+// One side of fp4_norm_rotate, checked.
+static fp4_status head_rows(const fp4_head_rows *r, fp4_dtype xt, int64_t dim,
+                            fp4dev::HeadRows *R) {
+    if (r->heads < 1 || r->heads > 65535) return FP4_E_SHAPE;
+    if (!r->x || !r->y) return FP4_E_ARG;
+    fp4_status st = kv_rows(r->x, r->x_token_stride, r->x_head_stride, xt, dim);
+    if (st == FP4_OK) st = kv_rows(r->y, r->y_token_stride, r->y_head_stride, xt, dim);
+    if (st != FP4_OK) return st;
+    if (!aligned(r->weight, 16)) return FP4_E_ALIGN;
+    *R = {r->x, r->y, r->x_token_stride, r->x_head_stride, r->y_token_stride, r->y_head_stride,
+          r->weight, r->heads};
+    return FP4_OK;
+}
+
+fp4_status fp4_norm_rotate(const fp4_head_rows *q, const fp4_head_rows *k, fp4_dtype xt,
+                           fp4_dtype wt, int32_t head_dim, float eps, const int32_t *cu_tokens,
+                           const int32_t *lengths, int32_t seqs, int64_t tokens,
+                           const double *frequencies, int32_t rotary, int32_t interleaved,
+                           int32_t *status, void *stream) {
+    if (!q || !k || !cu_tokens || !lengths || !frequencies) return FP4_E_ARG;
+    if (!valid_dtype(xt) || !valid_dtype(wt)) return FP4_E_DTYPE;
+    if (interleaved != 0 && interleaved != 1) return FP4_E_ARG;
+    if (!(eps >= 0.0f && eps < __builtin_inff())) return FP4_E_ARG;
+    if (head_dim < 64 || head_dim > 256 || head_dim % 64) return FP4_E_SHAPE;
+    if (rotary < 16 || rotary > head_dim || rotary % 16) return FP4_E_SHAPE;
+    if (seqs < 1 || seqs > kMaxSeqs || tokens < 0 || tokens > kMaxTokens) return FP4_E_SHAPE;
+    if (!aligned(cu_tokens, 4) || !aligned(lengths, 4) || !aligned(frequencies, 8) ||
+        !aligned(status, 4))
+        return FP4_E_ALIGN;
+    if (tokens == 0) return FP4_OK;
+    fp4dev::RotateArgs A;
+    fp4_status st = head_rows(q, xt, head_dim, &A.q);
+    if (st == FP4_OK) st = head_rows(k, xt, head_dim, &A.k);
+    if (st != FP4_OK) return st;
+    A.frequencies = frequencies;
+    A.eps = eps;
+    A.rotary = rotary;
+    A.weight_f32 = wt == FP4_F32;
+    return from_hip(fp4dev::launch_norm_rotate(A, cu_tokens, lengths, seqs, (int32_t)tokens,
+                                               head_dim, xt == FP4_BF16, interleaved == 1, status,
+                                               (hipStream_t)stream));
 }
 
 size_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache *cache, const fp4_kv_batch *batch,

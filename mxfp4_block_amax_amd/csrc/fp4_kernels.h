@@ -147,4 +147,11 @@ hipError_t launch_attention(const KvCache &C, const KvBatch &B, const void *q, i
                             int window, void *out, float *lse, void *workspace, int32_t *status,
                             hipStream_t s);
 
+// The norm and rotation of queries and keys (fp4_rotate.h), rows [tokens, heads,
+// dim] of the batch that cu and lengths describe.
+struct RotateArgs;
+hipError_t launch_norm_rotate(const RotateArgs &A, const int32_t *cu, const int32_t *lengths,
+                              int32_t seqs, int32_t tokens, int dim, bool bf16, bool interleaved,
+                              int32_t *status, hipStream_t s);
+
 }  // namespace fp4dev
