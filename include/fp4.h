@@ -519,7 +519,7 @@ fp4_status fp4_linear_mxfp4(const void *x, fp4_dtype xt, int64_t M, int64_t K,
  * Products are exact: a weight's value fits bf16 (MXFP4 for scale bytes up to
  * 252), fp32 activations count with all their bits.  Sums are fp32, their order
  * is fixed: deterministic.  A NaN scale byte makes its row's outputs NaN.  K is
- * a multiple of the block (32 or 16); any M and N.  The weight is read once
+ * a multiple of the block (32 or 16) up to 2^20, M up to 2^19.  The weight is read once
  * for every 64 tokens, which bounds the time: for long prompts the W4A4
  * layers are faster.  One launch.
  */
@@ -550,7 +550,7 @@ fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int
  *   x          [tokens, hidden] fp32 or bf16     router [experts, hidden] fp32 or bf16
  *   chosen     [tokens, top_k] int32             weights [tokens, top_k] fp32
  *   workspace  fp4_moe_route_workspace_bytes(...) bytes, scratch
- * hidden is a multiple of 8; at most 1024 experts, 32 of a token, 2^21 tokens; x,
+ * hidden is a multiple of 8; at most 1024 experts, 32 of a token, 2^20 tokens; x,
  * router and workspace 16-byte aligned.  Sums are 64-bit, their order is fixed:
  * deterministic.  A NaN logit is below every other.  Two launches.
  */

@@ -113,8 +113,6 @@ hipError_t launch_linear_mxfp4(const void *x, bool x_bf16, const uint8_t *bt_cod
 
 // Linear layer of few tokens: x [M, K] times Bt [N, K] in FP4 (row-major, or
 // packed: codes and scales are then the two parts of the packed operand).
-// linear_w4_fits: the tiles of M x N fit a grid.
-bool linear_w4_fits(int64_t M, int64_t N);
 hipError_t launch_linear_w4(int fmt, const void *x, bool x_bf16, int64_t M, int64_t K,
                             const uint8_t *codes, const uint8_t *scales, const float *s_g,
                             bool packed, int64_t N, void *c, bool out_bf16, hipStream_t s);

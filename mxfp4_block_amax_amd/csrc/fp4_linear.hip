@@ -16,107 +16,123 @@ struct LinearArgs {
     const uint8_t *codes, *scales;  // packed: of the row tiles
     const float *s_g;
     void *c;
-    int64_t M, N, K;
-    int32_t row_tiles;
+    int32_t M, N, K;
     bool out_bf16;
 };
 
 constexpr int LINEAR_ROWS = 32;  // weight rows of a workgroup
+constexpr int LINEAR_WAVES = 16;
 
-// A workgroup has 32 weight rows and up to 16 CT tokens; its waves take units of
-// 256 K in turn, and add their sums in LDS in the order of the waves.
-template <int FMT, bool X_F32, bool PACKED, int CT>
-__global__ __launch_bounds__(1024) void linear_w4_kernel(LinearArgs A) {
+// Waves of a workgroup: 16, or 8 where more tokens leave registers or LDS for no more.
+template <bool X_F32, int TOKENS>
+constexpr int tile_waves() {
+    return TOKENS > 8 || (X_F32 && TOKENS > 4) ? 8 : LINEAR_WAVES;
+}
+
+// Up to TOKENS (16 at most) tokens and 32 weight rows a workgroup: its waves take
+// groups of K in turn, and add their sums in LDS in the
+// order of the waves.  The loop is short: instructions that run once come from memory,
+// and a longer one took 4 us more for a call of 1 x 512 x 2048.
+template <int FMT, bool X_F32, bool PACKED, int TOKENS, int WAVES>
+__global__ __launch_bounds__(WAVES *WAVE) void linear_w4_kernel(LinearArgs A) {
     using XT = std::conditional_t<X_F32, float, uint16_t>;
-    constexpr int NT = X_F32 ? 3 : 1;
-    extern __shared__ f32x4_t sums[];  // [waves][2][CT][64]
-    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
-    const int waves = blockDim.x / WAVE;
-    const int r = lane & 15, g = lane >> 4;
-    const int tile = blockIdx.x % A.row_tiles;
-    const int64_t m0 = (int64_t)(blockIdx.x / A.row_tiles) * (16 * CT);
-    const int64_t n0 = (int64_t)tile * LINEAR_ROWS;
+    using X = XPart<X_F32, TOKENS>;
+    extern __shared__ u32x4_t lds[];
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    constexpr int waves = WAVES;
+    const int m0 = blockIdx.y * TOKENS, row0 = blockIdx.x * LINEAR_ROWS, K = A.K;
+    const int tokens = min(TOKENS, A.M - m0);
 
-    W4Row<FMT> rows[2];
-    const uint8_t *packed_codes = nullptr, *packed_scales = nullptr;
-    if constexpr (PACKED) {
-        packed_codes = A.codes + n0 * (A.K / 2);
-        packed_scales = A.scales + n0 * (A.K / (FMT == 0 ? 32 : 16));
-    } else {
+    const Rsrc x = span((const XT *)A.x + (int64_t)m0 * K, tokens * K * (int)sizeof(XT));
+    uint32_t x_at[X::LOADS];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            // rows past the last one read the last one's, for sums that are not stored
-            const int64_t n = min(n0 + 16 * p + r, A.N - 1);
-            rows[p] = {A.codes + n * (A.K / 2), A.scales + n * (A.K / (FMT == 0 ? 32 : 16))};
-        }
+    for (int n = 0; n < X::LOADS; ++n) {
+        const auto p = X::place(n);
+        x_at[n] = (uint32_t)(p.row * K + p.k) * (uint32_t)sizeof(XT);
     }
-    const int stretch = PACKED ? packed_stretch(g) : g;
-    const XT *x[CT];
-    bool real[CT];
-#pragma unroll
-    for (int t = 0; t < CT; ++t) {
-        real[t] = m0 + 16 * t + r < A.M;
-        x[t] = (const XT *)A.x + (m0 + 16 * t + r) * A.K + 32 * stretch;
-    }
+    constexpr int BLK = FMT == 0 ? 32 : 16;
+    using W = std::conditional_t<PACKED, PackedAt<FMT>, RowsAt<FMT, 2>>;
+    u32x4_t *mine = lds + wave * (X::PIECES + W::LDS);
+    const uint8_t *codes = A.codes + (int64_t)row0 * (K / 2);
+    const uint8_t *scales = A.scales + (int64_t)row0 * (K / BLK);
 
-    f32x4_t acc[2][CT] = {};
+    f32x4_t acc[2][1] = {};
     uint32_t top[2] = {0, 0};
-    const int64_t units = (A.K + W4_UNIT - 1) / W4_UNIT, full = A.K / W4_UNIT;
-    for (int64_t u = wave; u < units; u += waves) {
-        W4Unit<FMT> w[2];
-        if constexpr (PACKED) {
-            w4_load_packed<FMT>(packed_codes, packed_scales, u, lane, w);
-        } else if (u < full) {
+    const int groups = (uint32_t)K / W4_GROUP;
+    const W weights = [&] {
+        if constexpr (PACKED) return W(codes, scales, K);
+        else return W(codes, scales, A.N - row0, 16, K, mine + X::PIECES);
+    }();
+    multiply_groups<FMT, PACKED, W, X>(
+        [&](int n) {
+            Group<W, X> a = {weights, (uint32_t)(n * W4_GROUP), {}};
 #pragma unroll
-            for (int p = 0; p < 2; ++p) w[p] = w4_load<FMT>(rows[p], u, g);
-        } else {
+            for (int i = 0; i < X::LOADS; ++i) a.x_at[i] = x_at[i];
+            return a;
+        },
+        x, mine, wave, waves, groups, acc, top, [](int) {});
+    if constexpr (!PACKED) {
+        // the stretches past the last whole group, by the waves that have fewer groups
+        const int r = lane & 15, g = lane >> 4;
+        int t = (wave - groups % waves + waves) % waves;
+        for (int k = groups * W4_GROUP + W4_STRETCH * t; k < K; k += W4_STRETCH * waves) {
+            W4Unit w[2];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) w[p] = w4_load_tail<FMT>(rows[p], u, g, A.K);
+            for (int p = 0; p < 2; ++p) {
+                const int n = min(16 * p + r, A.N - 1 - row0);
+                w[p] = load_tail<FMT>(codes + (int64_t)n * (K / 2), scales + (int64_t)n * (K / BLK), k, K);
+            }
+            Terms<X::TERMS> b[4] = {};
+            const int at = k + 32 * g;
+            if (r < tokens)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at + 8 * i < K)
+                        b[i] = load_terms((const XT *)A.x + (int64_t)(m0 + r) * K + at + 8 * i);
+            w4_multiply<FMT, X::TERMS>(w, [&](int, int i, int n) { return b[i].p[n]; }, acc, top);
         }
-w4_multiply<FMT>(
-            w,
-            [&](int t, int k) {
-                Terms<NT> b = {};
-                if (real[t] && (PACKED || u * W4_UNIT + k + 32 * stretch < A.K))
-                    b = load_terms(x[t] + u * W4_UNIT + k);
-                return b;
-            },
-            acc, top);
     }
     if constexpr (FMT == 0) w4_nan_rows(top, acc);
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int t = 0; t < CT; ++t) sums[((wave * 2 + p) * CT + t) * WAVE + lane] = acc[p][t];
     __syncthreads();
-    const float s_g = FMT == 0 ? 1.0f : *A.s_g;
-    for (int i = threadIdx.x; i < 2 * CT * WAVE; i += blockDim.x) {
-        f32x4_t s = sums[i];
-        for (int w = 1; w < waves; ++w) s += sums[w * 2 * CT * WAVE + i];
-        const int p = i / (CT * WAVE), t = i / WAVE % CT, l = i % WAVE;
-        const int64_t m = m0 + 16 * t + (l & 15), n = n0 + 16 * p + 4 * (l >> 4);
-        if (m >= A.M) continue;
+    f32x4_t *sums = (f32x4_t *)lds;  // [waves][2][64]
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (n + j >= A.N) break;
-            const float y = FMT == 0 ? s[j] : s[j] * s_g;
-            if (A.out_bf16) ((__bf16 *)A.c)[m * A.N + n + j] = (__bf16)y;
-            else ((float *)A.c)[m * A.N + n + j] = y;
-        }
+    for (int p = 0; p < 2; ++p) sums[(wave * 2 + p) * WAVE + lane] = acc[p][0];
+    __syncthreads();
+    // four sums at a time: a wave has 64 / 4 outputs' quarters
+    if (wave >= 2) return;
+    f32x4_t s = sums[wave * WAVE + lane];
+    for (int v = 1; v < waves; ++v) s += sums[(v * 2 + wave) * WAVE + lane];
+    const int m = m0 + (lane & 15), n = row0 + 16 * wave + 4 * (lane >> 4);
+    if ((lane & 15) >= tokens) return;
+    if constexpr (FMT == 1) s = s * *A.s_g;
+    const int64_t to = (int64_t)m * A.N + n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (n + j >= A.N) break;
+        if (A.out_bf16) ((__bf16 *)A.c)[to + j] = (__bf16)s[j];
+        else ((float *)A.c)[to + j] = s[j];
     }
+}
+
+template <int FMT, bool X_F32, bool PACKED, int TOKENS>
+hipError_t launch_tile(const LinearArgs &A, hipStream_t s) {
+    constexpr int waves = tile_waves<X_F32, TOKENS>();
+    const size_t pieces =
+        (size_t)waves * (XPart<X_F32, TOKENS>::PIECES + (PACKED ? 0 : RowsAt<FMT, 2>::LDS)) * 16;
+    const size_t sums = (size_t)waves * 2 * WAVE * sizeof(f32x4_t);
+    const dim3 grid((uint32_t)((A.N + LINEAR_ROWS - 1) / LINEAR_ROWS),
+                    (uint32_t)((A.M + TOKENS - 1) / TOKENS));
+    linear_w4_kernel<FMT, X_F32, PACKED, TOKENS, waves>
+        <<<grid, waves * WAVE, pieces > sums ? pieces : sums, s>>>(A);
+    return hipGetLastError();
 }
 
 template <int FMT, bool X_F32, bool PACKED>
 hipError_t launch_tokens(const LinearArgs &A, hipStream_t s) {
-    const int ct = A.M <= 16 ? 1 : A.M <= 32 ? 2 : 4;
-    const int64_t token_tiles = (A.M + 16 * ct - 1) / (16 * ct);
-    const int waves = ct == 4 ? 8 : 16;
-    const dim3 grid((uint32_t)(A.row_tiles * token_tiles)), block(waves * WAVE);
-    const size_t lds = (size_t)waves * 2 * ct * WAVE * sizeof(f32x4_t);
-    if (ct == 1) linear_w4_kernel<FMT, X_F32, PACKED, 1><<<grid, block, lds, s>>>(A);
-    else if (ct == 2) linear_w4_kernel<FMT, X_F32, PACKED, 2><<<grid, block, lds, s>>>(A);
-    else linear_w4_kernel<FMT, X_F32, PACKED, 4><<<grid, block, lds, s>>>(A);
-    return hipGetLastError();
+    if (A.M <= 4) return launch_tile<FMT, X_F32, PACKED, 4>(A, s);
+    if (A.M <= 8) return launch_tile<FMT, X_F32, PACKED, 8>(A, s);
+    return launch_tile<FMT, X_F32, PACKED, 16>(A, s);
 }
 
 template <int FMT, bool PACKED>
@@ -126,21 +142,13 @@ hipError_t launch_types(const LinearArgs &A, bool x_bf16, hipStream_t s) {
 
 }  // namespace
 
-bool linear_w4_fits(int64_t M, int64_t N) {
-    const int64_t rows = (N + LINEAR_ROWS - 1) / LINEAR_ROWS, tokens = (M + 15) / 16;
-    return rows <= INT32_MAX / tokens;
-}
-
 hipError_t launch_linear_w4(int fmt, const void *x, bool x_bf16, int64_t M, int64_t K,
                             const uint8_t *codes, const uint8_t *scales, const float *s_g,
                             bool packed, int64_t N, void *c, bool out_bf16, hipStream_t s) {
-    const int32_t row_tiles = (int32_t)((N + LINEAR_ROWS - 1) / LINEAR_ROWS);
-    const LinearArgs A = {x, codes, scales, s_g, c, M, N, K, row_tiles, out_bf16};
+    const LinearArgs A = {x, codes, scales, s_g, c, (int32_t)M, (int32_t)N, (int32_t)K, out_bf16};
     if (fmt == 0)
-        return packed ? launch_types<0, true>(A, x_bf16, s)
-                      : launch_types<0, false>(A, x_bf16, s);
-    return packed ? launch_types<1, true>(A, x_bf16, s)
-                  : launch_types<1, false>(A, x_bf16, s);
+        return packed ? launch_types<0, true>(A, x_bf16, s) : launch_types<0, false>(A, x_bf16, s);
+    return packed ? launch_types<1, true>(A, x_bf16, s) : launch_types<1, false>(A, x_bf16, s);
 }
 
 }  // namespace fp4dev

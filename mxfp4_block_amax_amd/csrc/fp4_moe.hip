@@ -144,6 +144,7 @@ __global__ __launch_bounds__(WAVE) void route_choose_kernel(const double *logits
 
 // ---- experts ----------------------------------------------------------------
 constexpr int MOE_BLOCK = 64;  // tokens that share a reading of the weights
+constexpr size_t LDS_BYTES = 160 * 1024 - 256;  // of a workgroup, but for small fixed arrays
 
 struct MoeArgs {
     const void *x;
@@ -187,19 +188,43 @@ __device__ __forceinline__ void store_terms(uint16_t *p, int64_t stride, float v
     }
 }
 
+// The products of what K has past its last whole group, stretch k of weight rows base
+// + the lane's row; x(at, i) gives the terms of values at .. at + 7.
+template <int FMT, int TERMS, int PARTS, typename RowOf, typename X>
+__device__ __forceinline__ void multiply_tail(const uint8_t *codes, const uint8_t *scales, int k, int K,
+                                              const RowOf &row_of, const X &x,
+                                              f32x4_t (&acc)[PARTS][1], uint32_t (&top)[PARTS]) {
+    constexpr int BLK = FMT == 0 ? 32 : 16;
+    const int lane = threadIdx.x & (WAVE - 1), at = k + 32 * (lane >> 4);
+    W4Unit w[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        const int64_t row = row_of(p, lane & 15);
+        w[p] = load_tail<FMT>(codes + row * (K / 2), scales + row * (K / BLK), k, K);
+    }
+    Terms<TERMS> b[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (at + 8 * i < K) b[i] = x(at + 8 * i);
+    w4_multiply<FMT, TERMS>(w, [&](int, int i, int n) { return b[i].p[n]; }, acc, top);
+}
+
 constexpr int UP_WAVES = 8;
 
 // Gate and up: a workgroup has 16 rows of each of one expert and the tokens of a
-// block that go there, 16 CT of them at a time; its waves share K = hidden.
-template <int FMT, bool X_F32, int CT>
-__global__ __launch_bounds__(UP_WAVES *WAVE) void moe_up_kernel(MoeArgs A, int32_t *status) {
+// block that go there, up to TOKENS of them at a time; its waves share K = hidden.
+template <int FMT, bool X_F32, int TOKENS>
+__global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_kernel(MoeArgs A,
+                                                                                    int32_t *status) {
     using XT = std::conditional_t<X_F32, float, uint16_t>;
-    constexpr int NT = X_F32 ? 3 : 1, NA = X_F32 ? 3 : 2;
-    constexpr int BLK = FMT == 0 ? 32 : 16;
-    __shared__ f32x4_t sums[UP_WAVES][2][CT][WAVE];
+    using X = XPart<X_F32, TOKENS>;
+    using W = RowsAt<FMT, 2>;
+    constexpr int NA = X_F32 ? 3 : 2, BLK = FMT == 0 ? 32 : 16;
+    extern __shared__ u32x4_t lds[];
     __shared__ uint16_t list[MOE_BLOCK];
     __shared__ int count;
-    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), waves = blockDim.x / WAVE;
     const int r = lane & 15, g = lane >> 4;
     const int64_t token0 = (int64_t)blockIdx.z * MOE_BLOCK;
     const int block = (int)min((int64_t)MOE_BLOCK, A.tokens - token0);
@@ -216,10 +241,10 @@ __global__ __launch_bounds__(UP_WAVES *WAVE) void moe_up_kernel(MoeArgs A, int32
             return;
         }
         bool earlier = false;
-        for (int p = threadIdx.x; p < slot; p += UP_WAVES * WAVE) earlier = earlier || ids[p] == e;
+        for (int p = threadIdx.x; p < slot; p += blockDim.x) earlier = earlier || ids[p] == e;
         if (__syncthreads_or(earlier)) return;
     } else if (blockIdx.x == 0 && e == 0) {
-        for (int p = threadIdx.x; p < pairs; p += UP_WAVES * WAVE)
+        for (int p = threadIdx.x; p < pairs; p += blockDim.x)
             if (ids[p] < -1 || ids[p] >= A.W.experts) flag(status, FLAG_EXPERT_INDEX);
     }
     if (wave == 0) {
@@ -227,186 +252,249 @@ __global__ __launch_bounds__(UP_WAVES *WAVE) void moe_up_kernel(MoeArgs A, int32
         if (lane == 0) count = n;
     }
     __syncthreads();
-    const int n = count;
+    const int n = __builtin_amdgcn_readfirstlane(count);
     if (n == 0) return;
 
-    const int64_t K = A.W.hidden, inner = A.W.inner;
-    const int64_t row0 = (int64_t)blockIdx.x * 16;
-    W4Row<FMT> rows[2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const int64_t row = ((int64_t)e * 2 + p) * inner + row0 + r;
-        rows[p] = {A.W.up_codes + row * (K / 2), A.W.up_scales + row * (K / BLK)};
-    }
+    const int K = (int)A.W.hidden, inner = (int)A.W.inner, row0 = blockIdx.x * 16;
+    const int64_t base = (int64_t)e * 2 * inner + row0;
+    const uint8_t *codes = A.W.up_codes + base * (K / 2), *scales = A.W.up_scales + base * (K / BLK);
+    const XT *x0 = (const XT *)A.x + token0 * K;
+    const Rsrc x = span(x0, block * K * (int)sizeof(XT));
+    u32x4_t *mine = lds + wave * (X::PIECES + W::LDS);
+    const W weights(codes, scales, inner + 16, inner, K, mine + X::PIECES);
     const float s_g = FMT == 0 ? 1.0f : A.W.up_global[(int64_t)e * A.W.global_stride];
-    const int64_t units = (K + W4_UNIT - 1) / W4_UNIT, full = K / W4_UNIT;
-    for (int c0 = 0; c0 < n; c0 += 16 * CT) {
-        const XT *x[CT];
-        bool real[CT];
+    const int groups = K / W4_GROUP;
+    for (int c0 = 0; c0 < n; c0 += TOKENS) {
+        const int rows = min(n - c0, TOKENS);
+        Group<W, X> a = {weights, 0, {}};
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            real[t] = c0 + 16 * t + r < n;
-            const int64_t token = token0 + (real[t] ? list[c0 + 16 * t + r] / A.top_k : 0);
-            x[t] = (const XT *)A.x + token * K + 32 * g;
+        for (int i = 0; i < X::LOADS; ++i) {
+            const auto p = X::place(i);
+            a.x_at[i] = p.row < rows ? (uint32_t)(list[c0 + p.row] / A.top_k * K + p.k) * (uint32_t)sizeof(XT)
+                                     : NOWHERE;
         }
-        f32x4_t acc[2][CT] = {};
+        f32x4_t acc[2][1] = {};
         uint32_t top[2] = {0, 0};
-        for (int64_t u = wave; u < units; u += UP_WAVES) {
-            W4Unit<FMT> w[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-                w[p] = u < full ? w4_load<FMT>(rows[p], u, g) : w4_load_tail<FMT>(rows[p], u, g, K);
-            w4_multiply<FMT>(
-                w,
-                [&](int t, int k) {
-                    Terms<NT> b = {};
-                    if (real[t] && u * W4_UNIT + k + 32 * g < K) b = load_terms(x[t] + u * W4_UNIT + k);
+        multiply_groups<FMT, false, W, X>(
+            [&](int q) {
+                a.k = q * W4_GROUP;
+                return a;
+            },
+            x, mine, wave, waves, groups, acc, top, [](int) {});
+        const int t = (wave - groups % waves + waves) % waves;
+        for (int k = groups * W4_GROUP + W4_STRETCH * t; k < K; k += W4_STRETCH * waves)
+            multiply_tail<FMT, X::TERMS>(
+                codes, scales, k, K, [&](int p, int row) { return (int64_t)p * inner + row; },
+                [&](int at) {
+                    Terms<X::TERMS> b = {};
+                    if (r < rows) b = load_terms(x0 + list[c0 + r] / A.top_k * (int64_t)K + at);
                     return b;
                 },
                 acc, top);
-        }
         if constexpr (FMT == 0) w4_nan_rows(top, acc);
-        if (c0 > 0) __syncthreads();
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int t = 0; t < CT; ++t) sums[wave][p][t][lane] = acc[p][t];
         __syncthreads();
-        for (int i = threadIdx.x; i < CT * WAVE; i += UP_WAVES * WAVE) {
-            const int t = i / WAVE, l = i & (WAVE - 1);
-            if (c0 + 16 * t + (l & 15) >= n) continue;
-            f32x4_t gate = sums[0][0][t][l], up = sums[0][1][t][l];
+        f32x4_t *sums = (f32x4_t *)lds;  // [waves][2][64]
 #pragma unroll
-            for (int w = 1; w < UP_WAVES; ++w) gate += sums[w][0][t][l], up += sums[w][1][t][l];
-            const int64_t pair = token0 * A.top_k + list[c0 + 16 * t + (l & 15)];
-            uint16_t *a = A.act + pair * NA * inner + row0 + 4 * (l >> 4);
+        for (int p = 0; p < 2; ++p) sums[(wave * 2 + p) * WAVE + lane] = acc[p][0];
+        __syncthreads();
+        if (wave == 0 && r < rows) {
+            f32x4_t gate = sums[lane], up = sums[WAVE + lane];
+            for (int v = 1; v < waves; ++v) {
+                gate += sums[v * 2 * WAVE + lane];
+                up += sums[(v * 2 + 1) * WAVE + lane];
+            }
+            const int64_t pair = token0 * A.top_k + list[c0 + r];
+            uint16_t *to = A.act + pair * NA * inner + row0 + 4 * g;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float gj = gate[j] * s_g, uj = up[j] * s_g;
-                store_terms<NA>(a + j, inner, gj / (1.0f + expf(-gj)) * uj);
+                store_terms<NA>(to + j, inner, gj / (1.0f + expf(-gj)) * uj);
             }
         }
+        __syncthreads();
     }
 }
 
+// What a block's tokens want, in LDS: its (token, expert) pairs sorted by expert, a
+// token that names an expert twice once, in its first slot, with both weights; and
+// items, an expert and up to TOKENS of its pairs each.
+struct MoeItem {
+    uint16_t expert, first, count, pad;
+};
+struct MoePlan {
+    MoeItem *items;     // [pairs]
+    float *share;       // [pairs]
+    uint32_t *used;     // [experts]: pairs of an expert; later where its next one goes
+    uint16_t *pair;     // [pairs]
+    __host__ __device__ static size_t bytes(int pairs, int experts) {
+        return ((size_t)pairs * (sizeof(MoeItem) + 4 + 2) + (size_t)experts * 4 + 15) / 16 * 16;
+    }
+    __device__ MoePlan(void *p, int pairs, int experts)
+        : items((MoeItem *)p), share((float *)(items + pairs)), used((uint32_t *)(share + pairs)),
+          pair((uint16_t *)(used + experts)) {}
+};
+
 constexpr int DOWN_WAVES = 16;
-constexpr int MOE_IDS = MOE_BLOCK * MOE_TOP_K;
+static_assert(DOWN_WAVES * WAVE >= MOE_EXPERTS, "a thread an expert");
 
-// Down and the weighted sum: a workgroup has 16 rows of every expert that a
-// block's tokens go to; its waves share the experts' K = inner, one after the
-// other, and keep the tokens' sums over the experts.  A token that an expert does
-// not have takes nothing of it, not a zero times its values.
-template <int FMT, bool X_F32, int CT>
-__global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A) {
-    constexpr int NA = X_F32 ? 3 : 2;
-    constexpr int BLK = FMT == 0 ? 32 : 16;
-    __shared__ union {
-        struct {
-            int32_t ids[MOE_IDS];
-            uint32_t seen[MOE_EXPERTS / 32];
-            uint16_t active[MOE_EXPERTS];
-        } plan;
-        f32x4_t sums[DOWN_WAVES][CT][WAVE];
-    } sh;
-    __shared__ int count;
-    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
+// Returns the items.
+template <int TOKENS>
+__device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *weights, int pairs,
+                         int top_k, int experts) {
+    __shared__ uint32_t wave_sum[DOWN_WAVES];
+    const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, me = threadIdx.x;
+    if (me < experts) plan.used[me] = 0;
+    __syncthreads();
+    const auto first_of = [&](int p, int e) {
+        for (int q = p / top_k * top_k; q < p; ++q)
+            if (ids[q] == e) return false;
+        return e >= 0 && e < experts;
+    };
+    for (int p = me; p < pairs; p += DOWN_WAVES * WAVE) {
+        const int e = ids[p];
+        if (first_of(p, e)) atomicAdd(&plan.used[e], 1u);
+    }
+    __syncthreads();
+    // pairs (low half) and items (high half) of the experts before: both below 2^16
+    const uint32_t n = me < experts ? plan.used[me] : 0;
+    const uint32_t own = n | (n + TOKENS - 1) / TOKENS << 16;
+    uint32_t before = own;
+    for (int off = 1; off < WAVE; off <<= 1) {
+        const uint32_t below = __shfl_up(before, off, WAVE);
+        if (lane >= off) before += below;
+    }
+    if (lane == WAVE - 1) wave_sum[wave] = before;
+    before -= own;
+    __syncthreads();
+    uint32_t all = 0;
+    for (int w = 0; w < DOWN_WAVES; ++w) {
+        if (w < wave) before += wave_sum[w];
+        all += wave_sum[w];
+    }
+    const uint32_t start = before & 0xFFFFu, item = before >> 16;
+    if (me < experts) {
+        plan.used[me] = start;
+        for (uint32_t i = 0; i * TOKENS < n; ++i)
+            plan.items[item + i] = {(uint16_t)me, (uint16_t)(start + i * TOKENS),
+                                    (uint16_t)min(n - i * TOKENS, (uint32_t)TOKENS), 0};
+    }
+    __syncthreads();
+    for (int p = me; p < pairs; p += DOWN_WAVES * WAVE) {
+        const int e = ids[p];
+        if (first_of(p, e)) plan.pair[atomicAdd(&plan.used[e], 1u)] = (uint16_t)p;
+    }
+    __syncthreads();
+    // in order, whatever order the pairs came in, and each with its weights' sum
+    if (me < experts && n > 0) {
+        for (uint32_t i = 1; i < n; ++i) {
+            const uint16_t p = plan.pair[start + i];
+            uint32_t j = i;
+            for (; j > 0 && plan.pair[start + j - 1] > p; --j) plan.pair[start + j] = plan.pair[start + j - 1];
+            plan.pair[start + j] = p;
+        }
+        for (uint32_t i = 0; i < n; ++i) {
+            const int p = plan.pair[start + i], end = (p / top_k + 1) * top_k;
+            float s = weights[p];
+            for (int q = p + 1; q < end; ++q)
+                if (ids[q] == me) s += weights[q];
+            plan.share[start + i] = s;
+        }
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(all >> 16);
+}
+
+// Down and the weighted sum.  A workgroup has 16 rows and a block's tokens; its waves
+// go through the items' groups of K = inner in turn.  A wave adds each group's sums,
+// weighted, to its own of the tokens, in LDS: a token that an expert does not have takes
+// nothing of it, not a zero times its values.
+template <int FMT, bool X_F32, int TOKENS>
+__global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, int block_tokens) {
+    constexpr int NA = X_F32 ? 3 : 2, BLK = FMT == 0 ? 32 : 16;
+    using X = XPart<false, TOKENS, NA>;
+    using W = RowsAt<FMT, 1>;
+    extern __shared__ u32x4_t lds[];
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int r = lane & 15, g = lane >> 4;
-    const int64_t token0 = (int64_t)blockIdx.y * (16 * CT);
-    const int block = (int)min((int64_t)(16 * CT), A.tokens - token0);
+    const int64_t token0 = (int64_t)blockIdx.y * block_tokens;
+    const int block = (int)min((int64_t)block_tokens, A.tokens - token0);
     const int pairs = block * A.top_k;
-    const int64_t K = A.W.inner, hidden = A.W.hidden;
-    const int64_t row0 = (int64_t)blockIdx.x * 16;
+    const int K = (int)A.W.inner, hidden = (int)A.W.hidden, row0 = blockIdx.x * 16;
+    f32x4_t *sums = (f32x4_t *)lds;  // [waves][tokens][4]: 16 rows
+    u32x4_t *mine = lds + DOWN_WAVES * block_tokens * 4 + wave * (X::PIECES + W::LDS);
+    const MoePlan plan(lds + DOWN_WAVES * (block_tokens * 4 + X::PIECES + W::LDS),
+                       block_tokens * A.top_k, A.W.experts);
 
-    for (int i = threadIdx.x; i < MOE_EXPERTS / 32; i += DOWN_WAVES * WAVE) sh.plan.seen[i] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += DOWN_WAVES * WAVE) {
-        const int e = A.ids[token0 * A.top_k + p];
-        sh.plan.ids[p] = e;
-        if (e >= 0 && e < A.W.experts) atomicOr(&sh.plan.seen[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    if (wave == 0) {
-        // experts ascending: a lane has 32 of them, one word
-        static_assert(MOE_EXPERTS / 32 <= WAVE, "a word a lane");
-        uint32_t word = lane < MOE_EXPERTS / 32 ? sh.plan.seen[lane] : 0;
-        int before = __builtin_popcount(word), all = before;
-        for (int off = 1; off < WAVE; off <<= 1) {
-            const int below = __shfl_up(all, off, WAVE);
-            if (lane >= off) all += below;
-        }
-        before = all - before;
-        for (; word; word &= word - 1) sh.plan.active[before++] = 32 * lane + __builtin_ctz(word);
-        if (lane == WAVE - 1) count = all;
-    }
-    __syncthreads();
+    for (int i = threadIdx.x; i < DOWN_WAVES * block_tokens * 4; i += DOWN_WAVES * WAVE)
+        sums[i] = {0, 0, 0, 0};
+    const int items = make_plan<TOKENS>(plan, A.ids + token0 * A.top_k, A.weights + token0 * A.top_k,
+                                        pairs, A.top_k, A.W.experts);
 
-    const int per = (int)((K + W4_UNIT - 1) / W4_UNIT), full = (int)(K / W4_UNIT);
-    const int64_t units = (int64_t)count * per;
-    int64_t u = units * wave / DOWN_WAVES;
-    const int64_t end = units * (wave + 1) / DOWN_WAVES;
-    f32x4_t out[CT] = {};
-    while (u < end) {
-        const int at = (int)(u / per);
-        const int e = __builtin_amdgcn_readfirstlane(sh.plan.active[at]);
-        int v = (int)(u - (int64_t)at * per);
-        const int v_end = (int)min((int64_t)per, v + end - u);
-        u += v_end - v;
-        // the lane's tokens' slots of this expert and their weight
-        const uint16_t *a[CT];
-        float share[CT];
-        bool real[CT];
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            real[t] = false;
-            share[t] = 0;
-            a[t] = A.act;
-            const int token = 16 * t + r;
-            if (token >= block) continue;
-            for (int j = A.top_k - 1; j >= 0; --j) {
-                if (sh.plan.ids[token * A.top_k + j] != e) continue;
-                const int64_t pair = (token0 + token) * A.top_k + j;
-                real[t] = true;
-                share[t] += A.weights[pair];
-                a[t] = A.act + pair * NA * K + 32 * g;
-            }
-        }
-        const int64_t row = (int64_t)e * hidden + row0 + r;
-        const W4Row<FMT> rows = {A.W.down_codes + row * (K / 2), A.W.down_scales + row * (K / BLK)};
-        f32x4_t acc[1][CT] = {};
-        uint32_t top[1] = {0};
-        for (; v < v_end; ++v) {
-            W4Unit<FMT> w[1];
-            w[0] = v < full ? w4_load<FMT>(rows, v, g) : w4_load_tail<FMT>(rows, v, g, K);
-            w4_multiply<FMT>(
-                w,
-                [&](int t, int k) {
-                    Terms<NA> b = {};
-                    if (real[t] && v * W4_UNIT + k + 32 * g < K) {
-#pragma unroll
-                        for (int m = 0; m < NA; ++m)
-                            b.p[m] = load_terms(a[t] + m * K + v * W4_UNIT + k).p[0];
-                    }
-                    return b;
-                },
-                acc, top);
-        }
+    const uint16_t *act0 = A.act + token0 * A.top_k * NA * K;
+    const Rsrc act = span(act0, pairs * NA * K * 2);
+    const int per = K / W4_GROUP;
+    f32x4_t acc[1][1] = {};
+    uint32_t top[1] = {0};
+    // the sums of an item's products so far go to its tokens
+    const auto add = [&](const MoeItem &it) {
         if constexpr (FMT == 0) w4_nan_rows(top, acc);
-        const float s_g = FMT == 0 ? 1.0f : A.W.down_global[(int64_t)e * A.W.global_stride];
+        if (r < it.count) {
+            const float s_g = FMT == 0 ? 1.0f : A.W.down_global[(int64_t)it.expert * A.W.global_stride];
+            f32x4_t *to = sums + (wave * block_tokens + plan.pair[it.first + r] / A.top_k) * 4 + g;
+            *to += acc[0][0] * (plan.share[it.first + r] * s_g);
+        }
+        acc[0][0] = {0, 0, 0, 0};
+        top[0] = 0;
+    };
+    const auto item_of = [&](int i) {
+        MoeItem it = plan.items[i];
+        it.expert = __builtin_amdgcn_readfirstlane(it.expert);
+        return it;
+    };
+    multiply_groups<FMT, false, W, X>(
+        [&](int n) {
+            const MoeItem it = item_of(n / per);
+            const int64_t row = (int64_t)it.expert * hidden + row0;
+            Group<W, X> a = {W(A.W.down_codes + row * (K / 2), A.W.down_scales + row * (K / BLK), 16, 16,
+                               K, mine + X::PIECES),
+                             (uint32_t)(n % per * W4_GROUP), {}};
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-            if (real[t]) out[t] += acc[0][t] * (share[t] * s_g);
+            for (int i = 0; i < X::LOADS; ++i) {
+                const auto p = X::place(i);
+                a.x_at[i] = p.row < it.count
+                                ? (uint32_t)((plan.pair[it.first + p.row] * NA + p.plane) * K + p.k) * 2
+                                : NOWHERE;
+            }
+            return a;
+        },
+        act, mine, wave, DOWN_WAVES, items * per, acc, top, [&](int n) { add(item_of(n / per)); });
+    // and stretches past the last whole group, by the waves that have fewer groups
+    const int rest = (K - per * W4_GROUP + W4_STRETCH - 1) / W4_STRETCH;
+    for (int n = (wave - items * per % DOWN_WAVES + DOWN_WAVES) % DOWN_WAVES; n < items * rest;
+         n += DOWN_WAVES) {
+        const MoeItem it = item_of(n / rest);
+        const int64_t row = (int64_t)it.expert * hidden + row0;
+        multiply_tail<FMT, NA>(
+            A.W.down_codes + row * (K / 2), A.W.down_scales + row * (K / BLK),
+            per * W4_GROUP + n % rest * W4_STRETCH, K, [](int, int rr) { return (int64_t)rr; },
+            [&](int at) {
+                Terms<NA> b = {};
+                if (r < it.count) {
+                    const uint16_t *from = act0 + (int64_t)plan.pair[it.first + r] * NA * K + at;
+#pragma unroll
+                    for (int m = 0; m < NA; ++m) b.p[m] = load_terms(from + (int64_t)m * K).p[0];
+                }
+                return b;
+            },
+            acc, top);
+        add(it);
     }
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < CT; ++t) sh.sums[wave][t][lane] = out[t];
-    __syncthreads();
-    for (int i = threadIdx.x; i < CT * WAVE; i += DOWN_WAVES * WAVE) {
-        const int t = i / WAVE, l = i & (WAVE - 1), token = 16 * t + (l & 15);
-        if (token >= block) continue;
-        f32x4_t s = sh.sums[0][t][l];
-#pragma unroll
-        for (int w = 1; w < DOWN_WAVES; ++w) s += sh.sums[w][t][l];
-        const int64_t at = (token0 + token) * hidden + row0 + 4 * (l >> 4);
+    for (int i = threadIdx.x; i < block * 4; i += DOWN_WAVES * WAVE) {
+        f32x4_t s = sums[i];
+        for (int w = 1; w < DOWN_WAVES; ++w) s += sums[w * block_tokens * 4 + i];
+        const int64_t at = (token0 + i / 4) * hidden + row0 + 4 * (i & 3);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (A.out_bf16) ((__bf16 *)A.out)[at + j] = (__bf16)s[j];
@@ -415,21 +503,37 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A) {
     }
 }
 
-template <int FMT, bool X_F32>
-hipError_t launch_experts(MoeArgs A, int32_t *status, hipStream_t s) {
+template <int FMT, bool X_F32, int TOKENS>
+hipError_t launch_tile(MoeArgs A, int32_t *status, hipStream_t s) {
     const int block = (int)(A.tokens < MOE_BLOCK ? A.tokens : MOE_BLOCK);
     A.slots = (int64_t)block * A.top_k < A.W.experts;
-    const dim3 up((uint32_t)(A.W.inner / 16), (uint32_t)(A.slots ? block * A.top_k : A.W.experts),
-                  (uint32_t)((A.tokens + MOE_BLOCK - 1) / MOE_BLOCK));
-    if (block <= 16) moe_up_kernel<FMT, X_F32, 1><<<up, UP_WAVES * WAVE, 0, s>>>(A, status);
-    else moe_up_kernel<FMT, X_F32, 4><<<up, UP_WAVES * WAVE, 0, s>>>(A, status);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int ct = block <= 16 ? 1 : 4;
-    const dim3 down((uint32_t)(A.W.hidden / 16), (uint32_t)((A.tokens + 16 * ct - 1) / (16 * ct)));
-    if (ct == 1) moe_down_kernel<FMT, X_F32, 1><<<down, DOWN_WAVES * WAVE, 0, s>>>(A);
-    else moe_down_kernel<FMT, X_F32, 4><<<down, DOWN_WAVES * WAVE, 0, s>>>(A);
+    const uint32_t blocks = (uint32_t)((A.tokens + MOE_BLOCK - 1) / MOE_BLOCK);
+    {
+        const int groups = (int)(A.W.hidden / W4_GROUP), waves = groups <= 4 ? 4 : UP_WAVES;
+        const dim3 grid((uint32_t)(A.W.inner / 16),
+                        (uint32_t)(A.slots ? block * A.top_k : A.W.experts), blocks);
+        const size_t lds = waves * (XPart<X_F32, TOKENS>::PIECES + RowsAt<FMT, 2>::LDS) * 16;
+        moe_up_kernel<FMT, X_F32, TOKENS><<<grid, waves * WAVE, lds, s>>>(A, status);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    constexpr int NA = X_F32 ? 3 : 2;
+    const auto down_lds = [&](int tokens) {
+        return (size_t)DOWN_WAVES *
+                   (tokens * 4 + XPart<false, TOKENS, NA>::PIECES + RowsAt<FMT, 1>::LDS) * 16 +
+               MoePlan::bytes(tokens * A.top_k, A.W.experts);
+    };
+    int down_block = block;  // fewer tokens where a plan of many pairs leaves no room for them
+    while (down_block > 16 && down_lds(down_block) > LDS_BYTES) down_block = (down_block + 1) / 2;
+    const dim3 grid((uint32_t)(A.W.hidden / 16), (uint32_t)((A.tokens + down_block - 1) / down_block));
+    moe_down_kernel<FMT, X_F32, TOKENS>
+        <<<grid, DOWN_WAVES * WAVE, down_lds(down_block), s>>>(A, down_block);
     return hipGetLastError();
+}
+
+template <int FMT, bool X_F32>
+hipError_t launch_experts(const MoeArgs &A, int32_t *status, hipStream_t s) {
+    return launch_tile<FMT, X_F32, 4>(A, status, s);
 }
 
 int route_splits(int64_t tokens, int64_t hidden, int experts) {

@@ -15,25 +15,31 @@
 // bits each, all 24.  Sums are fp32.
 #pragma once
 
+#include <type_traits>
+
 #include "fp4_device.h"
 
 namespace fp4dev {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-// vectors in memory that start where their first element may
-typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
-typedef u32x4_t u32x4_at1_t __attribute__((aligned(1)));
-typedef u32x2_t u32x2_at1_t __attribute__((aligned(1)));
 
-constexpr int W4_UNIT = 256;  // values of K that a lane group's two loads of a row cover
+// f(0), .. f(N - 1), the index a constant in each.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unroll(const F &f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        unroll<N, I + 1>(f);
+    }
+}
 
-// The scale bytes of a lane's two 32-value stretches of a unit: MXFP4 one byte
-// each, NVFP4 two.
-template <int FMT>
+constexpr int W4_STRETCH = 128;  // values of K that a load of 16 rows' codes covers
+
+// A lane's part of 16 rows' stretch: the codes of 32 values of its row, and their
+// scale bytes (MXFP4 one, NVFP4 two).
 struct W4Unit {
-    u32x4_t codes[2];
-    uint32_t scale[2];
+    u32x4_t codes;
+    uint32_t scale;
 };
 
 // NaN scale bytes of MXFP4 (255) are no operand of the converter: the largest
@@ -66,15 +72,14 @@ __device__ __forceinline__ bf16x8_t w4_values_e4m3(uint32_t codes, float s) {
     return v;
 }
 
-// Values 8 i .. 8 i + 7 of a lane's stretch h of a unit.
+// Values 8 i .. 8 i + 7 of a lane's 32.
 template <int FMT>
-__device__ __forceinline__ bf16x8_t w4_decode(const W4Unit<FMT> &u, int h, int i) {
+__device__ __forceinline__ bf16x8_t w4_decode(const W4Unit &u, int i) {
     if constexpr (FMT == 0) {
-        return w4_values(u.codes[h][i], e8m0_operand(u.scale[h]));
+        return w4_values(u.codes[i], e8m0_operand(u.scale));
     } else {
-        return w4_values_e4m3(u.codes[h][i],
-                              i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u.scale[h], 0)
-                                    : __builtin_amdgcn_cvt_f32_fp8((int)u.scale[h], 1));
+        return w4_values_e4m3(u.codes[i], i < 2 ? __builtin_amdgcn_cvt_f32_fp8((int)u.scale, 0)
+                                                : __builtin_amdgcn_cvt_f32_fp8((int)u.scale, 1));
     }
 }
 
@@ -83,38 +88,34 @@ struct Terms {
     bf16x8_t p[N];
 };
 
-// Eight fp32 values as three bf16 terms: a value's upper 16 bits, those of what
+// Four fp32 values as three bf16 terms each: a value's upper 16 bits, those of what
 // they leave, and the rest (differences are exact, and nothing overflows).  A
 // value that is not finite is its first term alone.
-__device__ __forceinline__ Terms<3> split_f32x8(const float (&x)[8]) {
-    uint32_t top = 0;
+__device__ __forceinline__ void split_f32x4(const float (&x)[4], u32x2_t (&t)[3]) {
+    float rest[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, f2u(x[i]) & 0x7FFFFFFFu);
-    float rest[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rest[i] = x[i];
-    Terms<3> t;
+    for (int i = 0; i < 4; ++i) rest[i] = x[i];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        uint32_t w[4];
+        t[k] = {__builtin_amdgcn_perm(f2u(rest[1]), f2u(rest[0]), 0x07060302u),
+                __builtin_amdgcn_perm(f2u(rest[3]), f2u(rest[2]), 0x07060302u)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = __builtin_amdgcn_perm(f2u(rest[2 * i + 1]), f2u(rest[2 * i]), 0x07060302u);
-        __builtin_memcpy(&t.p[k], w, sizeof(w));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rest[i] = rest[i] - u2f(f2u(rest[i]) & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) rest[i] = rest[i] - u2f(f2u(rest[i]) & 0xFFFF0000u);
     }
+    const uint32_t top = max(max(f2u(x[0]) & 0x7FFFFFFFu, f2u(x[1]) & 0x7FFFFFFFu),
+                             max(f2u(x[2]) & 0x7FFFFFFFu, f2u(x[3]) & 0x7FFFFFFFu));
     if (top >= 0x7F800000u) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = f2u(x[i]), a = b & 0x7FFFFFFFu;
-            if (a >= 0x7F800000u) {
-                t.p[0][i] = a > 0x7F800000u ? (__bf16)__builtin_nanf("") : (__bf16)x[i];
-                t.p[1][i] = t.p[2][i] = (__bf16)0.0f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t b = f2u(x[i]), a = b & 0x7FFFFFFFu, shift = 16 * (i & 1);
+            if (a < 0x7F800000u) continue;
+            const uint32_t keep = ~(0xFFFFu << shift);
+            const uint32_t first = a > 0x7F800000u ? 0x7FC0u : b >> 16;
+            t[0][i / 2] = (t[0][i / 2] & keep) | first << shift;
+            t[1][i / 2] &= keep;
+            t[2][i / 2] &= keep;
         }
     }
-    return t;
 }
 
 // Eight activations from memory: bf16 as they are, fp32 in three terms.
@@ -122,74 +123,134 @@ __device__ __forceinline__ Terms<1> load_terms(const uint16_t *p) {
     return {__builtin_bit_cast(bf16x8_t, *(const uint4 *)p)};
 }
 __device__ __forceinline__ Terms<3> load_terms(const float *p) {
-    float x[8];
-    widen_f32x8(((const uint4 *)p)[0], ((const uint4 *)p)[1], x);
-    return split_f32x8(x);
+    u32x2_t t[2][3];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 v = ((const float4 *)p)[h];
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        split_f32x4(x, t[h]);
+    }
+    Terms<3> r;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        const u32x4_t w = {t[0][n].x, t[0][n].y, t[1][n].x, t[1][n].y};
+        r.p[n] = __builtin_bit_cast(bf16x8_t, w);
+    }
+    return r;
 }
 
 __device__ __forceinline__ f32x4_t mfma_w4(bf16x8_t w, bf16x8_t x, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
 }
 
-// Where a lane's weight row lies: codes [rows, K/2] and scales [rows, K/block].
-template <int FMT>
-struct W4Row {
-    const uint8_t *codes, *scales;
-};
+// ---- loads ------------------------------------------------------------------
+// Buffer loads: past the end of what the resource spans they give zeros and move
+// nothing, so that a pipeline's loads need no branches (around which the waits for
+// them would lose count).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+// Resources are below 2^30 bytes: an offset of 2^31 is past any.
+constexpr uint32_t NOWHERE = 0x80000000u;
+constexpr int STREAMED = 2;  // cache policy: nontemporal
 
-// Unit u of a row, all of it inside the row.
-template <int FMT>
-__device__ __forceinline__ W4Unit<FMT> w4_load(const W4Row<FMT> &row, int64_t u, int g) {
-    W4Unit<FMT> r;
-    const uint8_t *c = row.codes + u * (W4_UNIT / 2) + 16 * g;
-    r.codes[0] = *(const u32x4_at4_t *)c;
-    r.codes[1] = *(const u32x4_at4_t *)(c + 64);
-    if constexpr (FMT == 0) {
-        const u32x2_t s = *(const u32x2_at1_t *)(row.scales + u * (W4_UNIT / 32));
-        r.scale[0] = (s.x >> (8 * g)) & 0xFFu;
-        r.scale[1] = (s.y >> (8 * g)) & 0xFFu;
-    } else {
-        const u32x4_t s = *(const u32x4_at1_t *)(row.scales + u * (W4_UNIT / 16));
-        r.scale[0] = (g & 2 ? s.y : s.x) >> (16 * (g & 1));
-        r.scale[1] = (g & 2 ? s.w : s.z) >> (16 * (g & 1));
-    }
-    return r;
+// bytes, alike in all lanes, is made a scalar: the compiler clamps in vector registers,
+// and then every load loops over what it takes for different resources.
+__device__ __forceinline__ Rsrc span(const void *p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes),
+                                             kBufferRsrcWord3);
+}
+__device__ __forceinline__ u32x4_t load16(Rsrc r, uint32_t at) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 0);
+}
+__device__ __forceinline__ u32x4_t load16_streamed(Rsrc r, uint32_t at) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, STREAMED);
 }
 
-// The last unit of a row whose K is no multiple of a unit: stretches past the
-// row's end are zero, and so is the half past it of one that NVFP4's K ends in.
-template <int FMT>
-__device__ __forceinline__ W4Unit<FMT> w4_load_tail(const W4Row<FMT> &row, int64_t u, int g,
-                                                    int64_t K) {
-    W4Unit<FMT> r;
+// A wave takes K in groups of 512 values, four stretches; it loads weights by pairs of
+// stretches, 128 bytes of a row, and a group's scales at once.  Loads are laid out for
+// the memory: lanes next to each other have what is next to each other, a load has whole
+// lines, and a line is loaded by one wave.  (With lanes in the products' order, where
+// neighbours have different rows, 16 tokens through 8192 x 28672 in NVFP4 took 70 us;
+// with stretches of 64 bytes and scales a stretch at a time, lines that several waves
+// wait for, 50.)  What K has past its last whole group is load_tail's.
+constexpr int W4_GROUP = 4 * W4_STRETCH;
+
+// PARTS parts of 16 rows of row-major weights, codes [rows, K/2] and scales [rows,
+// K/block].  A pair's load n has rows 8 n .. 8 n + 7, eight lanes a row.
+template <int FMT, int PARTS>
+struct RowsAt {
+    static constexpr int LDS = PARTS * (128 + (FMT == 0 ? 16 : 32));  // pieces of a wave
+    struct Pair {
+        u32x4_t v[2 * PARTS];
+    };
+    struct Scales {
+        u32x4_t v;
+    };
+    Rsrc codes, scales;
+    uint32_t code[2 * PARTS], scale;
+    u32x4_t *lds;  // the wave's: [part][row][8 pieces of a pair], [part][row] scales
+
+    // rows: of those from row0 on, how many there are; part p has rows row0 + p *
+    // part_rows + 0 .. 15; base: of row row0.
+    __device__ __forceinline__ RowsAt(const uint8_t *code_base, const uint8_t *scale_base, int rows,
+                                      int part_rows, int K, u32x4_t *wave_lds)
+        : lds(wave_lds) {
+        constexpr int BLK = FMT == 0 ? 32 : 16, EACH = FMT == 0 ? 1 : 2;  // scale loads of a row
+        const int lane = threadIdx.x & (WAVE - 1);
+        const int code_row = (uint32_t)K / 2, scale_row = (uint32_t)K / BLK;
+        const int have = min(rows, (PARTS - 1) * part_rows + 16);
+        codes = span(code_base, have * code_row);
+        scales = span(scale_base, have * scale_row);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t k = u * W4_UNIT + 128 * h + 32 * g;
-        r.codes[h] = {0, 0, 0, 0};
-        r.scale[h] = 0;
-        if (k >= K) continue;
-        if constexpr (FMT == 0) {
-            r.codes[h] = *(const u32x4_at4_t *)(row.codes + k / 2);
-            r.scale[h] = row.scales[k / 32];
-        } else {
-            const uint32_t *c = (const uint32_t *)(row.codes + k / 2);
-            r.codes[h].x = c[0], r.codes[h].y = c[1];
-            r.scale[h] = row.scales[k / 16];
-            if (k + 16 < K) {
-                r.codes[h].z = c[2], r.codes[h].w = c[3];
-                r.scale[h] |= (uint32_t)row.scales[k / 16 + 1] << 8;
-            }
+        for (int n = 0; n < 2 * PARTS; ++n)
+            code[n] = (uint32_t)(n / 2 * part_rows + n % 2 * 8 + (lane >> 3)) * (uint32_t)code_row +
+                      16 * (lane & 7);
+        const int row = lane / EACH;
+        scale = row < 16 * PARTS ? (uint32_t)(row / 16 * part_rows + row % 16) * (uint32_t)scale_row +
+                                       16 * (lane % EACH)
+                                 : NOWHERE;
+    }
+    // of the group or pair at k (a group past the end: NOWHERE)
+    __device__ __forceinline__ Scales load_scales(uint32_t k) const {
+        return {load16(scales, scale + (k == NOWHERE ? k / 2 : k / (FMT == 0 ? 32 : 16)))};
+    }
+    __device__ __forceinline__ Pair load_pair(uint32_t k) const {
+        Pair r;
+#pragma unroll
+        for (int n = 0; n < 2 * PARTS; ++n)
+            r.v[n] = load16_streamed(codes, code[n] + (k == NOWHERE ? k : k / 2));
+        return r;
+    }
+    // into LDS: codes of row r, piece v at 8 r + (v ^ r), which spreads what is written
+    // and what is read over the banks
+    __device__ __forceinline__ void put(const Scales &s) const {
+        const int lane = threadIdx.x & (WAVE - 1);
+        if (lane < 16 * PARTS * (FMT == 0 ? 1 : 2)) lds[PARTS * 128 + lane] = s.v;
+    }
+    __device__ __forceinline__ void put(const Pair &p) const {
+        const int lane = threadIdx.x & (WAVE - 1);
+#pragma unroll
+        for (int n = 0; n < 2 * PARTS; ++n) lds[64 * n + (lane ^ (lane >> 3))] = p.v[n];
+    }
+    // stretch j of the group, of the pair that is in LDS
+    __device__ __forceinline__ void units(const Scales &, const Pair &, int j,
+                                          W4Unit (&w)[PARTS]) const {
+        const int lane = threadIdx.x & (WAVE - 1), r = lane & 15, g = lane >> 4;
+        const uint8_t *s = (const uint8_t *)(lds + PARTS * 128);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            w[p].codes = lds[128 * p + 8 * r + ((4 * (j & 1) + g) ^ (r & 7))];
+            if constexpr (FMT == 0) w[p].scale = s[(16 * p + r) * 16 + 4 * j + g];
+            else w[p].scale = ((const uint16_t *)s)[(16 * p + r) * 16 + 4 * j + g];
         }
     }
-    return r;
-}
+};
 
-// The same unit of a packed operand's row tile of 32 rows: a lane's loads are of
-// rows l % 32 and 32-value stretches 2 ks + l / 32 of four K steps ks.  Exchanging
-// odd groups of 16 lanes of one step with even ones of the next gives a register
-// rows 0 .. 15 and another rows 16 .. 31, with the stretches 0, 2, 1, 3 in lane
-// groups 0 .. 3.
-__device__ __forceinline__ int packed_stretch(int g) { return (g & 1) * 2 + (g >> 1); }
+// Two parts (a row tile of 32) of a packed operand: a load has 32 rows, 32 values of
+// each of two, rows l % 32 and values 32 (l / 32) .. of a K step.  Exchanging odd groups
+// of 16 lanes of one step with even ones of the next gives a register rows 0 .. 15 and
+// another rows 16 .. 31, with the 32s 0, 2, 1, 3 of the stretch in lane groups 0 .. 3.
+__device__ __forceinline__ int packed_group(int g) { return (g & 1) * 2 + (g >> 1); }
 
 __device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
     const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
@@ -198,75 +259,110 @@ __device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
 }
 
 template <int FMT>
-__device__ __forceinline__ void w4_load_packed(const uint8_t *codes, const uint8_t *scales,
-                                               int64_t u, int lane, W4Unit<FMT> (&r)[2]) {
-    const u32x4_t *c = (const u32x4_t *)(codes + u * 4096) + lane;
-    const int odd = (lane >> 4) & 1;
+struct PackedAt {
+    static constexpr int LDS = 0;
+    struct Pair {
+        u32x4_t v[4];
+    };
+    struct Scales {
+        std::conditional_t<FMT == 0, u32x2_t, u32x4_t> v;
+    };
+    Rsrc codes, scales;
+
+    __device__ __forceinline__ PackedAt(const uint8_t *code_base, const uint8_t *scale_base, int K) {
+        codes = span(code_base, 16 * K);
+        scales = span(scale_base, FMT == 0 ? K : 2 * K);
+    }
+    __device__ __forceinline__ Scales load_scales(uint32_t k) const {
+        const int lane = threadIdx.x & (WAVE - 1);
+        if constexpr (FMT == 0)
+            return {__builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                                    scales, (int)(k + 8 * lane), 0, 0))};
+        else return {load16(scales, (k == NOWHERE ? k : 2 * k) + 16 * lane)};
+    }
+    __device__ __forceinline__ Pair load_pair(uint32_t k) const {
+        const int lane = threadIdx.x & (WAVE - 1);
+        Pair r;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        u32x4_t a = c[128 * h], b = c[128 * h + 64];
+        for (int n = 0; n < 4; ++n)
+            r.v[n] = load16_streamed(codes, (k == NOWHERE ? k : 16 * k) + 1024 * n + 16 * lane);
+        return r;
+    }
+    __device__ __forceinline__ void put(const Scales &) const {}
+    __device__ __forceinline__ void put(const Pair &) const {}
+    __device__ __forceinline__ void units(const Scales &s, const Pair &p, int j,
+                                          W4Unit (&w)[2]) const {
+        const int odd = (threadIdx.x >> 4) & 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t x = a[i], y = b[i];
+            uint32_t x = p.v[2 * (j & 1)][i], y = p.v[2 * (j & 1) + 1][i];
             swap16(x, y);
-            r[0].codes[h][i] = x;
-            r[1].codes[h][i] = y;
+            w[0].codes[i] = x;
+            w[1].codes[i] = y;
         }
-    }
-    if constexpr (FMT == 0) {
-        uint32_t s0 = *(const uint32_t *)(scales + (u >> 1) * 512 + 8 * lane + 4 * (u & 1)), s1 = s0;
+        uint32_t s0 = s.v[FMT == 0 ? j / 2 : j], s1 = s0;
         swap16(s0, s1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            r[0].scale[h] = (s0 >> (16 * h + 8 * odd)) & 0xFFu;
-            r[1].scale[h] = (s1 >> (16 * h + 8 * odd)) & 0xFFu;
-        }
+        const int by = FMT == 0 ? 16 * (j & 1) + 8 * odd : 16 * odd;
+        w[0].scale = FMT == 0 ? (s0 >> by) & 0xFFu : s0 >> by;
+        w[1].scale = FMT == 0 ? (s1 >> by) & 0xFFu : s1 >> by;
+    }
+};
+
+// A lane's unit of the stretch from k on, for what K has past its last whole group:
+// zeros past the row's end, which may be inside the lane's 32 values (NVFP4).
+template <int FMT>
+__device__ __forceinline__ W4Unit load_tail(const uint8_t *codes, const uint8_t *scales, int k,
+                                            int K) {
+    const int at = k + 32 * ((threadIdx.x & (WAVE - 1)) >> 4);
+    W4Unit u = {{0, 0, 0, 0}, 0};
+    if (at >= K) return u;
+    const uint32_t *c = (const uint32_t *)(codes + at / 2);
+    u.codes.x = c[0], u.codes.y = c[1];
+    if constexpr (FMT == 0) {
+        u.codes.z = c[2], u.codes.w = c[3];
+        u.scale = scales[at / 32];
     } else {
-        const u32x2_t s = *(const u32x2_t *)(scales + (u >> 1) * 1024 + 16 * lane + 8 * (u & 1));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t s0 = h ? s.y : s.x, s1 = s0;
-            swap16(s0, s1);
-            r[0].scale[h] = s0 >> (16 * odd);
-            r[1].scale[h] = s1 >> (16 * odd);
+        u.scale = scales[at / 16];
+        if (at + 16 < K) {
+            u.codes.z = c[2], u.codes.w = c[3];
+            u.scale |= (uint32_t)scales[at / 16 + 1] << 8;
         }
     }
+    return u;
 }
 
-// One unit: its products with X's activations are added to acc; top takes part in
-// w4_nan_rows.  x(t, k) gives the terms of values k .. k + 7 of the unit for the
-// lane's row of activation tile t.
-template <int FMT, int ROWS, int TILES, typename X>
-__device__ __forceinline__ void w4_multiply(const W4Unit<FMT> (&w)[ROWS], const X &x,
-                                            f32x4_t (&acc)[ROWS][TILES], uint32_t (&top)[ROWS]) {
+// ---- products ----------------------------------------------------------------
+// A stretch: its products with activations are added to acc; top takes part in
+// w4_nan_rows.  x(t, i, n) is term n of values 8 i .. 8 i + 7 of the lane's 32 for
+// its row of activation tile t.
+template <int FMT, int TERMS, int PARTS, int TILES, typename X>
+__device__ __forceinline__ void w4_multiply(const W4Unit (&w)[PARTS], const X &x,
+                                            f32x4_t (&acc)[PARTS][TILES], uint32_t (&top)[PARTS]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int p = 0; p < PARTS; ++p) top[p] = max(top[p], w[p].scale);
 #pragma unroll
-        for (int p = 0; p < ROWS; ++p) top[p] = max(top[p], w[p].scale[h]);
+    for (int i = 0; i < 4; ++i) {
+        bf16x8_t v[PARTS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bf16x8_t v[ROWS];
+        for (int p = 0; p < PARTS; ++p) v[p] = w4_decode<FMT>(w[p], i);
 #pragma unroll
-            for (int p = 0; p < ROWS; ++p) v[p] = w4_decode<FMT>(w[p], h, i);
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-                const auto b = x(t, 128 * h + 8 * i);
+            for (int n = 0; n < TERMS; ++n) {
+                const bf16x8_t b = x(t, i, n);
 #pragma unroll
-                for (auto &term : b.p)
-#pragma unroll
-                    for (int p = 0; p < ROWS; ++p) acc[p][t] = mfma_w4(v[p], term, acc[p][t]);
+                for (int p = 0; p < PARTS; ++p) acc[p][t] = mfma_w4(v[p], b, acc[p][t]);
             }
-        }
     }
 }
 
 // A scale byte of 255 in any lane of a row makes the row's sums NaN (MXFP4).
-template <int ROWS, int TILES>
-__device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[ROWS],
-                                            f32x4_t (&acc)[ROWS][TILES]) {
+template <int PARTS, int TILES>
+__device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[PARTS],
+                                            f32x4_t (&acc)[PARTS][TILES]) {
     const int g = (threadIdx.x & (WAVE - 1)) >> 4;
 #pragma unroll
-    for (int p = 0; p < ROWS; ++p) {
+    for (int p = 0; p < PARTS; ++p) {
         uint64_t bad = __ballot(top[p] == 255u);
         if (bad == 0) continue;
         bad |= bad >> 32;
@@ -276,6 +372,131 @@ __device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[ROWS],
             if (bad >> (4 * g + i) & 1)
 #pragma unroll
                 for (int t = 0; t < TILES; ++t) acc[p][t][i] = __builtin_nanf("");
+    }
+}
+
+// ---- activations of one stretch, up to 16 rows ---------------------------------
+// A wave brings the activations of its stretch into LDS of its own, as 16-byte pieces
+// of 8 values, and reads them as its products want them.  Lanes next to each other load
+// what is next to each other in memory (of 64 lanes in as many lines, a load takes four
+// times as long), every lane has a share of the rows there are (from a lane's row alone,
+// 16 - ROWS of 16 lanes would load nothing), and fp32 is split into its terms once a
+// value, not once for each row of a tile.  Rows that are not there are others' or
+// whatever LDS held: they end in sums that nothing stores.  A wave's LDS operations keep
+// their order, so there is no barrier.
+//
+// Piece of values 8 v .. of row `row`, term n: [v][n][row ^ v], which spreads both what
+// lanes write at a time (a row's v) and what they read (a v's rows) over the banks.
+template <bool F32, int ROWS, int PLANES = 1>
+struct XPart {
+    static constexpr int TERMS = F32 ? 3 : PLANES;
+    static constexpr int PIECES = ROWS * 16 * TERMS;                      // in LDS
+    static constexpr int HALVES = F32 ? 2 : 1;                            // loads of a piece
+    static constexpr int LOADS = ROWS * 16 * HALVES * PLANES / WAVE;      // of a lane
+    static_assert(ROWS * 16 * HALVES * PLANES % WAVE == 0, "every lane loads");
+    u32x4_t v[LOADS];
+
+    // Load n of a lane: its row and plane, and the value of the stretch it starts at.
+    struct Place {
+        int row, k, plane;
+    };
+    static __device__ __forceinline__ Place place(int n) {
+        const int p = n * WAVE + (threadIdx.x & (WAVE - 1));
+        const int q = p / (16 * HALVES);
+        return {q / PLANES, p % (16 * HALVES) * (8 / HALVES), q % PLANES};
+    }
+
+    // at[n]: the lane's byte offset of load n in the activations, of the stretch at 0
+    // (NOWHERE: no such row); k: the stretch's offset in values, or NOWHERE.
+    __device__ __forceinline__ void load(Rsrc x, const uint32_t (&at)[LOADS], uint32_t k) {
+#pragma unroll
+        for (int n = 0; n < LOADS; ++n)
+            v[n] = load16(x, at[n] + (k == NOWHERE ? NOWHERE / 2 : k * (F32 ? 4 : 2)));
+    }
+
+    __device__ __forceinline__ void store(u32x4_t *lds) const {
+#pragma unroll
+        for (int n = 0; n < LOADS; ++n) {
+            const auto at = place(n);
+            const int piece = at.k / 8, row = at.row ^ (piece & (ROWS - 1));
+            if constexpr (F32) {
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = u2f(v[n][j]);
+                u32x2_t t[3];
+                split_f32x4(x, t);
+                u32x2_t *to = (u32x2_t *)(lds + piece * 3 * ROWS + row) + (at.k / 4 & 1);
+#pragma unroll
+                for (int m = 0; m < 3; ++m) to[m * 2 * ROWS] = t[m];
+            } else {
+                lds[(piece * PLANES + at.plane) * ROWS + row] = v[n];
+            }
+        }
+    }
+
+    // Term n of values 8 i .. 8 i + 7 of the lane's 32 for its row; the 32 values of lane
+    // group g are the stretch's group_of(g)-th.
+    static __device__ __forceinline__ bf16x8_t piece(const u32x4_t *lds, int group, int i, int n) {
+        const int v = 4 * group + i, row = (threadIdx.x & (ROWS - 1)) ^ (v & (ROWS - 1));
+        return __builtin_bit_cast(bf16x8_t, lds[(v * TERMS + n) * ROWS + row]);
+    }
+};
+
+// A group of K that a wave multiplies: the weights that have it, its place k in them
+// and in the activations (NOWHERE: none), and the lane's rows of the activations.
+template <typename W, typename X>
+struct Group {
+    W w;
+    uint32_t k;
+    uint32_t x_at[X::LOADS];
+};
+
+// A wave's groups group(first), group(first + step), .. up to `groups`: their products
+// are added to acc, and done(n) is called after each.  Weights are loaded two pairs
+// ahead, activations two stretches.  The loop is short on purpose: instructions that run
+// once have to come from memory first (four groups unrolled: 1 x 512 x 2048 9 us, not 4).
+template <int FMT, bool PACKED, typename W, typename X, int PARTS, typename GroupAt, typename Done>
+__device__ __forceinline__ void multiply_groups(const GroupAt &group, Rsrc x, u32x4_t *x_lds,
+                                                int first, int step, int groups,
+                                                f32x4_t (&acc)[PARTS][1], uint32_t (&top)[PARTS],
+                                                const Done &done) {
+    const int g = (threadIdx.x & (WAVE - 1)) >> 4, part = PACKED ? packed_group(g) : g;
+    const auto from = [](uint32_t k, int more) { return k == NOWHERE ? k : k + more; };
+    if (first >= groups) return;
+    Group<W, X> here = group(first);
+    typename W::Scales scales = here.w.load_scales(here.k);
+    typename W::Pair pair[2];
+    X xs[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        pair[j] = here.w.load_pair(here.k + 2 * W4_STRETCH * j);
+        if (j == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) xs[i].load(x, here.x_at, here.k + W4_STRETCH * i);
+        __builtin_amdgcn_sched_barrier(0);  // in the order that they are waited for
+    }
+    for (int n = first; n < groups; n += step) {
+        Group<W, X> next = group(n + step < groups ? n + step : n);
+        if (n + step >= groups) next.k = NOWHERE;
+        const typename W::Scales s = scales;
+        here.w.put(s);
+        scales = next.w.load_scales(next.k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j % 2 == 0) here.w.put(pair[j / 2]);
+            xs[j & 1].store(x_lds);
+            if (j < 2) xs[j].load(x, here.x_at, here.k + W4_STRETCH * (j + 2));
+            else xs[j & 1].load(x, next.x_at, from(next.k, W4_STRETCH * (j - 2)));
+            __builtin_amdgcn_sched_barrier(0);
+            W4Unit u[PARTS];
+            here.w.units(s, pair[j / 2], j, u);
+            w4_multiply<FMT, X::TERMS>(
+                u, [&](int, int i, int m) { return X::piece(x_lds, part, i, m); }, acc, top);
+            if (j % 2 == 1) pair[j / 2] = next.w.load_pair(from(next.k, W4_STRETCH * (j - 1)));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        done(n);
+        here = next;
     }
 }
 

@@ -31,7 +31,8 @@ def test_refused(call):
     for name in ("m", "n", "k"):
         for bad in (0, -1, -512, 2 ** 31, 2 ** 62):
             assert call(**{name: bad}) == E_SHAPE
-    assert call(m=2 ** 30 - 1, n=2 ** 30 - 1, k=512) == E_SHAPE  # more tiles than a grid has
+    assert call(m=2 ** 19 + 1) == E_SHAPE and call(k=2 ** 20 + 512) == E_SHAPE
+    assert call(n=2 ** 29, k=2 ** 19) == E_SHAPE
     for bad in (16, 40, 500):
         assert call(k=bad) == E_SHAPE
     assert call(x=P + 8) == E_ALIGN and call(codes=P + 8) == E_ALIGN

@@ -23,7 +23,7 @@ def test_route():
         assert route(**{null: None}) == E_ARG
     assert route(renormalize=2) == E_ARG
     assert route(xt=2) == E_DTYPE and route(rt=-1) == E_DTYPE
-    for bad in (0, -1, 2 ** 21 + 1, 2 ** 62):
+    for bad in (0, -1, 2 ** 20 + 1, 2 ** 62):
         assert route(tokens=bad) == E_SHAPE
     for bad in (0, -8, 4, 12, 2 ** 40):
         assert route(hidden=bad) == E_SHAPE
@@ -66,7 +66,7 @@ def test_experts(fmt):
     for bad in (-1, 2):
         assert experts(fmt=bad) == E_DTYPE and call(xt=bad) == E_DTYPE and call(ot=bad) == E_DTYPE
         assert call(w=weights(stride=bad)) == E_ARG
-    for bad in (0, -1, 2 ** 21 + 1, 2 ** 62):
+    for bad in (0, -1, 2 ** 20 + 1, 2 ** 62):
         assert call(tokens=bad) == E_SHAPE
     for bad in (0, -1, 33):
         assert call(top_k=bad) == E_SHAPE
@@ -74,7 +74,8 @@ def test_experts(fmt):
         assert call(w=weights(hidden=bad)) == E_SHAPE and call(w=weights(inner=bad)) == E_SHAPE
     for bad in (0, -1, 1025):
         assert call(w=weights(experts=bad)) == E_SHAPE
-    assert call(w=weights(hidden=2 ** 28, inner=2 ** 28)) == E_SHAPE
+    assert call(w=weights(hidden=2 ** 20, inner=2 ** 11)) == E_SHAPE
+    assert call(w=weights(inner=2 ** 16 + 32)) == E_SHAPE
     for name in ("uc", "dc"):
         assert call(w=weights(**{name: P + 8})) == E_ALIGN
     assert call(x=P + 8) == E_ALIGN and call(ws=P + 8) == E_ALIGN and call(ids=P + 2) == E_ALIGN
