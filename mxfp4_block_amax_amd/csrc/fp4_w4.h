@@ -179,7 +179,7 @@ constexpr int W4_GROUP = 4 * W4_STRETCH;
 // K/block].  A pair's load n has rows 8 n .. 8 n + 7, eight lanes a row.
 template <int FMT, int PARTS>
 struct RowsAt {
-    static constexpr int LDS = PARTS * (128 + (FMT == 0 ? 16 : 32));  // pieces of a wave
+    static constexpr int LDS = 128 + PARTS * (FMT == 0 ? 16 : 32);  // pieces of a wave
     struct Pair {
         u32x4_t v[2 * PARTS];
     };
@@ -188,7 +188,7 @@ struct RowsAt {
     };
     Rsrc codes, scales;
     uint32_t code[2 * PARTS], scale;
-    u32x4_t *lds;  // the wave's: [part][row][8 pieces of a pair], [part][row] scales
+    u32x4_t *lds;  // the wave's: [row][8 pieces of a pair], [part][row] scales
 
     // rows: of those from row0 on, how many there are; part p has rows row0 + p *
     // part_rows + 0 .. 15; base: of row row0.
@@ -221,25 +221,33 @@ struct RowsAt {
             r.v[n] = load16_streamed(codes, code[n] + (k == NOWHERE ? k : k / 2));
         return r;
     }
-    // into LDS: codes of row r, piece v at 8 r + (v ^ r), which spreads what is written
-    // and what is read over the banks
     __device__ __forceinline__ void put(const Scales &s) const {
         const int lane = threadIdx.x & (WAVE - 1);
-        if (lane < 16 * PARTS * (FMT == 0 ? 1 : 2)) lds[PARTS * 128 + lane] = s.v;
+        if (lane < 16 * PARTS * (FMT == 0 ? 1 : 2)) lds[128 + lane] = s.v;
     }
-    __device__ __forceinline__ void put(const Pair &p) const {
-        const int lane = threadIdx.x & (WAVE - 1);
-#pragma unroll
-        for (int n = 0; n < 2 * PARTS; ++n) lds[64 * n + (lane ^ (lane >> 3))] = p.v[n];
-    }
-    // stretch j of the group, of the pair that is in LDS
-    __device__ __forceinline__ void units(const Scales &, const Pair &, int j,
-                                          W4Unit (&w)[PARTS]) const {
+    // to the products' order, v[PARTS * stretch + part]: piece v of row r goes through
+    // 8 r + (v ^ r), which spreads what is written and what is read over the banks
+    __device__ __forceinline__ void spread(Pair &pair) const {
         const int lane = threadIdx.x & (WAVE - 1), r = lane & 15, g = lane >> 4;
-        const uint8_t *s = (const uint8_t *)(lds + PARTS * 128);
+        u32x4_t in[2 * PARTS];
+#pragma unroll
+        for (int n = 0; n < 2 * PARTS; ++n) in[n] = pair.v[n];
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
-            w[p].codes = lds[128 * p + 8 * r + ((4 * (j & 1) + g) ^ (r & 7))];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) lds[64 * n + (lane ^ (lane >> 3))] = in[2 * p + n];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) pair.v[PARTS * h + p] = lds[8 * r + ((4 * h + g) ^ (r & 7))];
+        }
+    }
+    // stretch j of the group, of a spread pair
+    __device__ __forceinline__ void units(const Scales &, const Pair &pair, int j,
+                                          W4Unit (&w)[PARTS]) const {
+        const int lane = threadIdx.x & (WAVE - 1), r = lane & 15, g = lane >> 4;
+        const uint8_t *s = (const uint8_t *)(lds + 128);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+            w[p].codes = pair.v[PARTS * (j & 1) + p];
             if constexpr (FMT == 0) w[p].scale = s[(16 * p + r) * 16 + 4 * j + g];
             else w[p].scale = ((const uint16_t *)s)[(16 * p + r) * 16 + 4 * j + g];
         }
@@ -289,17 +297,22 @@ struct PackedAt {
         return r;
     }
     __device__ __forceinline__ void put(const Scales &) const {}
-    __device__ __forceinline__ void put(const Pair &) const {}
-    __device__ __forceinline__ void units(const Scales &s, const Pair &p, int j,
+    __device__ __forceinline__ void spread(Pair &pair) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x = pair.v[2 * h][i], y = pair.v[2 * h + 1][i];
+                swap16(x, y);
+                pair.v[2 * h][i] = x;
+                pair.v[2 * h + 1][i] = y;
+            }
+    }
+    __device__ __forceinline__ void units(const Scales &s, const Pair &pair, int j,
                                           W4Unit (&w)[2]) const {
         const int odd = (threadIdx.x >> 4) & 1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t x = p.v[2 * (j & 1)][i], y = p.v[2 * (j & 1) + 1][i];
-            swap16(x, y);
-            w[0].codes[i] = x;
-            w[1].codes[i] = y;
-        }
+        w[0].codes = pair.v[2 * (j & 1)];
+        w[1].codes = pair.v[2 * (j & 1) + 1];
         uint32_t s0 = s.v[FMT == 0 ? j / 2 : j], s1 = s0;
         swap16(s0, s1);
         const int by = FMT == 0 ? 16 * (j & 1) + 8 * odd : 16 * odd;
@@ -442,6 +455,13 @@ struct XPart {
     }
 };
 
+// A barrier for what the workgroup has in LDS: loads from memory stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // A group of K that a wave multiplies: the weights that have it, its place k in them
 // and in the activations (NOWHERE: none), and the lane's rows of the activations.
 template <typename W, typename X>
@@ -483,7 +503,7 @@ __device__ __forceinline__ void multiply_groups(const GroupAt &group, Rsrc x, u3
         scales = next.w.load_scales(next.k);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (j % 2 == 0) here.w.put(pair[j / 2]);
+            if (j % 2 == 0) here.w.spread(pair[j / 2]);
             xs[j & 1].store(x_lds);
             if (j < 2) xs[j].load(x, here.x_at, here.k + W4_STRETCH * (j + 2));
             else xs[j & 1].load(x, next.x_at, from(next.k, W4_STRETCH * (j - 2)));
