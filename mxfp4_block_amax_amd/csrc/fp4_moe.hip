@@ -37,16 +37,14 @@ __device__ __forceinline__ Wide8 load8(const float *p) {
     return r;
 }
 
-constexpr int ROUTE_WAVES = 4;
-
-// A workgroup has 16 tokens, 16 experts and one of `splits` ranges of K, its
+// A workgroup has 16 tokens, 16 experts and one of `splits` shares of K, its
 // waves 32 values of K at a time in turn; v_mfma_f64_16x16x4_f64 eight times on
 // the eight values that a lane loads of its token and of its expert.
-template <typename XT, typename RT>
-__global__ __launch_bounds__(ROUTE_WAVES *WAVE) void route_logits_kernel(
+template <typename XT, typename RT, int WAVES>
+__global__ __launch_bounds__(WAVES *WAVE) void route_logits_kernel(
     const XT *x, const RT *router, double *logits, int64_t tokens, int64_t hidden, int experts,
     int expert_tiles, int splits) {
-    __shared__ f64x4_t sums[ROUTE_WAVES][WAVE];
+    __shared__ f64x4_t sums[WAVES][WAVE];
     const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE;
     const int r = lane & 15, g = lane >> 4;
     const int tile = blockIdx.x % expert_tiles, split = blockIdx.x / expert_tiles % splits;
@@ -55,90 +53,107 @@ __global__ __launch_bounds__(ROUTE_WAVES *WAVE) void route_logits_kernel(
     const XT *xr = x + min(t0 + r, tokens - 1) * hidden;
     const RT *rr = router + (int64_t)min(e0 + r, experts - 1) * hidden;
     f64x4_t acc = {0, 0, 0, 0};
-    for (int64_t k = 32 * (split * ROUTE_WAVES + wave); k < hidden; k += 32 * ROUTE_WAVES * splits) {
-        Wide8 a = {}, b = {};
-        if (k + 8 * g < hidden) {
-            a = load8(xr + k + 8 * g);
-            b = load8(rr + k + 8 * g);
+    const int h = (int)hidden, step = 32 * WAVES * splits;
+    const auto load = [&](int k, Wide8 &a, Wide8 &b) {
+        a = {}, b = {};
+        if (k < h) {
+            a = load8(xr + k);
+            b = load8(rr + k);
         }
+    };
+    Wide8 a, b;
+    int k = 32 * (split * WAVES + wave) + 8 * g;
+    load(k, a, b);
+    for (; k - 8 * g < h; k += step) {
+        Wide8 a2, b2;
+        load(k + step, a2, b2);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)a.v[i], (double)b.v[i], acc, 0, 0, 0);
+        a = a2, b = b2;
     }
     sums[wave][lane] = acc;
     __syncthreads();
     // a lane's sums: expert r, tokens g + 4 i
-    for (int i = threadIdx.x; i < 256; i += ROUTE_WAVES * WAVE) {
+    for (int i = threadIdx.x; i < 256; i += WAVES * WAVE) {
         const int l = i & (WAVE - 1), j = i / WAVE;
         double s = sums[0][l][j];
 #pragma unroll
-        for (int w = 1; w < ROUTE_WAVES; ++w) s += sums[w][l][j];
+        for (int w = 1; w < WAVES; ++w) s += sums[w][l][j];
         const int64_t t = t0 + (l >> 4) + 4 * j;
         const int e = e0 + (l & 15);
         if (t < tokens && e < experts) logits[(split * tokens + t) * experts + e] = s;
     }
 }
 
-// A wave has a token, a lane the experts lane + 64 i.
-template <int PER_LANE>
-__global__ __launch_bounds__(WAVE) void route_choose_kernel(const double *logits, int64_t tokens,
-                                                            int experts, int splits, int top_k,
-                                                            bool renormalize, int32_t *chosen,
-                                                            float *weights) {
-    const int lane = threadIdx.x;
+// A workgroup has a token, a thread an expert: its place is the number of experts
+// before it, which a thread counts by itself, so that the time does not grow with top_k
+// (a maximum over the wave for every place took 7 us for 4 of 64, 14 for 8 of 256).
+__global__ __launch_bounds__(MOE_EXPERTS) void route_choose_kernel(const double *logits,
+                                                                  int64_t tokens, int experts,
+                                                                  int splits, int top_k,
+                                                                  bool renormalize, int32_t *chosen,
+                                                                  float *weights) {
+    // keys that order as logits do, a NaN below all others; those of no expert below that
+    __shared__ alignas(16) uint64_t keys[MOE_EXPERTS];
+    __shared__ double places[MOE_TOP_K], sums[MOE_EXPERTS / WAVE];
     const int64_t t = blockIdx.x;
-    double v[PER_LANE];
-    bool left[PER_LANE];
+    const int e = threadIdx.x, lane = e & (WAVE - 1);
+    double v = 0;
+    if (e < experts) {
+        const double *p = logits + t * experts + e;
+        for (int s = 0; s < splits; s += 4) {
+            double part[4];
 #pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) {
-        const int e = lane + WAVE * i;
-        left[i] = e < experts;
-        v[i] = 0;
-        if (!left[i]) continue;
-        for (int s = 0; s < splits; ++s) v[i] += logits[(s * tokens + t) * experts + e];
-    }
-    double mine = 0, first = 0;  // slot `lane`'s logit, the largest
-    int mine_e = 0;
-    for (int j = 0; j < top_k; ++j) {
-        // a lane's best; a NaN is below all others, and no expert (none left) below that
-        double best = 0;
-        int best_e = -1;
+            for (int i = 0; i < 4; ++i) part[i] = s + i < splits ? p[(s + i) * tokens * experts] : 0.0;
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-            if (!left[i]) continue;
-            if (best_e < 0 || v[i] > best || (best != best && v[i] == v[i])) {
-                best = v[i];
-                best_e = lane + WAVE * i;
-            }
+            for (int i = 0; i < 4; ++i) v += part[i];
         }
-        for (int off = 1; off < WAVE; off <<= 1) {
-            const double other = __shfl_xor(best, off, WAVE);
-            const int other_e = __shfl_xor(best_e, off, WAVE);
-            if (other_e < 0) continue;
-            const bool on = other == other, bn = best == best;
-            const bool better = best_e < 0 || (on && !bn) || other > best ||
-                                ((other == best || (!on && !bn)) && other_e < best_e);
-            if (better) best = other, best_e = other_e;
-        }
-        if (j == 0) first = best;
-        if (lane == j) mine = best, mine_e = best_e;
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i)
-            if (best_e == lane + WAVE * i) left[i] = false;
     }
-    const double p = lane < top_k ? exp(mine - first) : 0.0;
+    const uint64_t bits = (uint64_t)__double_as_longlong(v == 0 ? 0.0 : v);  // -0 equals 0
+    uint64_t key = bits >> 63 ? ~bits : bits | 1ull << 63;
+    if (v != v) key = 1;
+    if (e >= experts) key = 0;
+    keys[e] = key;
+    __syncthreads();
+    // before e: greater keys, and equal ones of lower ids: all equal ones of the waves
+    // before its own, none of those after
+    int place = 0;
+    const int own = __builtin_amdgcn_readfirstlane(e & ~(WAVE - 1));
+#pragma unroll 16
+    for (int j = 0; j < own; ++j) place += keys[j] >= key ? 1 : 0;
+#pragma unroll 16
+    for (int j = 0; j < WAVE; ++j) {
+        const uint64_t other = keys[own + j];
+        place += (j < lane ? other >= key : other > key) ? 1 : 0;
+    }
+#pragma unroll 16
+    for (int j = own + WAVE; j < (int)blockDim.x; ++j) place += keys[j] > key ? 1 : 0;
+    const bool mine = e < experts && place < top_k;
+    if (mine) places[place] = v;
+    __syncthreads();
+    const double first = places[0];
+    double p = 0;
+    if (mine || (!renormalize && e < experts)) p = exp(v - first);
+    // the sum in a fixed order: of the places, or over lanes and then waves
     double sum = 0;
     if (renormalize) {
-        sum = p;
+        __syncthreads();
+        if (mine) places[place] = p;
+        __syncthreads();
+        if (mine)
+            for (int j = 0; j < top_k; ++j) sum += places[j];
     } else {
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i)
-            if (lane + WAVE * i < experts) sum += exp(v[i] - first);
+        double part = p;
+        for (int off = 1; off < WAVE; off <<= 1) part += __shfl_xor(part, off, WAVE);
+        if (lane == 0) sums[e / WAVE] = part;
+        __syncthreads();
+        if (mine)
+            for (int w = 0; w < (int)blockDim.x / WAVE; ++w) sum += sums[w];
     }
-    for (int off = 1; off < WAVE; off <<= 1) sum += __shfl_xor(sum, off, WAVE);
-    if (lane < top_k) {
-        chosen[t * top_k + lane] = mine_e;
-        weights[t * top_k + lane] = (float)(p / sum);
+    if (mine) {
+        chosen[t * top_k + place] = e;
+        weights[t * top_k + place] = (float)(p / sum);
     }
 }
 
@@ -536,28 +551,41 @@ hipError_t launch_experts(const MoeArgs &A, int32_t *status, hipStream_t s) {
     return launch_tile<FMT, X_F32, 4>(A, status, s);
 }
 
-int route_splits(int64_t tokens, int64_t hidden, int experts) {
+// Shares of K: so many that there is a workgroup for each CU, and work for its waves.
+// Four waves of one step each where there are few tiles (1 x 2048 of 64 experts: 3.2 us),
+// sixteen where there are many, so that loads wait for each other less.
+struct RouteShape {
+    int waves, splits;
+};
+RouteShape route_shape(int64_t tokens, int64_t hidden, int experts) {
     const int64_t tiles = (tokens + 15) / 16 * ((experts + 15) / 16);
-    const int64_t most = (hidden + 32 * ROUTE_WAVES - 1) / (32 * ROUTE_WAVES);
-    int64_t splits = (256 + tiles - 1) / tiles;
-    if (splits > 16) splits = 16;
-    return (int)(splits < most ? splits : most);
+    const int waves = tiles < 32 ? 4 : 16;
+    const int64_t most = (hidden + 32 * waves - 1) / (32 * waves), want = (256 + tiles - 1) / tiles;
+    int splits = 1;
+    while (splits < 16 && splits < want && splits < most) splits *= 2;
+    return {waves, splits};
 }
 
 template <typename XT, typename RT>
 hipError_t launch_logits(const void *x, const void *router, double *logits, int64_t tokens,
-                         int64_t hidden, int experts, int splits, hipStream_t s) {
+                         int64_t hidden, int experts, RouteShape shape, hipStream_t s) {
     const int expert_tiles = (experts + 15) / 16;
-    const int64_t groups = (tokens + 15) / 16 * expert_tiles * splits;
-    route_logits_kernel<XT, RT><<<(uint32_t)groups, ROUTE_WAVES * WAVE, 0, s>>>(
-        (const XT *)x, (const RT *)router, logits, tokens, hidden, experts, expert_tiles, splits);
+    const uint32_t groups = (uint32_t)((tokens + 15) / 16 * expert_tiles * shape.splits);
+    if (shape.waves == 4)
+        route_logits_kernel<XT, RT, 4><<<groups, 4 * WAVE, 0, s>>>(
+            (const XT *)x, (const RT *)router, logits, tokens, hidden, experts, expert_tiles,
+            shape.splits);
+    else
+        route_logits_kernel<XT, RT, 16><<<groups, 16 * WAVE, 0, s>>>(
+            (const XT *)x, (const RT *)router, logits, tokens, hidden, experts, expert_tiles,
+            shape.splits);
     return hipGetLastError();
 }
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t tokens, int64_t hidden, int experts) {
-    return (size_t)route_splits(tokens, hidden, experts) * tokens * experts * sizeof(double);
+    return (size_t)route_shape(tokens, hidden, experts).splits * tokens * experts * sizeof(double);
 }
 
 hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidden,
@@ -565,29 +593,22 @@ hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidd
                         bool renormalize, int32_t *chosen, float *weights, void *workspace,
                         hipStream_t s) {
     double *logits = (double *)workspace;
-    const int splits = route_splits(tokens, hidden, experts);
+    const RouteShape shape = route_shape(tokens, hidden, experts);
     hipError_t e;
     if (x_bf16)
         e = router_bf16 ? launch_logits<uint16_t, uint16_t>(x, router, logits, tokens, hidden,
-                                                            experts, splits, s)
+                                                            experts, shape, s)
                         : launch_logits<uint16_t, float>(x, router, logits, tokens, hidden, experts,
-                                                         splits, s);
+                                                         shape, s);
     else
         e = router_bf16 ? launch_logits<float, uint16_t>(x, router, logits, tokens, hidden, experts,
-                                                         splits, s)
+                                                         shape, s)
                         : launch_logits<float, float>(x, router, logits, tokens, hidden, experts,
-                                                      splits, s);
+                                                      shape, s);
     if (e != hipSuccess) return e;
-    const dim3 grid((uint32_t)tokens);
-    if (experts <= WAVE)
-        route_choose_kernel<1><<<grid, WAVE, 0, s>>>(logits, tokens, experts, splits, top_k,
-                                                     renormalize, chosen, weights);
-    else if (experts <= 4 * WAVE)
-        route_choose_kernel<4><<<grid, WAVE, 0, s>>>(logits, tokens, experts, splits, top_k,
-                                                     renormalize, chosen, weights);
-    else
-        route_choose_kernel<16><<<grid, WAVE, 0, s>>>(logits, tokens, experts, splits, top_k,
-                                                      renormalize, chosen, weights);
+    const int threads = (experts + WAVE - 1) / WAVE * WAVE;
+    route_choose_kernel<<<(uint32_t)tokens, threads, 0, s>>>(logits, tokens, experts, shape.splits,
+                                                            top_k, renormalize, chosen, weights);
     return hipGetLastError();
 }
 
