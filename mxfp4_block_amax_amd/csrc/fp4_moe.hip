@@ -191,6 +191,11 @@ __device__ __forceinline__ int expert_pairs(const int32_t *ids, int pairs, int t
     return n;
 }
 
+// The slots of slot p's token, of up to 64.
+__device__ __forceinline__ uint64_t own_slots(int p, int top_k) {
+    return ((1ull << top_k) - 1) << (p / top_k * top_k);
+}
+
 // A value as N bf16 terms: each the nearest to what the ones before left.
 template <int N>
 __device__ __forceinline__ void store_terms(uint16_t *p, int64_t stride, float v) {
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
     using W = RowsAt<FMT, 2>;
     constexpr int NA = X_F32 ? 3 : 2, BLK = FMT == 0 ? 32 : 16;
     extern __shared__ u32x4_t lds[];
-    __shared__ uint16_t list[MOE_BLOCK];
+    __shared__ uint16_t lists[UP_WAVES][MOE_BLOCK];
     __shared__ int count;
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), waves = blockDim.x / WAVE;
@@ -245,29 +250,49 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
     const int block = (int)min((int64_t)MOE_BLOCK, A.tokens - token0);
     const int pairs = block * A.top_k;
     const int32_t *ids = A.ids + token0 * A.top_k;
-    // the workgroup's expert: one each, or one for every slot (its first of an expert)
+    // the workgroup's expert: one each, or one for every slot (its first of an expert);
+    // up to 64 pairs every wave looks at all of them by itself, in one load
+    const bool few = pairs <= WAVE;
     int e = blockIdx.y;
-    if (A.slots) {
-        if (e >= pairs) return;
-        const int slot = e;
-        e = ids[slot];
-        if (e < 0 || e >= A.W.experts) {
-            if (e != -1 && threadIdx.x == 0) flag(status, FLAG_EXPERT_INDEX);
-            return;
+    if (A.slots && e >= pairs) return;
+    uint16_t *list = lists[few ? wave : 0];
+    int n = 0;
+    if (few) {
+        const int id = lane < pairs ? ids[lane] : -1;
+        if (A.slots) e = __builtin_amdgcn_readlane(id, blockIdx.y);
+        if (blockIdx.x == 0 && wave == 0 && (A.slots || e == 0) &&
+            __ballot(id < -1 || id >= A.W.experts) != 0 && lane == 0)
+            flag(status, FLAG_EXPERT_INDEX);
+        if (e < 0 || e >= A.W.experts) return;
+        const uint64_t all = __ballot(id == e);
+        if (A.slots && (all & ((1ull << blockIdx.y) - 1)) != 0) return;
+        const uint64_t mine = all & own_slots(lane, A.top_k) & ((1ull << lane) - 1);
+        const uint64_t firsts = __ballot((all >> lane & 1) != 0 && mine == 0);
+        n = __builtin_popcountll(firsts);
+        if (firsts >> lane & 1)
+            list[__builtin_popcountll(firsts & ((1ull << lane) - 1))] = (uint16_t)lane;
+    } else {
+        if (A.slots) {
+            const int slot = e;
+            e = ids[slot];
+            if (e < 0 || e >= A.W.experts) {
+                if (e != -1 && threadIdx.x == 0) flag(status, FLAG_EXPERT_INDEX);
+                return;
+            }
+            bool earlier = false;
+            for (int p = threadIdx.x; p < slot; p += blockDim.x) earlier = earlier || ids[p] == e;
+            if (__syncthreads_or(earlier)) return;
+        } else if (blockIdx.x == 0 && e == 0) {
+            for (int p = threadIdx.x; p < pairs; p += blockDim.x)
+                if (ids[p] < -1 || ids[p] >= A.W.experts) flag(status, FLAG_EXPERT_INDEX);
         }
-        bool earlier = false;
-        for (int p = threadIdx.x; p < slot; p += blockDim.x) earlier = earlier || ids[p] == e;
-        if (__syncthreads_or(earlier)) return;
-    } else if (blockIdx.x == 0 && e == 0) {
-        for (int p = threadIdx.x; p < pairs; p += blockDim.x)
-            if (ids[p] < -1 || ids[p] >= A.W.experts) flag(status, FLAG_EXPERT_INDEX);
+        if (wave == 0) {
+            const int found = expert_pairs(ids, pairs, A.top_k, e, list);
+            if (lane == 0) count = found;
+        }
+        __syncthreads();
+        n = __builtin_amdgcn_readfirstlane(count);
     }
-    if (wave == 0) {
-        const int n = expert_pairs(ids, pairs, A.top_k, e, list);
-        if (lane == 0) count = n;
-    }
-    __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(count);
     if (n == 0) return;
 
     const int K = (int)A.W.hidden, inner = (int)A.W.inner, row0 = blockIdx.x * 16;
@@ -351,6 +376,46 @@ struct MoePlan {
 
 constexpr int DOWN_WAVES = 16;
 static_assert(DOWN_WAVES * WAVE >= MOE_EXPERTS, "a thread an expert");
+
+// The plan of up to 64 pairs, by one wave, experts in the order they are named first:
+// no barriers but the one after it (the other way took a third of the kernel's time for
+// a single token).  Returns the items.
+template <int TOKENS>
+__device__ int make_small_plan(const MoePlan &plan, const int32_t *ids, const float *weights,
+                               int pairs, int top_k, int experts) {
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int e = lane < pairs ? ids[lane] : -1;
+    const float w = lane < pairs ? weights[lane] : 0.0f;
+    const uint64_t token = own_slots(lane, top_k), below = (1ull << lane) - 1;
+    uint64_t left = __ballot(e >= 0 && e < experts);
+    int items = 0, at = 0;
+    while (left != 0) {
+        const int expert = __builtin_amdgcn_readlane(e, __builtin_ctzll(left));
+        const uint64_t all = __ballot(e == expert);
+        left &= ~all;
+        const bool first = (all >> lane & 1) != 0 && (all & token & below) == 0;
+        const uint64_t firsts = __ballot(first);
+        float share = w;
+        if (firsts != all)
+            for (int j = 1; j < top_k; ++j) {  // the token's other slots of this expert
+                const int other = lane + j;
+                const float more = __shfl(w, other & (WAVE - 1), WAVE);
+                if (other < WAVE && (all & token) >> other & 1) share += more;
+            }
+        const int n = __builtin_popcountll(firsts);
+        if (first) {
+            const int place = at + __builtin_popcountll(firsts & below);
+            plan.pair[place] = (uint16_t)lane;
+            plan.share[place] = share;
+        }
+        for (int i = 0; i < n; i += TOKENS, ++items)
+            if (lane == 0)
+                plan.items[items] = {(uint16_t)expert, (uint16_t)(at + i),
+                                     (uint16_t)min(n - i, TOKENS), 0};
+        at += n;
+    }
+    return items;
+}
 
 // Returns the items.
 template <int TOKENS>
@@ -443,8 +508,20 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, i
 
     for (int i = threadIdx.x; i < DOWN_WAVES * block_tokens * 4; i += DOWN_WAVES * WAVE)
         sums[i] = {0, 0, 0, 0};
-    const int items = make_plan<TOKENS>(plan, A.ids + token0 * A.top_k, A.weights + token0 * A.top_k,
-                                        pairs, A.top_k, A.W.experts);
+    const int32_t *ids = A.ids + token0 * A.top_k;
+    const float *weights = A.weights + token0 * A.top_k;
+    int items;
+    if (pairs <= WAVE) {
+        __shared__ int found;
+        if (wave == 0) {
+            const int n = make_small_plan<TOKENS>(plan, ids, weights, pairs, A.top_k, A.W.experts);
+            if (lane == 0) found = n;
+        }
+        __syncthreads();
+        items = __builtin_amdgcn_readfirstlane(found);
+    } else {
+        items = make_plan<TOKENS>(plan, ids, weights, pairs, A.top_k, A.W.experts);
+    }
 
     const uint16_t *act0 = A.act + token0 * A.top_k * NA * K;
     const Rsrc act = span(act0, pairs * NA * K * 2);
