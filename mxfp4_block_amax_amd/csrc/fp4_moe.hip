@@ -229,7 +229,7 @@ __device__ __forceinline__ void multiply_tail(const uint8_t *codes, const uint8_
     w4_multiply<FMT, TERMS>(w, [&](int, int i, int n) { return b[i].p[n]; }, acc, top);
 }
 
-constexpr int UP_WAVES = 8;
+constexpr int UP_WAVES = 4;
 
 // Gate and up: a workgroup has 16 rows of each of one expert and the tokens of a
 // block that go there, up to TOKENS of them at a time; its waves share K = hidden.
