@@ -52,7 +52,7 @@ __global__ __launch_bounds__(WAVES *WAVE) void linear_w4_kernel(LinearArgs A) {
         x_at[n] = (uint32_t)(p.row * K + p.k) * (uint32_t)sizeof(XT);
     }
     constexpr int BLK = FMT == 0 ? 32 : 16;
-    using W = std::conditional_t<PACKED, PackedAt<FMT>, RowsAt<FMT, 2>>;
+    using W = std::conditional_t<PACKED, PackedAt<FMT, 2>, RowsAt<FMT, 2>>;
     u32x4_t *mine = lds + wave * (X::PIECES + W::LDS);
     const uint8_t *codes = A.codes + (int64_t)row0 * (K / 2);
     const uint8_t *scales = A.scales + (int64_t)row0 * (K / BLK);
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(WAVES *WAVE) void linear_w4_kernel(LinearArgs A) {
     uint32_t top[2] = {0, 0};
     const int groups = (uint32_t)K / W4_GROUP;
     const W weights = [&] {
-        if constexpr (PACKED) return W(codes, scales, K);
+        if constexpr (PACKED) return W(codes, scales, A.N - row0, K);
         else return W(codes, scales, A.N - row0, 16, K, mine + X::PIECES);
     }();
     multiply_groups<FMT, PACKED, W, X>(
@@ -128,61 +128,61 @@ hipError_t launch_tile(const LinearArgs &A, hipStream_t s) {
     return hipGetLastError();
 }
 
-// More tokens, bf16: 16 TILES of them (32 or 64) and 128 weight rows a workgroup.  Four
-// waves side by side have 32 rows each, two such rows of waves take every other group of
-// K.  The activations of both waves' pairs (a slab of 2 x 256 K) are in LDS for all, the
-// next slab's on their way in registers.  64 x 28672 x 8192: the products take 12 us of
-// the matrix units, and as many of LDS, while the weights take 24 of HBM.
-constexpr int WIDE_ROW_WAVES = 4, WIDE_K_WAVES = 2, WIDE_ROWS = 32 * WIDE_ROW_WAVES;
+// More tokens, bf16: 16 TILES of them and 128 weight rows a workgroup.  A wave has 64 rows
+// (what it reads of the activations then serves as many products as the matrix units do
+// while LDS gives them), two waves side by side; four such pairs of waves take the groups
+// of K in turn.  A slab, a stretch of each of the four's groups, of the activations is in
+// LDS for all; the next one is on its way in registers.
+constexpr int WIDE_PARTS = 4, WIDE_ROW_WAVES = 2, WIDE_K_WAVES = 4;
+constexpr int WIDE_ROWS = 16 * WIDE_PARTS * WIDE_ROW_WAVES;
 constexpr int WIDE_THREADS = WIDE_ROW_WAVES * WIDE_K_WAVES * WAVE;
 
 template <int FMT, bool PACKED, int TILES>
 __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearArgs A) {
-    constexpr int BLK = FMT == 0 ? 32 : 16;
-    constexpr int SLAB = WIDE_K_WAVES * 2 * TILES * 256;  // pieces: [wave][stretch][tile][v][row ^ v]
+    constexpr int BLK = FMT == 0 ? 32 : 16, PARTS = WIDE_PARTS;
+    constexpr int SLAB = WIDE_K_WAVES * TILES * 256;  // pieces: [K wave][tile][v][row ^ v]
     constexpr int LOADS = SLAB / WIDE_THREADS;
-    using W = std::conditional_t<PACKED, PackedAt<FMT>, RowsAt<FMT, 2>>;
+    using W = std::conditional_t<PACKED, PackedAt<FMT, PARTS>, RowsAt<FMT, PARTS>>;
     extern __shared__ u32x4_t lds[];  // [2][SLAB], then the waves' own
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int k_wave = wave % WIDE_K_WAVES, row_wave = wave / WIDE_K_WAVES;
     const int r = lane & 15, g = lane >> 4, part = PACKED ? packed_group(g) : g;
     const int m0 = blockIdx.y * (16 * TILES), K = A.K;
-    const int row0 = blockIdx.x * WIDE_ROWS + 32 * row_wave;
+    const int row0 = blockIdx.x * WIDE_ROWS + 16 * PARTS * row_wave;
     const int tokens = min(16 * TILES, A.M - m0);
     const int groups = (uint32_t)K / W4_GROUP;
-    const int slabs = (groups + WIDE_K_WAVES - 1) / WIDE_K_WAVES * 2;  // two pairs a group
+    const int slabs = (groups + WIDE_K_WAVES - 1) / WIDE_K_WAVES * 4;  // four stretches a group
 
     // a wave past the last row has the last ones' weights, for sums that are not stored
     const int first = min(row0, (A.N - 1) / 32 * 32);
     const uint8_t *codes = A.codes + (int64_t)first * (K / 2);
     const uint8_t *scales = A.scales + (int64_t)first * (K / BLK);
     const W w = [&] {
-        if constexpr (PACKED) return W(codes, scales, K);
+        if constexpr (PACKED) return W(codes, scales, A.N - first, K);
         else return W(codes, scales, A.N - first, 16, K, lds + 2 * SLAB + wave * W::LDS);
     }();
     const Rsrc x = span((const uint16_t *)A.x + (int64_t)m0 * K, tokens * K * 2);
     const auto group_k = [&](int n) { return n < groups ? (uint32_t)(n * W4_GROUP) : NOWHERE; };
     const auto from = [](uint32_t k, int more) { return k == NOWHERE ? k : k + more; };
 
-    // a thread's load n of a slab: 32 lanes have a row's pair
+    // a thread's load n of a slab: 16 lanes have a row's stretch
     u32x4_t xs[LOADS];
     const auto load_slab = [&](int s) {
 #pragma unroll
         for (int n = 0; n < LOADS; ++n) {
-            const int e = n * WIDE_THREADS + threadIdx.x, q = e & 31, v = e / 32 % WIDE_K_WAVES;
-            const int row = e / (32 * WIDE_K_WAVES);
-            const uint32_t k = group_k(s / 2 * WIDE_K_WAVES + v);
-            xs[n] = load16(x, (uint32_t)(row * K + 8 * q) * 2 +
-                                  (k == NOWHERE ? NOWHERE / 2 : (k + (s & 1) * 2 * W4_STRETCH) * 2));
+            const int e = n * WIDE_THREADS + threadIdx.x, v = e / 16 % WIDE_K_WAVES;
+            const uint32_t k = group_k(s / 4 * WIDE_K_WAVES + v);
+            xs[n] = load16(x, (uint32_t)(e / (16 * WIDE_K_WAVES) * K + 8 * (e & 15)) * 2 +
+                                  (k == NOWHERE ? NOWHERE / 2 : (k + (s & 3) * W4_STRETCH) * 2));
         }
     };
     const auto store_slab = [&](u32x4_t *to) {
 #pragma unroll
         for (int n = 0; n < LOADS; ++n) {
-            const int e = n * WIDE_THREADS + threadIdx.x, q = e & 31, v = e / 32 % WIDE_K_WAVES;
-            const int row = e / (32 * WIDE_K_WAVES), piece = q & 15;
-            to[(((v * 2 + q / 16) * TILES + row / 16) * 16 + piece) * 16 + ((row & 15) ^ piece)] = xs[n];
+            const int e = n * WIDE_THREADS + threadIdx.x, piece = e & 15, v = e / 16 % WIDE_K_WAVES;
+            const int row = e / (16 * WIDE_K_WAVES);
+            to[((v * TILES + row / 16) * 16 + piece) * 16 + ((row & 15) ^ piece)] = xs[n];
         }
     };
     load_slab(0);
@@ -193,43 +193,40 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
     store_slab(lds);
     lds_barrier();
 
-    f32x4_t acc[2][TILES] = {};
-    uint32_t top[2] = {0, 0};
-    for (int s = 0; s < slabs; s += 2) {
-        const uint32_t next = group_k(s / 2 * WIDE_K_WAVES + WIDE_K_WAVES + k_wave);
+    f32x4_t acc[PARTS][TILES] = {};
+    uint32_t top[PARTS] = {};
+    for (int s = 0; s < slabs; s += 4) {
+        const uint32_t next = group_k(s / 4 * WIDE_K_WAVES + WIDE_K_WAVES + k_wave);
         const typename W::Scales here = scale;
         w.put(here);
         scale = w.load_scales(next);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
             load_slab(s + j + 1);
             __builtin_amdgcn_sched_barrier(0);
-            w.spread(pair[j]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                W4Unit u[2];
-                w.units(here, pair[j], 2 * j + h, u);
-                const u32x4_t *mine = lds + j * SLAB + (k_wave * 2 + h) * TILES * 256;
-                w4_multiply<FMT, 1>(
-                    u,
-                    [&](int t, int i, int) {
-                        const int v = 4 * part + i;
-                        return __builtin_bit_cast(bf16x8_t, mine[(t * 16 + v) * 16 + (r ^ v)]);
-                    },
-                    acc, top);
-            }
-            pair[j] = w.load_pair(from(next, 2 * W4_STRETCH * j));
+            if (j % 2 == 0) w.spread(pair[j / 2]);
+            W4Unit u[PARTS];
+            w.units(here, pair[j / 2], j, u);
+            const u32x4_t *mine = lds + (j & 1) * SLAB + k_wave * TILES * 256;
+            w4_multiply<FMT, 1>(
+                u,
+                [&](int t, int i, int) {
+                    const int v = 4 * part + i;
+                    return __builtin_bit_cast(bf16x8_t, mine[(t * 16 + v) * 16 + (r ^ v)]);
+                },
+                acc, top);
+            if (j % 2 == 1) pair[j / 2] = w.load_pair(from(next, W4_STRETCH * (j - 1)));
             __builtin_amdgcn_sched_barrier(0);
-            store_slab(lds + (j ^ 1) * SLAB);
+            store_slab(lds + ((j + 1) & 1) * SLAB);
             lds_barrier();
         }
     }
     if constexpr (!PACKED) {
         // the stretches past the last whole group, in turn
         for (int q = groups * W4_GROUP + W4_STRETCH * k_wave; q < K; q += W4_STRETCH * WIDE_K_WAVES) {
-            W4Unit u[2];
+            W4Unit u[PARTS];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < PARTS; ++p) {
                 const int64_t n = min(16 * p + r, A.N - 1 - first);
                 u[p] = load_tail<FMT>(codes + n * (K / 2), scales + n * (K / BLK), q, K);
             }
@@ -246,25 +243,25 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
         }
     }
     if constexpr (FMT == 0) w4_nan_rows(top, acc);
-    __syncthreads();
-    f32x4_t *sums = (f32x4_t *)lds;  // of the second row of waves
-    constexpr int EACH = WIDE_ROW_WAVES * 2 * TILES * WAVE;
-    static_assert(WIDE_K_WAVES == 2 && EACH <= 2 * SLAB);
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int t = 0; t < TILES; ++t)
-            if (k_wave == 1) sums[((row_wave * 2 + p) * TILES + t) * WAVE + lane] = acc[p][t];
-    __syncthreads();
-    if (k_wave == 1) return;
+    // the K waves' sums, one part after the other, added in their order
+    f32x4_t *sums = (f32x4_t *)lds;  // [K wave][row wave][TILES][64]
+    constexpr int EACH = WIDE_ROW_WAVES * TILES * WAVE;
+    static_assert(WIDE_K_WAVES * EACH <= 2 * SLAB);
     const float s_g = FMT == 0 ? 1.0f : *A.s_g;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < PARTS; ++p) {
+        __syncthreads();
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-            f32x4_t y = acc[p][t] + sums[((row_wave * 2 + p) * TILES + t) * WAVE + lane];
+        for (int t = 0; t < TILES; ++t)
+            sums[k_wave * EACH + (row_wave * TILES + t) * WAVE + lane] = acc[p][t];
+        __syncthreads();
+        for (int i = threadIdx.x; i < EACH; i += WIDE_THREADS) {
+            f32x4_t y = sums[i];
+#pragma unroll
+            for (int v = 1; v < WIDE_K_WAVES; ++v) y += sums[v * EACH + i];
             if constexpr (FMT == 1) y = y * s_g;
-            const int m = m0 + 16 * t + r, n = row0 + 16 * p + 4 * g;
+            const int l = i % WAVE, m = m0 + 16 * (i / WAVE % TILES) + (l & 15);
+            const int n = blockIdx.x * WIDE_ROWS + i / (TILES * WAVE) * 16 * PARTS + 16 * p + 4 * (l >> 4);
             if (m >= A.M) continue;
             const int64_t to = (int64_t)m * A.N + n;
 #pragma unroll
@@ -274,12 +271,13 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
                 else ((float *)A.c)[to + j] = y[j];
             }
         }
+    }
 }
 
 template <int FMT, bool PACKED, int TILES>
 hipError_t launch_wide(const LinearArgs &A, hipStream_t s) {
-    const size_t lds = 2 * WIDE_K_WAVES * 2 * TILES * 256 * 16 +
-                       (PACKED ? 0 : WIDE_THREADS / WAVE * RowsAt<FMT, 2>::LDS * 16);
+    const size_t lds = 2 * WIDE_K_WAVES * TILES * 256 * 16 +
+                       (PACKED ? 0 : WIDE_THREADS / WAVE * RowsAt<FMT, WIDE_PARTS>::LDS * 16);
     const dim3 grid((uint32_t)((A.N + WIDE_ROWS - 1) / WIDE_ROWS),
                     (uint32_t)((A.M + 16 * TILES - 1) / (16 * TILES)));
     linear_w4_wide_kernel<FMT, PACKED, TILES><<<grid, WIDE_THREADS, lds, s>>>(A);
@@ -291,8 +289,12 @@ hipError_t launch_tokens(const LinearArgs &A, hipStream_t s) {
     if (A.M <= 4) return launch_tile<FMT, X_F32, PACKED, 4>(A, s);
     if (A.M <= 8) return launch_tile<FMT, X_F32, PACKED, 8>(A, s);
     if constexpr (!X_F32) {
-        if (A.M > 32) return launch_wide<FMT, PACKED, 4>(A, s);
-        if (A.M > 16) return launch_wide<FMT, PACKED, 2>(A, s);
+        // as many tokens a workgroup as still leave one for most CUs
+        const int64_t row_tiles = (A.N + WIDE_ROWS - 1) / WIDE_ROWS;
+        const int64_t tokens = (A.M + 15) / 16;
+        if (A.M > 32 && row_tiles * ((tokens + 3) / 4) > 128) return launch_wide<FMT, PACKED, 4>(A, s);
+        if (A.M > 16 && row_tiles * ((tokens + 1) / 2) > 64) return launch_wide<FMT, PACKED, 2>(A, s);
+        if (A.M > 16) return launch_wide<FMT, PACKED, 1>(A, s);
     }
     return launch_tile<FMT, X_F32, PACKED, 16>(A, s);
 }

@@ -183,11 +183,13 @@ struct RowsAt {
     struct Pair {
         u32x4_t v[2 * PARTS];
     };
+    static constexpr int EACH = FMT == 0 ? 1 : 2;                       // scale pieces of a row
+    static constexpr int SCALE_LOADS = (16 * PARTS * EACH + WAVE - 1) / WAVE;
     struct Scales {
-        u32x4_t v;
+        u32x4_t v[SCALE_LOADS];
     };
     Rsrc codes, scales;
-    uint32_t code[2 * PARTS], scale;
+    uint32_t code[2 * PARTS], scale[SCALE_LOADS];
     u32x4_t *lds;  // the wave's: [row][8 pieces of a pair], [part][row] scales
 
     // rows: of those from row0 on, how many there are; part p has rows row0 + p *
@@ -195,7 +197,7 @@ struct RowsAt {
     __device__ __forceinline__ RowsAt(const uint8_t *code_base, const uint8_t *scale_base, int rows,
                                       int part_rows, int K, u32x4_t *wave_lds)
         : lds(wave_lds) {
-        constexpr int BLK = FMT == 0 ? 32 : 16, EACH = FMT == 0 ? 1 : 2;  // scale loads of a row
+        constexpr int BLK = FMT == 0 ? 32 : 16;
         const int lane = threadIdx.x & (WAVE - 1);
         const int code_row = (uint32_t)K / 2, scale_row = (uint32_t)K / BLK;
         const int have = min(rows, (PARTS - 1) * part_rows + 16);
@@ -205,14 +207,22 @@ struct RowsAt {
         for (int n = 0; n < 2 * PARTS; ++n)
             code[n] = (uint32_t)(n / 2 * part_rows + n % 2 * 8 + (lane >> 3)) * (uint32_t)code_row +
                       16 * (lane & 7);
-        const int row = lane / EACH;
-        scale = row < 16 * PARTS ? (uint32_t)(row / 16 * part_rows + row % 16) * (uint32_t)scale_row +
-                                       16 * (lane % EACH)
-                                 : NOWHERE;
+#pragma unroll
+        for (int n = 0; n < SCALE_LOADS; ++n) {
+            const int row = (n * WAVE + lane) / EACH;
+            scale[n] = row < 16 * PARTS
+                           ? (uint32_t)(row / 16 * part_rows + row % 16) * (uint32_t)scale_row +
+                                 16 * (lane % EACH)
+                           : NOWHERE;
+        }
     }
     // of the group or pair at k (a group past the end: NOWHERE)
     __device__ __forceinline__ Scales load_scales(uint32_t k) const {
-        return {load16(scales, scale + (k == NOWHERE ? k / 2 : k / (FMT == 0 ? 32 : 16)))};
+        Scales s;
+#pragma unroll
+        for (int n = 0; n < SCALE_LOADS; ++n)
+            s.v[n] = load16(scales, scale[n] + (k == NOWHERE ? k / 2 : k / (FMT == 0 ? 32 : 16)));
+        return s;
     }
     __device__ __forceinline__ Pair load_pair(uint32_t k) const {
         Pair r;
@@ -223,7 +233,9 @@ struct RowsAt {
     }
     __device__ __forceinline__ void put(const Scales &s) const {
         const int lane = threadIdx.x & (WAVE - 1);
-        if (lane < 16 * PARTS * (FMT == 0 ? 1 : 2)) lds[128 + lane] = s.v;
+#pragma unroll
+        for (int n = 0; n < SCALE_LOADS; ++n)
+            if (n * WAVE + lane < 16 * PARTS * EACH) lds[128 + n * WAVE + lane] = s.v[n];
     }
     // to the products' order, v[PARTS * stretch + part]: piece v of row r goes through
     // 8 r + (v ^ r), which spreads what is written and what is read over the banks
@@ -254,7 +266,7 @@ struct RowsAt {
     }
 };
 
-// Two parts (a row tile of 32) of a packed operand: a load has 32 rows, 32 values of
+// Row tiles of 32, two parts each, of a packed operand: a load has 32 rows, 32 values of
 // each of two, rows l % 32 and values 32 (l / 32) .. of a K step.  Exchanging odd groups
 // of 16 lanes of one step with even ones of the next gives a register rows 0 .. 15 and
 // another rows 16 .. 31, with the 32s 0, 2, 1, 3 of the stretch in lane groups 0 .. 3.
@@ -266,58 +278,77 @@ __device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {
     b = r[1];
 }
 
-template <int FMT>
+template <int FMT, int PARTS>
 struct PackedAt {
-    static constexpr int LDS = 0;
+    static constexpr int LDS = 0, TILES = PARTS / 2;
     struct Pair {
-        u32x4_t v[4];
+        u32x4_t v[2 * PARTS];  // [tile][K step], spread [stretch][part]
     };
     struct Scales {
-        std::conditional_t<FMT == 0, u32x2_t, u32x4_t> v;
+        std::conditional_t<FMT == 0, u32x2_t, u32x4_t> v[TILES];
     };
     Rsrc codes, scales;
+    uint32_t code_tile, scale_tile;
 
-    __device__ __forceinline__ PackedAt(const uint8_t *code_base, const uint8_t *scale_base, int K) {
-        codes = span(code_base, 16 * K);
-        scales = span(scale_base, FMT == 0 ? K : 2 * K);
+    // rows: of those from the base on, how many there are
+    __device__ __forceinline__ PackedAt(const uint8_t *code_base, const uint8_t *scale_base, int rows,
+                                        int K)
+        : code_tile(16 * K), scale_tile(FMT == 0 ? K : 2 * K) {
+        const int have = min((rows + 31) / 32, TILES);
+        codes = span(code_base, have * (int)code_tile);
+        scales = span(scale_base, have * (int)scale_tile);
     }
     __device__ __forceinline__ Scales load_scales(uint32_t k) const {
         const int lane = threadIdx.x & (WAVE - 1);
-        if constexpr (FMT == 0)
-            return {__builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
-                                                    scales, (int)(k + 8 * lane), 0, 0))};
-        else return {load16(scales, (k == NOWHERE ? k : 2 * k) + 16 * lane)};
+        Scales s;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            if constexpr (FMT == 0)
+                s.v[t] = __builtin_bit_cast(
+                    u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                 scales, (int)(k + t * scale_tile + 8 * lane), 0, 0));
+            else
+                s.v[t] = load16(scales, (k == NOWHERE ? k : 2 * k) + t * scale_tile + 16 * lane);
+        }
+        return s;
     }
     __device__ __forceinline__ Pair load_pair(uint32_t k) const {
         const int lane = threadIdx.x & (WAVE - 1);
         Pair r;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            r.v[n] = load16_streamed(codes, (k == NOWHERE ? k : 16 * k) + 1024 * n + 16 * lane);
+        for (int n = 0; n < 2 * PARTS; ++n)
+            r.v[n] = load16_streamed(codes, (k == NOWHERE ? k : 16 * k) + n / 4 * code_tile +
+                                                1024 * (n & 3) + 16 * lane);
         return r;
     }
     __device__ __forceinline__ void put(const Scales &) const {}
     __device__ __forceinline__ void spread(Pair &pair) const {
+        u32x4_t out[2 * PARTS];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t x = pair.v[2 * h][i], y = pair.v[2 * h + 1][i];
-                swap16(x, y);
-                pair.v[2 * h][i] = x;
-                pair.v[2 * h + 1][i] = y;
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x = pair.v[4 * t + 2 * h][i], y = pair.v[4 * t + 2 * h + 1][i];
+                    swap16(x, y);
+                    out[PARTS * h + 2 * t][i] = x;
+                    out[PARTS * h + 2 * t + 1][i] = y;
+                }
+#pragma unroll
+        for (int n = 0; n < 2 * PARTS; ++n) pair.v[n] = out[n];
     }
     __device__ __forceinline__ void units(const Scales &s, const Pair &pair, int j,
-                                          W4Unit (&w)[2]) const {
-        const int odd = (threadIdx.x >> 4) & 1;
-        w[0].codes = pair.v[2 * (j & 1)];
-        w[1].codes = pair.v[2 * (j & 1) + 1];
-        uint32_t s0 = s.v[FMT == 0 ? j / 2 : j], s1 = s0;
-        swap16(s0, s1);
-        const int by = FMT == 0 ? 16 * (j & 1) + 8 * odd : 16 * odd;
-        w[0].scale = FMT == 0 ? (s0 >> by) & 0xFFu : s0 >> by;
-        w[1].scale = FMT == 0 ? (s1 >> by) & 0xFFu : s1 >> by;
+                                          W4Unit (&w)[PARTS]) const {
+        const int odd = (threadIdx.x >> 4) & 1, by = FMT == 0 ? 16 * (j & 1) + 8 * odd : 16 * odd;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            uint32_t s0 = s.v[t][FMT == 0 ? j / 2 : j], s1 = s0;
+            swap16(s0, s1);
+            w[2 * t] = {pair.v[PARTS * (j & 1) + 2 * t], FMT == 0 ? (s0 >> by) & 0xFFu : s0 >> by};
+            w[2 * t + 1] = {pair.v[PARTS * (j & 1) + 2 * t + 1],
+                            FMT == 0 ? (s1 >> by) & 0xFFu : s1 >> by};
+        }
     }
 };
 
