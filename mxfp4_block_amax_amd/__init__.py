@@ -660,13 +660,13 @@ def linear_mxfp4(x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torch.Tenso
 # As the cache calls further down, the layers of a decoding step check each
 # property once and pass pointers as integers: the host's time counts there.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _on(x: torch.Tensor, fn, *args):
-    """fn(*args, stream) on x's device and its current stream."""
-    device = x.get_device()
-    if device == torch.cuda.current_device():
+def _on(device: int, fn, *args):
+    """fn(*args, stream) on a device and its current stream."""
+    if device == _current_device():
         code = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -675,30 +675,48 @@ def _on(x: torch.Tensor, fn, *args):
         _ok(code)
 
 
-def _w4_output(fmt, x, K, N, global_scale, out_dtype, out):
-    """What both layouts of a four-bit weight check; (x's rows, its dtype's code,
-    the tensor scale's pointer, the output)."""
-    if fmt != MXFP4 and fmt != NVFP4:
-        raise ValueError("fmt must be MXFP4 or NVFP4")
-    dtype, shape = x.dtype, x.shape
-    code = _DTYPES.get(dtype)
+def _bytes(t: torch.Tensor, numel: int, what: str, device: int) -> int:
+    """The address of a contiguous uint8 tensor of `numel` elements on `device`."""
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"{what} must be a uint8 tensor")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous on the same device as x")
+    if t.numel() != numel:
+        raise ValueError(f"{what} has {t.numel()} elements, needs {numel}")
+    return t.data_ptr()
+
+
+def _scalar(t, what: str, device: int) -> int:
+    """The address of a tensor scale."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
+        raise TypeError(f"{what} must be a float32 tensor")
+    if t.get_device() != device or t.numel() < 1:
+        raise ValueError(f"{what} must hold at least one element, on the same device as x")
+    return t.data_ptr()
+
+
+def _dense(x: torch.Tensor):
+    """(device, dtype's code) of activations: a contiguous device tensor."""
+    code = _DTYPES.get(x.dtype)
     if code is None:
-        code = _dtype_code(dtype)
-    if len(shape) < 1 or shape[-1] != K:
-        raise ValueError(f"x must have {K} columns, as the weight")
+        code = _dtype_code(x.dtype)
+    device = x.get_device()
+    if device < 0:
+        raise TypeError("expected a device tensor")
     if not x.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    if fmt == MXFP4:
-        s_g = None
-    else:
-        _check_global_scale(global_scale, "global_scale", x.device)
-        s_g = global_scale.data_ptr()
+    return device, code
+
+
+def _output(out, shape, dtype, x, out_dtype):
+    """The output tensor and its dtype's code."""
     if out is None:
-        out = torch.empty(*shape[:-1], N, dtype=out_dtype or dtype, device=x.device)
-    elif (out.shape != (*shape[:-1], N) or out.device != x.device or not out.is_contiguous()
-          or (out_dtype is not None and out.dtype != out_dtype)):
-        raise ValueError("out must be a contiguous tensor of x's rows and N columns, of out_dtype")
-    return x.numel() // K, code, s_g, out
+        out = torch.empty(shape, dtype=out_dtype or dtype, device=x.device)
+    elif (out.shape != shape or out.get_device() != x.get_device() or not out.is_contiguous()
+          or (out_dtype is not None and out.dtype is not out_dtype)):
+        raise ValueError("out must be a contiguous tensor of the result's shape, of out_dtype")
+    code = _DTYPES.get(out.dtype)
+    return out, _dtype_code(out.dtype) if code is None else code
 
 
 def linear_w4(fmt: int, x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torch.Tensor,
@@ -706,42 +724,53 @@ def linear_w4(fmt: int, x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torc
     """Linear layer of few tokens: x [.., K] (fp32 or bf16, not quantized) times
     the FP4 weight Bt [N, K] (codes [N, K/2], scales [N, K/block], for NVFP4 its
     tensor scale).  Returns [.., N] of x's dtype, or of out_dtype."""
-    if bt_codes.dim() != 2 or not x.is_cuda:
-        raise ValueError("expected device tensors, the weight's codes as [N, K/2]")
-    N, kh = bt_codes.shape
-    _check_u8(bt_codes, N * kh, "bt_codes", x.device)
-    _check_u8(bt_scales, N * (2 * kh) // (32 if fmt == MXFP4 else 16), "bt_scales", x.device)
-    M, code, s_g, out = _w4_output(fmt, x, 2 * kh, N, global_scale, out_dtype, out)
+    weight, shape = bt_codes.shape, x.shape
+    if fmt != MXFP4 and fmt != NVFP4:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    if len(weight) != 2 or len(shape) < 1 or shape[-1] != 2 * weight[1]:
+        raise ValueError("x must be [.., K], the weight's codes [N, K/2]")
+    device, code = _dense(x)
+    N, kh = weight
+    codes = _bytes(bt_codes, N * kh, "bt_codes", device)
+    scales = _bytes(bt_scales, N * kh // (16 if fmt == MXFP4 else 8), "bt_scales", device)
+    s_g = None if fmt == MXFP4 else _scalar(global_scale, "global_scale", device)
+    out, out_code = _output(out, (*shape[:-1], N), x.dtype, x, out_dtype)
+    M = x.numel() // (2 * kh) if kh else 0
     if M > 0:
-        _on(x, (_lib or lib()).fp4_linear_w4, fmt, x.data_ptr(), code, M, 2 * kh,
-            bt_codes.data_ptr(), bt_scales.data_ptr(), s_g, N, out.data_ptr(),
-            _dtype_code(out.dtype))
+        _on(device, (_lib or lib()).fp4_linear_w4, fmt, x.data_ptr(), code, M, 2 * kh, codes,
+            scales, s_g, N, out.data_ptr(), out_code)
     return out
 
 
 def linear_w4_packed(fmt: int, x: torch.Tensor, bt_packed: torch.Tensor, N: int,
                      global_scale=None, out_dtype=None, out=None) -> torch.Tensor:
     """linear_w4 with a weight of pack_mxfp4_operand or pack_nvfp4_operand."""
-    if not x.is_cuda:
-        raise TypeError("expected a device tensor")
-    K, N = x.shape[-1], int(N)
-    need = (packed_operand_bytes if fmt == MXFP4 else nv_packed_operand_bytes)(N, K)
+    if fmt != MXFP4 and fmt != NVFP4:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    device, code = _dense(x)
+    shape = x.shape
+    K, N = shape[-1] if shape else 0, int(N)
+    L = _lib or lib()
+    need = (L.fp4_packed_operand_bytes if fmt == MXFP4 else L.fp4_nv_packed_operand_bytes)(N, K)
     if need == 0:
         raise ValueError("the packed layout needs N >= 1 and K a positive multiple of 512")
-    if bt_packed.numel() < need:
+    size = bt_packed.numel()
+    if size < need:
         raise ValueError("packed operand smaller than its shape")
-    _check_u8(bt_packed, bt_packed.numel(), "bt_packed", x.device)
-    M, code, s_g, out = _w4_output(fmt, x, K, N, global_scale, out_dtype, out)
+    packed = _bytes(bt_packed, size, "bt_packed", device)
+    s_g = None if fmt == MXFP4 else _scalar(global_scale, "global_scale", device)
+    out, out_code = _output(out, (*shape[:-1], N), x.dtype, x, out_dtype)
+    M = x.numel() // K
     if M > 0:
-        _on(x, (_lib or lib()).fp4_linear_w4_packed, fmt, x.data_ptr(), code, M, K,
-            bt_packed.data_ptr(), s_g, N, out.data_ptr(), _dtype_code(out.dtype))
+        _on(device, L.fp4_linear_w4_packed, fmt, x.data_ptr(), code, M, K, packed, s_g, N,
+            out.data_ptr(), out_code)
     return out
 
 
 def _workspace(workspace, need: int, device):
     """A scratch buffer of at least `need` bytes (its address and size)."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the same device")
     return workspace, workspace.data_ptr(), workspace.nbytes
@@ -765,65 +794,63 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int, renormalize: bo
     router [experts, hidden] (fp32 or bf16 each), softmax over the chosen experts
     (renormalize) or over all.  Returns (experts int32, weights fp32), each
     [tokens, top_k], descending; of equal logits the lower id comes first."""
-    if x.dim() != 2 or router.dim() != 2 or x.shape[1] != router.shape[1]:
+    shape, kept = x.shape, router.shape
+    if len(shape) != 2 or len(kept) != 2 or shape[1] != kept[1]:
         raise ValueError("x must be [tokens, hidden], router [experts, hidden]")
-    if not x.is_cuda:
-        raise TypeError("expected device tensors")
-    device = x.device
-    if router.device != device or not x.is_contiguous() or not router.is_contiguous():
-        raise ValueError("x and router must be contiguous, on one device")
-    xt, rt = _dtype_code(x.dtype), _dtype_code(router.dtype)
-    (tokens, hidden), experts = x.shape, router.shape[0]
-    top_k = int(top_k)
+    device, xt = _dense(x)
+    other, rt = _dense(router)
+    if other != device:
+        raise ValueError("x and router must be on one device")
+    (tokens, hidden), experts, top_k = shape, kept[0], int(top_k)
     if out is None:
         if not 1 <= top_k <= experts:
             raise ValueError("top_k must be from 1 to the number of experts")
-        chosen = torch.empty(tokens, top_k, dtype=torch.int32, device=device)
-        weights = torch.empty(tokens, top_k, dtype=torch.float32, device=device)
+        chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
+        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
     else:
         chosen, weights = out
         for t, dtype in ((chosen, torch.int32), (weights, torch.float32)):
-            if (t.shape != (tokens, top_k) or t.dtype != dtype or t.device != device
+            if (t.shape != (tokens, top_k) or t.dtype is not dtype or t.get_device() != device
                     or not t.is_contiguous()):
                 raise ValueError("out must be contiguous int32 and float32 [tokens, top_k]")
     if tokens == 0:
         return chosen, weights
     L = _lib or lib()
     need = L.fp4_moe_route_workspace_bytes(tokens, hidden, experts)
-    workspace, space, size = _workspace(workspace, need, device)
-    _on(x, L.fp4_moe_route, x.data_ptr(), xt, tokens, hidden, router.data_ptr(), rt, experts,
+    workspace, space, size = _workspace(workspace, need, x.device)
+    _on(device, L.fp4_moe_route, x.data_ptr(), xt, tokens, hidden, router.data_ptr(), rt, experts,
         top_k, 1 if renormalize else 0, chosen.data_ptr(), weights.data_ptr(), space, size)
     return chosen, weights
 
 
-def _moe_weights(fmt, up, down, device) -> bytes:
-    (uc, us), (dc, ds) = up[:2], down[:2]
-    if uc.dim() != 3 or dc.dim() != 3:
+def _moe_weights(fmt, up, down, device: int) -> bytes:
+    """fp4_moe_weights of up and down as moe_experts takes them."""
+    uc, dc = up[0], down[0]
+    wide, back = uc.shape, dc.shape
+    if len(wide) != 3 or len(back) != 3:
         raise ValueError("codes must be [experts, 2 inner, hidden/2] and [experts, hidden, inner/2]")
-    experts, rows, hh = uc.shape
+    experts, rows, hh = wide
     inner, hidden = rows // 2, 2 * hh
-    if rows % 2 or dc.shape != (experts, hidden, inner // 2) or inner % 2:
+    if rows % 2 or inner % 2 or back != (experts, hidden, inner // 2):
         raise ValueError("codes must be [experts, 2 inner, hidden/2] and [experts, hidden, inner/2]")
     block = 32 if fmt == MXFP4 else 16
-    _check_u8(uc, uc.numel(), "up codes", device)
-    _check_u8(dc, dc.numel(), "down codes", device)
-    _check_u8(us, experts * rows * (hidden // block), "up scales", device)
-    _check_u8(ds, experts * hidden * (inner // block), "down scales", device)
-    ug = dg = None
-    stride = 0
+    uc = _bytes(uc, experts * rows * hh, "up codes", device)
+    dc = _bytes(dc, experts * rows * hh // 2, "down codes", device)
+    us = _bytes(up[1], experts * rows * (hidden // block), "up scales", device)
+    ds = _bytes(down[1], experts * hidden * (inner // block), "down scales", device)
+    ug = dg = stride = 0
     if fmt == NVFP4:
         if len(up) < 3 or len(down) < 3:
             raise ValueError("NVFP4 weights need their tensor scales")
         ug, dg = up[2], down[2]
-        _check_global_scale(ug, "up's tensor scale", device)
-        _check_global_scale(dg, "down's tensor scale", device)
-        if ug.numel() != dg.numel() or ug.numel() not in (1, experts) or not (
+        ug_at, dg_at = (_scalar(t, "a tensor scale", device) for t in (ug, dg))
+        n = ug.numel()
+        if n != dg.numel() or n not in (1, experts) or not (
                 ug.is_contiguous() and dg.is_contiguous()):
             raise ValueError("tensor scales are one for all experts or one each, for up and down")
-        stride = 1 if ug.numel() > 1 else 0
-        ug, dg = ug.data_ptr(), dg.data_ptr()
-    return _pack_moe_weights(uc.data_ptr(), us.data_ptr(), dc.data_ptr(), ds.data_ptr(), ug or 0,
-                             dg or 0, hidden, inner, experts, stride)
+        stride = 1 if n > 1 else 0
+        ug, dg = ug_at, dg_at
+    return _pack_moe_weights(uc, us, dc, ds, ug, dg, hidden, inner, experts, stride)
 
 
 def moe_experts(fmt: int, x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor, up, down,
@@ -837,36 +864,28 @@ def moe_experts(fmt: int, x: torch.Tensor, experts: torch.Tensor, weights: torch
     Returns [tokens, hidden] of x's dtype, or of out_dtype."""
     if fmt != MXFP4 and fmt != NVFP4:
         raise ValueError("fmt must be MXFP4 or NVFP4")
-    if x.dim() != 2 or experts.dim() != 2 or weights.shape != experts.shape:
+    shape, chosen = x.shape, experts.shape
+    if len(shape) != 2 or len(chosen) != 2 or weights.shape != chosen or chosen[0] != shape[0]:
         raise ValueError("x must be [tokens, hidden], experts and weights [tokens, top_k]")
-    if not x.is_cuda:
-        raise TypeError("expected device tensors")
     if experts.dtype is not torch.int32 or weights.dtype is not torch.float32:
         raise TypeError("experts must be int32, weights float32")
-    device = x.device
-    if experts.device != device or weights.device != device or not (
-            x.is_contiguous() and experts.is_contiguous() and weights.is_contiguous()):
-        raise ValueError("x, experts and weights must be contiguous, on one device")
-    tokens, hidden = x.shape
-    top_k = experts.shape[1]
-    if experts.shape[0] != tokens or down[0].dim() != 3 or down[0].shape[1] != hidden:
-        raise ValueError("experts and weights need x's tokens, the weights x's hidden size")
+    device, code = _dense(x)
+    if not (experts.get_device() == weights.get_device() == device
+            and experts.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("experts and weights must be contiguous, on x's device")
+    tokens, hidden = shape
+    if down[0].dim() != 3 or down[0].shape[1] != hidden:
+        raise ValueError("the weights must have x's hidden size")
     w = _moe_weights(fmt, up, down, device)
-    code = _dtype_code(x.dtype)
-    if out is None:
-        out = torch.empty(tokens, hidden, dtype=out_dtype or x.dtype, device=device)
-    elif (out.shape != x.shape or out.device != device or not out.is_contiguous()
-          or (out_dtype is not None and out.dtype != out_dtype)):
-        raise ValueError("out must be a contiguous tensor of x's shape, of out_dtype")
-    ot = _dtype_code(out.dtype)
-    status = _check_status(status, check, device)
+    out, ot = _output(out, shape, x.dtype, x, out_dtype)
+    status = _check_status(status, check, x.device)
     if tokens == 0:
         return out
     L = _lib or lib()
-    need = L.fp4_moe_experts_workspace_bytes(w, fmt, tokens, top_k, code)
-    workspace, space, size = _workspace(workspace, need, device)
-    _on(x, L.fp4_moe_experts, fmt, w, x.data_ptr(), code, tokens, experts.data_ptr(),
-        weights.data_ptr(), top_k, out.data_ptr(), ot, space, size,
+    need = L.fp4_moe_experts_workspace_bytes(w, fmt, tokens, chosen[1], code)
+    workspace, space, size = _workspace(workspace, need, x.device)
+    _on(device, L.fp4_moe_experts, fmt, w, x.data_ptr(), code, tokens, experts.data_ptr(),
+        weights.data_ptr(), chosen[1], out.data_ptr(), ot, space, size,
         None if status is None else status.data_ptr())
     if check:
         _raise_flags(int(status.item()))
@@ -1012,11 +1031,11 @@ def _kv_call(fn, cache, batch, args, check, status):
         _raise_flags(int(status.item()))
 
 
-def _head_rows(x, y, weight, dim, what):
-    """fp4_head_rows of rows x [tokens, heads, dim] and their output."""
-    if len(x.shape) != 3 or x.shape[2] != dim or y.shape != x.shape:
-        raise ValueError(f"{what} and its output must be [tokens, heads, {dim}]")
-    tokens, heads, _ = x.shape
+def _head_rows(x, y, weight, device, dtype, shape, what):
+    """fp4_head_rows of rows x and their output, [tokens, heads, head_dim]."""
+    if y.shape != shape or y.dtype is not dtype or y.get_device() != device:
+        raise ValueError(f"{what}'s output must have its shape and dtype, on its device")
+    tokens, heads, dim = shape
     xt, xh, xi = x.stride()
     yt, yh, yi = y.stride()
     if xi != 1 or yi != 1:
@@ -1025,8 +1044,13 @@ def _head_rows(x, y, weight, dim, what):
         xt = yt = 0
     if heads < 2:
         xh = yh = dim
-    return _pack_head_rows(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh,
-                           0 if weight is None else weight.data_ptr(), heads)
+    if weight is None:
+        at = 0
+    elif weight.shape != (dim,) or weight.get_device() != device or not weight.is_contiguous():
+        raise ValueError("weights must be dense [head_dim] tensors on q's device")
+    else:
+        at = weight.data_ptr()
+    return _pack_head_rows(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, at, heads)
 
 
 def norm_rotate(q: torch.Tensor, k: torch.Tensor, cu_tokens: torch.Tensor, lengths: torch.Tensor,
@@ -1039,42 +1063,46 @@ def norm_rotate(q: torch.Tensor, k: torch.Tensor, cu_tokens: torch.Tensor, lengt
     lengths [n] (int32) are the batch's; frequencies float64 [rotary / 2], radians
     per position.  Returns (q, k), new dense tensors or `out` (out=(q, k): in
     place)."""
-    device, dtype = q.device, q.dtype
+    dtype, q_shape, k_shape = q.dtype, q.shape, k.shape
     code = _DTYPES.get(dtype)
     if code is None:
         code = _dtype_code(dtype)
-    if not q.is_cuda:
+    device = q.get_device()
+    if device < 0:
         raise TypeError("expected device tensors")
-    if k.dtype is not dtype or len(q.shape) != 3 or len(k.shape) != 3:
-        raise ValueError("q and k must be [tokens, heads, head_dim] of one dtype")
+    if (len(q_shape) != 3 or len(k_shape) != 3 or k.dtype is not dtype
+            or k_shape[0] != q_shape[0] or k_shape[2] != q_shape[2]):
+        raise ValueError("q and k must be [tokens, heads, head_dim], of one dtype")
     if cu_tokens.dtype is not torch.int32 or lengths.dtype is not torch.int32:
         raise TypeError("cu_tokens and lengths must be int32 tensors")
     if frequencies.dtype is not torch.float64:
         raise TypeError("frequencies must be a float64 tensor")
-    tokens, _, dim = q.shape
-    seqs = lengths.shape[0] if lengths.dim() == 1 else -1
-    if cu_tokens.shape != (seqs + 1,) or frequencies.dim() != 1 or k.shape[0] != tokens:
-        raise ValueError("lengths has n entries, cu_tokens n + 1; q and k have the same tokens")
-    out_q, out_k = (torch.empty(q.shape, dtype=dtype, device=device),
-                    torch.empty(k.shape, dtype=dtype, device=device)) if out is None else out
-    if out_q.dtype is not dtype or out_k.dtype is not dtype:
-        raise ValueError("out must have q's dtype")
+    if lengths.dim() != 1 or frequencies.dim() != 1:
+        raise ValueError("lengths and frequencies have one dimension")
+    seqs, half = lengths.shape[0], frequencies.shape[0]
+    if cu_tokens.shape != (seqs + 1,):
+        raise ValueError("for n lengths, cu_tokens has n + 1 entries")
+    if not (k.get_device() == cu_tokens.get_device() == lengths.get_device()
+            == frequencies.get_device() == device and cu_tokens.is_contiguous()
+            and lengths.is_contiguous() and frequencies.is_contiguous()):
+        raise ValueError("all tensors must be on q's device; cu_tokens, lengths and frequencies dense")
     weight = F32
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    for w in given:
-        if w.shape != (dim,) or w.dtype is not given[0].dtype:
-            raise ValueError("weights must be [head_dim], of one dtype")
-        weight = _dtype_code(w.dtype)
-    for t in (k, cu_tokens, lengths, frequencies, out_q, out_k, *given):
-        if t.device != device:
-            raise ValueError("all tensors must be on q's device")
-    if not all(t.is_contiguous() for t in (cu_tokens, lengths, frequencies, *given)):
-        raise ValueError("cu_tokens, lengths, frequencies and weights must be dense")
-    status = _check_status(status, check, device)
-    _on(q, (_lib or lib()).fp4_norm_rotate, _head_rows(q, out_q, q_weight, dim, "q"),
-        _head_rows(k, out_k, k_weight, dim, "k"), code, weight, dim, eps, cu_tokens.data_ptr(),
-        lengths.data_ptr(), seqs, tokens, frequencies.data_ptr(), 2 * frequencies.shape[0],
-        1 if interleaved else 0, None if status is None else status.data_ptr())
+    if q_weight is not None or k_weight is not None:
+        kind = (k_weight if q_weight is None else q_weight).dtype
+        if q_weight is not None and k_weight is not None and k_weight.dtype is not kind:
+            raise ValueError("weights must be of one dtype")
+        weight = _dtype_code(kind)
+    if out is None:
+        out_q = torch.empty(q_shape, dtype=dtype, device=q.device)
+        out_k = torch.empty(k_shape, dtype=dtype, device=q.device)
+    else:
+        out_q, out_k = out
+    status = _check_status(status, check, q.device)
+    _on(device, (_lib or lib()).fp4_norm_rotate,
+        _head_rows(q, out_q, q_weight, device, dtype, q_shape, "q"),
+        _head_rows(k, out_k, k_weight, device, dtype, k_shape, "k"), code, weight, q_shape[2], eps,
+        cu_tokens.data_ptr(), lengths.data_ptr(), seqs, q_shape[0], frequencies.data_ptr(),
+        2 * half, 1 if interleaved else 0, None if status is None else status.data_ptr())
     if check:
         _raise_flags(int(status.item()))
     return out_q, out_k

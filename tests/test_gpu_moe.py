@@ -239,7 +239,7 @@ def test_captured_with_given_buffers():
     ids = torch.zeros(tokens, 3, dtype=torch.int32, device="cuda")
     weights = torch.rand(tokens, 3, device="cuda")
     need = fp4.lib().fp4_moe_experts_workspace_bytes(
-        fp4._moe_weights(fp4.MXFP4, u, d, x.device), fp4.MXFP4, tokens, 3, fp4.F32)
+        fp4._moe_weights(fp4.MXFP4, u, d, 0), fp4.MXFP4, tokens, 3, fp4.F32)
     space = torch.empty(need, dtype=torch.uint8, device="cuda")
     out = torch.empty_like(x)
     how = dict(out=out, workspace=space, check=False)
