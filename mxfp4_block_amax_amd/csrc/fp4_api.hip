@@ -578,7 +578,7 @@ size_t fp4_moe_experts_workspace_bytes(const fp4_moe_weights *w, fp4_format fmt,
                                        int32_t top_k, fp4_dtype xt) {
     if (!w || (fmt != FP4_MXFP4 && fmt != FP4_NVFP4) || !valid_dtype(xt)) return 0;
     if (!moe_fits(w, fmt, tokens, top_k)) return 0;
-    return fp4dev::experts_workspace_bytes(tokens, top_k, w->inner, xt == FP4_BF16);
+    return fp4dev::experts_workspace_bytes(tokens, top_k, w->hidden, w->inner, xt == FP4_BF16);
 }
 
 fp4_status fp4_moe_experts(fp4_format fmt, const fp4_moe_weights *w, const void *x, fp4_dtype xt,

@@ -124,7 +124,8 @@ hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidd
                         const void *router, bool router_bf16, int experts, int top_k,
                         bool renormalize, int32_t *chosen, float *weights, void *workspace,
                         hipStream_t s);
-size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t inner, bool x_bf16);
+size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner,
+                               bool x_bf16);
 hipError_t launch_experts(int fmt, const MoeWeights &W, const void *x, bool x_bf16, int64_t tokens,
                           const int32_t *ids, const float *weights, int top_k, void *out,
                           bool out_bf16, void *workspace, int32_t *status, hipStream_t s);

@@ -166,7 +166,8 @@ struct MoeArgs {
     const int32_t *ids;
     const float *weights;
     MoeWeights W;
-    uint16_t *act;  // [tokens, top_k][terms][inner] bf16
+    uint16_t *act;   // [tokens, top_k][terms][inner] bf16
+    float *partial;  // [splits][tokens][hidden], of a down product in splits
     void *out;
     int64_t tokens;
     int32_t top_k, slots;
@@ -244,6 +245,7 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
     __shared__ uint16_t lists[UP_WAVES][MOE_BLOCK];
     __shared__ int count;
     const int lane = threadIdx.x & (WAVE - 1);
+    // (waves as a constant: loops unrolled, and 16 tokens of 128 experts 195 us, not 169)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), waves = blockDim.x / WAVE;
     const int r = lane & 15, g = lane >> 4;
     const int64_t token0 = (int64_t)blockIdx.z * MOE_BLOCK;
@@ -374,8 +376,18 @@ struct MoePlan {
           pair((uint16_t *)(used + experts)) {}
 };
 
-constexpr int DOWN_WAVES = 16;
-static_assert(DOWN_WAVES * WAVE >= MOE_EXPERTS, "a thread an expert");
+// Tokens of an item, a pass over an expert's weights: 4, or 8 where a block's tokens go to
+// an expert 4 times on average (64 tokens of 8 experts, top 2, through 2048 x 2816: 123 and
+// 98 us; of 64, top 6, 1408 in NVFP4: 237 and 203; but 32 of 128, top 8, 768: 119 and 140).
+// 16 win another tenth from 16 times on, and lose as much at 6.
+constexpr bool dense(int pairs, int experts) { return pairs >= 4 * experts; }
+
+// Waves of a workgroup of moe_down_kernel: 16, or 8 where more tokens take the LDS of two.
+// The plan has a thread for each expert.
+template <int TOKENS>
+constexpr int DOWN_WAVES = TOKENS > 4 ? 8 : 16;
+static_assert(DOWN_WAVES<4> * WAVE >= MOE_EXPERTS);
+static_assert(!dense(MOE_BLOCK * MOE_TOP_K, DOWN_WAVES<8> * WAVE + 1));
 
 // The plan of up to 64 pairs, by one wave, experts in the order they are named first:
 // no barriers but the one after it (the other way took a third of the kernel's time for
@@ -421,7 +433,7 @@ __device__ int make_small_plan(const MoePlan &plan, const int32_t *ids, const fl
 template <int TOKENS>
 __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *weights, int pairs,
                          int top_k, int experts) {
-    __shared__ uint32_t wave_sum[DOWN_WAVES];
+    __shared__ uint32_t wave_sum[DOWN_WAVES<TOKENS>];
     const int lane = threadIdx.x & (WAVE - 1), wave = threadIdx.x / WAVE, me = threadIdx.x;
     if (me < experts) plan.used[me] = 0;
     __syncthreads();
@@ -430,7 +442,7 @@ __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *w
             if (ids[q] == e) return false;
         return e >= 0 && e < experts;
     };
-    for (int p = me; p < pairs; p += DOWN_WAVES * WAVE) {
+    for (int p = me; p < pairs; p += DOWN_WAVES<TOKENS> * WAVE) {
         const int e = ids[p];
         if (first_of(p, e)) atomicAdd(&plan.used[e], 1u);
     }
@@ -447,7 +459,7 @@ __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *w
     before -= own;
     __syncthreads();
     uint32_t all = 0;
-    for (int w = 0; w < DOWN_WAVES; ++w) {
+    for (int w = 0; w < DOWN_WAVES<TOKENS>; ++w) {
         if (w < wave) before += wave_sum[w];
         all += wave_sum[w];
     }
@@ -459,7 +471,7 @@ __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *w
                                     (uint16_t)min(n - i * TOKENS, (uint32_t)TOKENS), 0};
     }
     __syncthreads();
-    for (int p = me; p < pairs; p += DOWN_WAVES * WAVE) {
+    for (int p = me; p < pairs; p += DOWN_WAVES<TOKENS> * WAVE) {
         const int e = ids[p];
         if (first_of(p, e)) plan.pair[atomicAdd(&plan.used[e], 1u)] = (uint16_t)p;
     }
@@ -484,12 +496,12 @@ __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *w
     return __builtin_amdgcn_readfirstlane(all >> 16);
 }
 
-// Down and the weighted sum.  A workgroup has 16 rows and a block's tokens; its waves
-// go through the items' groups of K = inner in turn.  A wave adds each group's sums,
+// Down and the weighted sum.  A workgroup has 16 rows and a block's tokens; its waves,
+// or those of `splits` workgroups, go through the items' groups of K = inner in turn.  A wave adds each group's sums,
 // weighted, to its own of the tokens, in LDS: a token that an expert does not have takes
 // nothing of it, not a zero times its values.
 template <int FMT, bool X_F32, int TOKENS>
-__global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, int block_tokens) {
+__global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeArgs A, int block_tokens) {
     constexpr int NA = X_F32 ? 3 : 2, BLK = FMT == 0 ? 32 : 16;
     using X = XPart<false, TOKENS, NA>;
     using W = RowsAt<FMT, 1>;
@@ -502,11 +514,11 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, i
     const int pairs = block * A.top_k;
     const int K = (int)A.W.inner, hidden = (int)A.W.hidden, row0 = blockIdx.x * 16;
     f32x4_t *sums = (f32x4_t *)lds;  // [waves][tokens][4]: 16 rows
-    u32x4_t *mine = lds + DOWN_WAVES * block_tokens * 4 + wave * (X::PIECES + W::LDS);
-    const MoePlan plan(lds + DOWN_WAVES * (block_tokens * 4 + X::PIECES + W::LDS),
+    u32x4_t *mine = lds + DOWN_WAVES<TOKENS> * block_tokens * 4 + wave * (X::PIECES + W::LDS);
+    const MoePlan plan(lds + DOWN_WAVES<TOKENS> * (block_tokens * 4 + X::PIECES + W::LDS),
                        block_tokens * A.top_k, A.W.experts);
 
-    for (int i = threadIdx.x; i < DOWN_WAVES * block_tokens * 4; i += DOWN_WAVES * WAVE)
+    for (int i = threadIdx.x; i < DOWN_WAVES<TOKENS> * block_tokens * 4; i += DOWN_WAVES<TOKENS> * WAVE)
         sums[i] = {0, 0, 0, 0};
     const int32_t *ids = A.ids + token0 * A.top_k;
     const float *weights = A.weights + token0 * A.top_k;
@@ -526,6 +538,8 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, i
     const uint16_t *act0 = A.act + token0 * A.top_k * NA * K;
     const Rsrc act = span(act0, pairs * NA * K * 2);
     const int per = K / W4_GROUP;
+    const int splits = gridDim.z, step = splits * DOWN_WAVES<TOKENS>;
+    const int turn = blockIdx.z * DOWN_WAVES<TOKENS> + wave;
     f32x4_t acc[1][1] = {};
     uint32_t top[1] = {0};
     // the sums of an item's products so far go to its tokens
@@ -560,11 +574,10 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, i
             }
             return a;
         },
-        act, mine, wave, DOWN_WAVES, items * per, acc, top, [&](int n) { add(item_of(n / per)); });
+        act, mine, turn, step, items * per, acc, top, [&](int n) { add(item_of(n / per)); });
     // and stretches past the last whole group, by the waves that have fewer groups
     const int rest = (K - per * W4_GROUP + W4_STRETCH - 1) / W4_STRETCH;
-    for (int n = (wave - items * per % DOWN_WAVES + DOWN_WAVES) % DOWN_WAVES; n < items * rest;
-         n += DOWN_WAVES) {
+    for (int n = (turn - items * per % step + step) % step; n < items * rest; n += step) {
         const MoeItem it = item_of(n / rest);
         const int64_t row = (int64_t)it.expert * hidden + row0;
         multiply_tail<FMT, NA>(
@@ -583,10 +596,14 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, i
         add(it);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < block * 4; i += DOWN_WAVES * WAVE) {
+    for (int i = threadIdx.x; i < block * 4; i += DOWN_WAVES<TOKENS> * WAVE) {
         f32x4_t s = sums[i];
-        for (int w = 1; w < DOWN_WAVES; ++w) s += sums[w * block_tokens * 4 + i];
+        for (int w = 1; w < DOWN_WAVES<TOKENS>; ++w) s += sums[w * block_tokens * 4 + i];
         const int64_t at = (token0 + i / 4) * hidden + row0 + 4 * (i & 3);
+        if (splits > 1) {
+            *(f32x4_t *)(A.partial + blockIdx.z * A.tokens * hidden + at) = s;
+            continue;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (A.out_bf16) ((__bf16 *)A.out)[at + j] = (__bf16)s[j];
@@ -595,36 +612,68 @@ __global__ __launch_bounds__(DOWN_WAVES *WAVE) void moe_down_kernel(MoeArgs A, i
     }
 }
 
+// The splits' sums, in their order.
+__global__ __launch_bounds__(256) void moe_join_kernel(const f32x4_t *partial, int splits, int64_t n,
+                                                       void *out, bool out_bf16) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    f32x4_t s = partial[i];
+    for (int z = 1; z < splits; ++z) s += partial[z * n + i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (out_bf16) ((__bf16 *)out)[4 * i + j] = (__bf16)s[j];
+        else ((float *)out)[4 * i + j] = s[j];
+    }
+}
+
+// Workgroups that share the down product of 16 rows and a block's tokens: as many as there
+// are CUs for, where each still has some 32 groups of K to go through (64 tokens of 128
+// experts, 2048 x 768: 169 us in one, 137 in two; 32 of 64, 1408 in NVFP4: 152 and 122; but
+// 2 of 128: 28.0 and 28.8, the launch that joins them).
+int down_splits(int64_t tokens, int top_k, int64_t hidden, int64_t inner) {
+    const int64_t groups = hidden / 16 * ((tokens + MOE_BLOCK - 1) / MOE_BLOCK);
+    const int64_t pairs = (tokens < MOE_BLOCK ? tokens : MOE_BLOCK) * top_k;
+    const int64_t work = pairs * ((inner + W4_GROUP - 1) / W4_GROUP);
+    const int64_t splits = 256 / groups < work / 32 ? 256 / groups : work / 32;
+    return splits < 1 ? 1 : splits > 8 ? 8 : (int)splits;
+}
+
 template <int FMT, bool X_F32, int TOKENS>
 hipError_t launch_tile(MoeArgs A, int32_t *status, hipStream_t s) {
     const int block = (int)(A.tokens < MOE_BLOCK ? A.tokens : MOE_BLOCK);
     A.slots = (int64_t)block * A.top_k < A.W.experts;
     const uint32_t blocks = (uint32_t)((A.tokens + MOE_BLOCK - 1) / MOE_BLOCK);
-    {
-        const int groups = (int)(A.W.hidden / W4_GROUP), waves = groups <= 4 ? 4 : UP_WAVES;
-        const dim3 grid((uint32_t)(A.W.inner / 16),
-                        (uint32_t)(A.slots ? block * A.top_k : A.W.experts), blocks);
-        const size_t lds = waves * (XPart<X_F32, TOKENS>::PIECES + RowsAt<FMT, 2>::LDS) * 16;
-        moe_up_kernel<FMT, X_F32, TOKENS><<<grid, waves * WAVE, lds, s>>>(A, status);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+    const dim3 up_grid((uint32_t)(A.W.inner / 16),
+                       (uint32_t)(A.slots ? block * A.top_k : A.W.experts), blocks);
+    const size_t up_lds = UP_WAVES * (XPart<X_F32, TOKENS>::PIECES + RowsAt<FMT, 2>::LDS) * 16;
+    moe_up_kernel<FMT, X_F32, TOKENS><<<up_grid, UP_WAVES * WAVE, up_lds, s>>>(A, status);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     constexpr int NA = X_F32 ? 3 : 2;
     const auto down_lds = [&](int tokens) {
-        return (size_t)DOWN_WAVES *
+        return (size_t)DOWN_WAVES<TOKENS> *
                    (tokens * 4 + XPart<false, TOKENS, NA>::PIECES + RowsAt<FMT, 1>::LDS) * 16 +
                MoePlan::bytes(tokens * A.top_k, A.W.experts);
     };
     int down_block = block;  // fewer tokens where a plan of many pairs leaves no room for them
     while (down_block > 16 && down_lds(down_block) > LDS_BYTES) down_block = (down_block + 1) / 2;
-    const dim3 grid((uint32_t)(A.W.hidden / 16), (uint32_t)((A.tokens + down_block - 1) / down_block));
+    const int splits = down_splits(A.tokens, A.top_k, A.W.hidden, A.W.inner);
+    const dim3 grid((uint32_t)(A.W.hidden / 16), (uint32_t)((A.tokens + down_block - 1) / down_block),
+                    (uint32_t)splits);
     moe_down_kernel<FMT, X_F32, TOKENS>
-        <<<grid, DOWN_WAVES * WAVE, down_lds(down_block), s>>>(A, down_block);
+        <<<grid, DOWN_WAVES<TOKENS> * WAVE, down_lds(down_block), s>>>(A, down_block);
+    e = hipGetLastError();
+    if (e != hipSuccess || splits == 1) return e;
+    const int64_t n = A.tokens * A.W.hidden / 4;
+    moe_join_kernel<<<(uint32_t)((n + 255) / 256), 256, 0, s>>>((const f32x4_t *)A.partial, splits, n,
+                                                                 A.out, A.out_bf16);
     return hipGetLastError();
 }
 
 template <int FMT, bool X_F32>
 hipError_t launch_experts(const MoeArgs &A, int32_t *status, hipStream_t s) {
+    const int block = (int)(A.tokens < MOE_BLOCK ? A.tokens : MOE_BLOCK);
+    if (dense(block * A.top_k, A.W.experts)) return launch_tile<FMT, X_F32, 8>(A, status, s);
     return launch_tile<FMT, X_F32, 4>(A, status, s);
 }
 
@@ -689,14 +738,22 @@ hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidd
     return hipGetLastError();
 }
 
-size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t inner, bool x_bf16) {
+static size_t act_bytes(int64_t tokens, int top_k, int64_t inner, bool x_bf16) {
     return (size_t)tokens * top_k * (x_bf16 ? 2 : 3) * inner * sizeof(uint16_t);
+}
+
+size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner, bool x_bf16) {
+    const int splits = down_splits(tokens, top_k, hidden, inner);
+    return act_bytes(tokens, top_k, inner, x_bf16) +
+           (splits > 1 ? (size_t)splits * tokens * hidden * sizeof(float) : 0);
 }
 
 hipError_t launch_experts(int fmt, const MoeWeights &W, const void *x, bool x_bf16, int64_t tokens,
                           const int32_t *ids, const float *weights, int top_k, void *out,
                           bool out_bf16, void *workspace, int32_t *status, hipStream_t s) {
-    const MoeArgs A = {x, ids, weights, W, (uint16_t *)workspace, out, tokens, top_k, 0, out_bf16};
+    // rows of act are multiples of 32 bytes, so partial is aligned too
+    float *partial = (float *)((char *)workspace + act_bytes(tokens, top_k, W.inner, x_bf16));
+    const MoeArgs A = {x, ids, weights, W, (uint16_t *)workspace, partial, out, tokens, top_k, 0, out_bf16};
     if (fmt == 0)
         return x_bf16 ? launch_experts<0, false>(A, status, s) : launch_experts<0, true>(A, status, s);
     return x_bf16 ? launch_experts<1, false>(A, status, s) : launch_experts<1, true>(A, status, s);
