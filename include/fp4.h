@@ -519,9 +519,9 @@ fp4_status fp4_linear_mxfp4(const void *x, fp4_dtype xt, int64_t M, int64_t K,
  * Products are exact: a weight's value fits bf16 (MXFP4 for scale bytes up to
  * 252), fp32 activations count with all their bits.  Sums are fp32, their order
  * is fixed: deterministic.  A NaN scale byte makes its row's outputs NaN.  K is
- * a multiple of the block (32 or 16) up to 2^20, M up to 2^19.  The weight is read once
- * for every 64 tokens, which bounds the time: for long prompts the W4A4
- * layers are faster.  One launch.
+ * a multiple of the block (32 or 16) up to 2^20, M up to 2^19, N up to 2^26; c is
+ * apart from the inputs.  bf16 tokens share a reading of the weight by up to 64,
+ * fp32 ones by 16: for long prompts the W4A4 layers are faster.  One launch.
  */
 fp4_status fp4_linear_w4(fp4_format fmt, const void *x, fp4_dtype xt, int64_t M, int64_t K,
                          const uint8_t *bt_codes, const uint8_t *bt_scales,
@@ -550,7 +550,7 @@ fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int
  *   x          [tokens, hidden] fp32 or bf16     router [experts, hidden] fp32 or bf16
  *   chosen     [tokens, top_k] int32             weights [tokens, top_k] fp32
  *   workspace  fp4_moe_route_workspace_bytes(...) bytes, scratch
- * hidden is a multiple of 8; at most 1024 experts, 32 of a token, 2^20 tokens; x,
+ * hidden is a multiple of 8; at most 1024 experts, 32 of a token, 2^19 tokens; x,
  * router and workspace 16-byte aligned.  Sums are 64-bit, their order is fixed:
  * deterministic.  A NaN logit is below every other.  Two launches.
  */
@@ -565,7 +565,8 @@ fp4_status fp4_moe_route(const void *x, fp4_dtype xt, int64_t tokens, int64_t hi
  *   up    [experts, 2 inner, hidden]  rows 0 .. inner - 1 of an expert its gate,
  *         the others its up projection
  *   down  [experts, hidden, inner]
- * codes 16-byte aligned; hidden and inner multiples of the block.  NVFP4: tensor
+ * codes 16-byte aligned; hidden and inner multiples of the block, hidden up to
+ * 2^20, inner to 2^16, their product to 2^30; at most 1024 experts.  NVFP4: tensor
  * scales, one for all experts (global_scale_stride 0) or one each (1).
  */
 typedef struct {
@@ -588,9 +589,10 @@ typedef struct {
  *              (calls that share one must be stream-ordered)
  * Products are exact as in fp4_linear_w4, sums fp32 in a fixed order; the gated
  * values go to the second product as two bf16 terms (17 bits) for bf16 x, three
- * for fp32 x.  An expert's weights reach only the tokens that name it.  Those of
- * each expert that some token names are read once for every 64 tokens.  Two
- * launches.  Deterministic.
+ * for fp32 x.  An expert's weights reach only the tokens that name it, those of an
+ * expert that no token names are not read.  At most 2^19 tokens, 32 experts of a
+ * token; out is apart from the inputs.  Two launches, or three where rows are few and
+ * tokens many.  Deterministic.
  */
 size_t fp4_moe_experts_workspace_bytes(const fp4_moe_weights *w, fp4_format fmt, int64_t tokens,
                                        int32_t top_k, fp4_dtype xt);

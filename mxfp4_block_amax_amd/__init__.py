@@ -16,9 +16,17 @@ Functions mirror the C entry points:
     kv_cache_write(cache, k, v, cu_tokens, lengths, table)
     kv_cache_read(cache, cu_tokens, lengths, table, tokens) -> (k, v)
     kv_attention(q, cache, cu_tokens, lengths, table)       -> out
+    linear_w4(fmt, x, bt_codes, bt_scales, s_g)             -> out
+    linear_w4_packed(fmt, x, bt_packed, N, s_g)             -> out
+    moe_route(x, router, top_k)                             -> (experts, weights)
+    moe_experts(fmt, x, experts, weights, up, down)         -> out
+    norm_rotate(q, k, cu_tokens, lengths, frequencies)      -> (q, k)
 
-The last four are the 8-bit key/value cache (E4M3FN codes, one E8M0 byte per
-page and head); include/fp4.h states its layout and what a batch is.
+The kv_ ones are the 8-bit key/value cache (E4M3FN codes, one E8M0 byte per
+page and head); include/fp4.h states its layout and what a batch is.  The last
+five are the rest of a decoding step around it: linear layers and a mixture of
+experts with four-bit weights and activations as they are, and the norm and
+rotation of queries and keys.
 
 Inputs of the others are contiguous CUDA (HIP) tensors of dtype float32 or bfloat16 whose
 last dimension is a multiple of the block (32 for MXFP4, 16 for NVFP4).

@@ -81,8 +81,8 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 23;    // rows of a batch
 constexpr int64_t kMaxPositions = (int64_t)1 << 27;  // positions of a sequence's table
 constexpr int32_t kMaxSeqs = 1 << 20;
 constexpr int64_t kMaxInner = (int64_t)1 << 20;  // K of a four-bit weight's product
-constexpr int64_t kMaxRows = (int64_t)1 << 19;   // and its activation rows
-constexpr int64_t kMaxMoeTokens = (int64_t)1 << 20;
+constexpr int64_t kMaxRows = (int64_t)1 << 19;   // and its activation rows, a router's too
+constexpr int64_t kMaxOutputs = (int64_t)1 << 26;  // N: a launch has below 2^32 threads a dimension
 static_assert(FP4_FLAG_EXPERT_INDEX == fp4dev::FLAG_EXPERT_INDEX, "the header states the flag");
 static_assert(FP4_FLAG_CACHE_INDEX == fp4dev::FLAG_CACHE_INDEX, "the header states the flag");
 
@@ -506,7 +506,7 @@ static fp4_status linear_w4_args(fp4_format fmt, const void *x, fp4_dtype xt, in
     if (!valid_dtype(xt) || !valid_dtype(ct)) return FP4_E_DTYPE;
     if (!x || !c || (fmt == FP4_NVFP4 && !bt_global_scale)) return FP4_E_ARG;
     if (M < 1 || N < 1 || K < 1 || K % k_unit) return FP4_E_SHAPE;
-    if (M > kMaxRows || N > INT32_MAX / 2 || K > kMaxInner || N > kMaxElems / K) return FP4_E_SHAPE;
+    if (M > kMaxRows || N > kMaxOutputs || K > kMaxInner || N > kMaxElems / K) return FP4_E_SHAPE;
     if (!aligned(x, 16) || !aligned(c, ct == FP4_BF16 ? 2 : 4)) return FP4_E_ALIGN;
     if (fmt == FP4_NVFP4 && !aligned(bt_global_scale, 4)) return FP4_E_ALIGN;
     return FP4_OK;
@@ -540,7 +540,7 @@ fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int
 }
 
 size_t fp4_moe_route_workspace_bytes(int64_t tokens, int64_t hidden, int32_t experts) {
-    if (tokens < 1 || tokens > kMaxMoeTokens || hidden < 8 || hidden % 8 ||
+    if (tokens < 1 || tokens > kMaxRows || hidden < 8 || hidden % 8 ||
         hidden > INT32_MAX / 2 || experts < 1 || experts > fp4dev::MOE_EXPERTS)
         return 0;
     return fp4dev::route_workspace_bytes(tokens, hidden, experts);
@@ -567,7 +567,7 @@ fp4_status fp4_moe_route(const void *x, fp4_dtype xt, int64_t tokens, int64_t hi
 // Sizes that the experts' calls take.
 static bool moe_fits(const fp4_moe_weights *w, fp4_format fmt, int64_t tokens, int32_t top_k) {
     const int64_t block = fmt == FP4_MXFP4 ? 32 : 16;
-    if (tokens < 1 || tokens > kMaxMoeTokens || top_k < 1 || top_k > fp4dev::MOE_TOP_K) return false;
+    if (tokens < 1 || tokens > kMaxRows || top_k < 1 || top_k > fp4dev::MOE_TOP_K) return false;
     if (w->experts < 1 || w->experts > fp4dev::MOE_EXPERTS) return false;
     if (w->hidden < 1 || w->hidden % block || w->hidden > kMaxInner) return false;
     if (w->inner < 1 || w->inner % block || w->inner > kMaxInner / 16) return false;
