@@ -5,6 +5,8 @@
 //
 // s_g = 1 for MXFP4.  What it cannot do without is reading the weight once: a
 // token's 2 N K operations are far below the MFMA's rate up to some 64 tokens.
+#include <utility>
+
 #include "fp4_kernels.h"
 #include "fp4_w4.h"
 
@@ -30,9 +32,12 @@ constexpr int tile_waves() {
 }
 
 // Up to TOKENS (16 at most) tokens and 32 weight rows a workgroup: its waves take
-// groups of K in turn, and add their sums in LDS in the
-// order of the waves.  The loop is short: instructions that run once come from memory,
-// and a longer one took 4 us more for a call of 1 x 512 x 2048.
+// groups of K in turn, and add their sums in LDS in the order of the waves.  Two parts of
+// 16 rows a wave, so that a fragment of the activations serves two products; and with 32
+// rows 8192 of them fill the CUs.  The weight's bytes bound it: captured, with inputs from
+// memory, 1 x 8192 x 8192 packed takes 9.8 us (3.6 TB/s; 2 us are a node's start), 1 x 8192
+// x 28672 23.8 (5.3 TB/s), 16 x 8192 x 28672 in NVFP4 38.5 (3.4 TB/s, vector instructions
+// 44 % of the cycles), and 1 x 512 x 2048 3.9, a chain of load, decode and join.
 template <int FMT, bool X_F32, bool PACKED, int TOKENS, int WAVES>
 __global__ __launch_bounds__(WAVES *WAVE) void linear_w4_kernel(LinearArgs A) {
     using XT = std::conditional_t<X_F32, float, uint16_t>;
@@ -132,7 +137,9 @@ hipError_t launch_tile(const LinearArgs &A, hipStream_t s) {
 // (what it reads of the activations then serves as many products as the matrix units do
 // while LDS gives them), two waves side by side; four such pairs of waves take the groups
 // of K in turn.  A slab, a stretch of each of the four's groups, of the activations is in
-// LDS for all; the next one is on its way in registers.
+// LDS for all; the next one is on its way in registers.  Matrix, vector and LDS
+// instructions bound it, some 2000 of a stretch's 5900 cycles each: 64 x 28672 x 8192
+// packed 47 us, of which the weight's bytes are 26.
 constexpr int WIDE_PARTS = 4, WIDE_ROW_WAVES = 2, WIDE_K_WAVES = 4;
 constexpr int WIDE_ROWS = 16 * WIDE_PARTS * WIDE_ROW_WAVES;
 constexpr int WIDE_THREADS = WIDE_ROW_WAVES * WIDE_K_WAVES * WAVE;
@@ -284,17 +291,35 @@ hipError_t launch_wide(const LinearArgs &A, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tiles of tokens for 17 tokens and more, in 16 tokens each: of the wide kernel, or 0 for
+// the 16-token one.  A kernel's time is its rounds of a workgroup a CU; a round of K = 8192
+// takes some 10 us in the 16-token kernel, 20, 25 and 38 us with tiles of 1, 2 and 4 in the
+// wide one.  (Packed MXFP4, 0, 1, 2, 4: 64 x 2048 x 8192 9.9, 20, 24, 38 us; 32 x 8192 21,
+// 22, 26, 37; 64 x 8192 39, 22, 25, 39; 32 x 28672 65, 53, 33, 43; 64 x 28672 126, 103, 62,
+// 47; 128 x 8192 74, 41, 27, 39.)
+int wide_tiles(int64_t M, int64_t N) {
+    const int64_t tokens = (M + 15) / 16, row_tiles = (N + WIDE_ROWS - 1) / WIDE_ROWS;
+    const auto rounds = [](int64_t workgroups) { return (workgroups + 255) / 256; };
+    int best = 0;
+    int64_t least = 4 * rounds((N + LINEAR_ROWS - 1) / LINEAR_ROWS * tokens);
+    for (const auto &[tiles, cost] : {std::pair{1, 8}, {2, 10}, {4, 15}}) {
+        const int64_t time = cost * rounds(row_tiles * ((tokens + tiles - 1) / tiles));
+        if (time < least) least = time, best = tiles;
+    }
+    return best;
+}
+
+// Tokens of a tile: the smallest that holds them (packed MXFP4, 8192 x 8192, tiles of 4, 8
+// and 16: 4 tokens 9.8, 10.5, 10.8 us; 8 tokens 16.5, 10.9, 10.9, in fp32 23, 15, 19).
 template <int FMT, bool X_F32, bool PACKED>
 hipError_t launch_tokens(const LinearArgs &A, hipStream_t s) {
     if (A.M <= 4) return launch_tile<FMT, X_F32, PACKED, 4>(A, s);
     if (A.M <= 8) return launch_tile<FMT, X_F32, PACKED, 8>(A, s);
     if constexpr (!X_F32) {
-        // as many tokens a workgroup as still leave one for most CUs
-        const int64_t row_tiles = (A.N + WIDE_ROWS - 1) / WIDE_ROWS;
-        const int64_t tokens = (A.M + 15) / 16;
-        if (A.M > 32 && row_tiles * ((tokens + 3) / 4) > 128) return launch_wide<FMT, PACKED, 4>(A, s);
-        if (A.M > 16 && row_tiles * ((tokens + 1) / 2) > 64) return launch_wide<FMT, PACKED, 2>(A, s);
-        if (A.M > 16) return launch_wide<FMT, PACKED, 1>(A, s);
+        const int tiles = A.M > 16 ? wide_tiles(A.M, A.N) : 0;
+        if (tiles == 1) return launch_wide<FMT, PACKED, 1>(A, s);
+        if (tiles == 2) return launch_wide<FMT, PACKED, 2>(A, s);
+        if (tiles == 4) return launch_wide<FMT, PACKED, 4>(A, s);
     }
     return launch_tile<FMT, X_F32, PACKED, 16>(A, s);
 }
