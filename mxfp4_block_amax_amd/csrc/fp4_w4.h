@@ -170,9 +170,11 @@ __device__ __forceinline__ u32x4_t load16_streamed(Rsrc r, uint32_t at) {
 // stretches, 128 bytes of a row, and a group's scales at once.  Loads are laid out for
 // the memory: lanes next to each other have what is next to each other, a load has whole
 // lines, and a line is loaded by one wave.  (With lanes in the products' order, where
-// neighbours have different rows, 16 tokens through 8192 x 28672 in NVFP4 took 70 us;
-// with stretches of 64 bytes and scales a stretch at a time, lines that several waves
-// wait for, 50.)  What K has past its last whole group is load_tail's.
+// neighbours have different rows, 16 tokens through 8192 x 28672 in NVFP4 took 70 us, not
+// 39; with stretches of 64 bytes and scales a stretch at a time, lines that several waves
+// wait for, 50.)  What K has past its last whole group is load_tail's: groups cut by the
+// rows' end cost K of whole groups 2 to 25 %, and as an instantiation of their own gained
+// as often as they lost.
 constexpr int W4_GROUP = 4 * W4_STRETCH;
 
 // PARTS parts of 16 rows of row-major weights, codes [rows, K/2] and scales [rows,
