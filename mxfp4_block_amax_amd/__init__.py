@@ -716,10 +716,10 @@ def _dense(x: torch.Tensor):
     return device, code
 
 
-def _output(out, shape, dtype, x, out_dtype):
+def _output(out, shape, x, out_dtype):
     """The output tensor and its dtype's code."""
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or dtype, device=x.device)
+        out = x.new_empty(shape, dtype=out_dtype) if out_dtype else x.new_empty(shape)
     elif (out.shape != shape or out.get_device() != x.get_device() or not out.is_contiguous()
           or (out_dtype is not None and out.dtype is not out_dtype)):
         raise ValueError("out must be a contiguous tensor of the result's shape, of out_dtype")
@@ -742,7 +742,7 @@ def linear_w4(fmt: int, x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torc
     codes = _bytes(bt_codes, N * kh, "bt_codes", device)
     scales = _bytes(bt_scales, N * kh // (16 if fmt == MXFP4 else 8), "bt_scales", device)
     s_g = None if fmt == MXFP4 else _scalar(global_scale, "global_scale", device)
-    out, out_code = _output(out, (*shape[:-1], N), x.dtype, x, out_dtype)
+    out, out_code = _output(out, (*shape[:-1], N), x, out_dtype)
     M = x.numel() // (2 * kh) if kh else 0
     if M > 0:
         _on(device, (_lib or lib()).fp4_linear_w4, fmt, x.data_ptr(), code, M, 2 * kh, codes,
@@ -767,7 +767,7 @@ def linear_w4_packed(fmt: int, x: torch.Tensor, bt_packed: torch.Tensor, N: int,
         raise ValueError("packed operand smaller than its shape")
     packed = _bytes(bt_packed, size, "bt_packed", device)
     s_g = None if fmt == MXFP4 else _scalar(global_scale, "global_scale", device)
-    out, out_code = _output(out, (*shape[:-1], N), x.dtype, x, out_dtype)
+    out, out_code = _output(out, (*shape[:-1], N), x, out_dtype)
     M = x.numel() // K
     if M > 0:
         _on(device, L.fp4_linear_w4_packed, fmt, x.data_ptr(), code, M, K, packed, s_g, N,
@@ -813,8 +813,8 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, top_k: int, renormalize: bo
     if out is None:
         if not 1 <= top_k <= experts:
             raise ValueError("top_k must be from 1 to the number of experts")
-        chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=x.device)
-        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=x.device)
+        chosen = x.new_empty((tokens, top_k), dtype=torch.int32)
+        weights = x.new_empty((tokens, top_k), dtype=torch.float32)
     else:
         chosen, weights = out
         for t, dtype in ((chosen, torch.int32), (weights, torch.float32)):
@@ -885,7 +885,7 @@ def moe_experts(fmt: int, x: torch.Tensor, experts: torch.Tensor, weights: torch
     if down[0].dim() != 3 or down[0].shape[1] != hidden:
         raise ValueError("the weights must have x's hidden size")
     w = _moe_weights(fmt, up, down, device)
-    out, ot = _output(out, shape, x.dtype, x, out_dtype)
+    out, ot = _output(out, shape, x, out_dtype)
     status = _check_status(status, check, x.device)
     if tokens == 0:
         return out
@@ -1101,8 +1101,7 @@ def norm_rotate(q: torch.Tensor, k: torch.Tensor, cu_tokens: torch.Tensor, lengt
             raise ValueError("weights must be of one dtype")
         weight = _dtype_code(kind)
     if out is None:
-        out_q = torch.empty(q_shape, dtype=dtype, device=q.device)
-        out_k = torch.empty(k_shape, dtype=dtype, device=q.device)
+        out_q, out_k = q.new_empty(q_shape), q.new_empty(k_shape)
     else:
         out_q, out_k = out
     status = _check_status(status, check, q.device)
