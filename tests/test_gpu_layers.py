@@ -203,6 +203,66 @@ def test_many_experts_a_token(tokens, experts, top_k, dtype):
     check_experts(_w4.MX, x, ids, weights, up, down)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt,tokens,hidden,inner,experts,top_k", [
+    (_w4.MX, 8, 64, 96, 2, 2), (_w4.NV, 30, 96, 544, 2, 2), (_w4.MX, 64, 32, 2048, 16, 2),
+    (_w4.NV, 21, 48, 1040, 4, 3), (_w4.MX, 64, 4096, 512, 3, 1), (_w4.NV, 100, 256, 512, 32, 4),
+    (_w4.MX, 4, 64, 8192, 2, 1)])
+def test_shared_passes(fmt, tokens, hidden, inner, experts, top_k, dtype):
+    """Experts with many tokens each, and rows so few that workgroups share them."""
+    announce(f"moe_experts {fmt} {tokens} {hidden} {inner} {experts} {top_k} {dtype}")
+    g = np.random.default_rng(inner + tokens)
+    up, down = weights_of(fmt, experts, hidden, inner, g)
+    ids = np.argsort(g.random((tokens, experts)), axis=1)[:, :top_k]
+    ids[0] = -1
+    weights = g.random((tokens, top_k)).astype(np.float32)
+    x = torch.from_numpy(g.standard_normal((tokens, hidden))).to(dtype)
+    check_experts(fmt, x, ids, weights, up, down)
+
+
+def test_shared_passes_captured():
+    g = np.random.default_rng(9)
+    up, down = weights_of(_w4.MX, 4, 128, 1024, g)
+    u, d = up.device()[:2], down.device()[:2]
+    x = torch.randn(40, 128, device="cuda").bfloat16()
+    ids = torch.randint(-1, 4, (40, 2), dtype=torch.int32, device="cuda")
+    weights = torch.rand(40, 2, device="cuda")
+    out = torch.empty(40, 128, device="cuda")
+
+    def step():
+        return fp4.moe_experts(fp4.MXFP4, x, ids, weights, u, d, out=out, check=False)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        x.normal_()
+        ids.random_(-1, 4)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, fp4.moe_experts(fp4.MXFP4, x, ids, weights, u, d,
+                                                out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("fmt,m,n,k", [
+    (_w4.MX, 17, 31, 96), (_w4.NV, 64, 8192, 80), (_w4.MX, 33, 28700, 544), (_w4.NV, 130, 4097, 528),
+    (_w4.MX, 64, 28672, 1024), (_w4.MX, 500, 1000, 224)])
+def test_every_tile_of_many_tokens(fmt, m, n, k):
+    """Whole-number activations: sums are exact, so every tile's is the same."""
+    announce(f"linear_w4 {fmt} {m} x {n} x {k}")
+    g = np.random.default_rng(n)
+    w = _w4.exact_weight(fmt, (n, k), g)
+    x = g.integers(-8, 9, (m, k)).astype(np.float32)
+    want = torch.from_numpy(x.astype(np.float64) @ w.values().T * w.factor()).float()
+    codes, scales, s_g = w.device()
+    for dtype in (torch.bfloat16, torch.float32):
+        xd = torch.from_numpy(x).to(dtype).cuda()
+        got = fp4.linear_w4(fmt, xd, codes, scales, s_g, out_dtype=torch.float32)
+        assert torch.equal(got.cpu(), want)
+
+
 # ---- past 32 bits ---------------------------------------------------------------
 def random_bytes(*shape):
     return torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda")
