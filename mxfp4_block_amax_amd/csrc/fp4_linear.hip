@@ -5,7 +5,7 @@
 //
 // s_g = 1 for MXFP4.  What it cannot do without is reading the weight once: a
 // token's 2 N K operations are far below the MFMA's rate up to some 64 tokens.
-#include <utility>
+#include <initializer_list>
 
 #include "fp4_kernels.h"
 #include "fp4_w4.h"
@@ -133,33 +133,33 @@ hipError_t launch_tile(const LinearArgs &A, hipStream_t s) {
     return hipGetLastError();
 }
 
-// More tokens, bf16: 16 TILES of them and 128 weight rows a workgroup.  A wave has 64 rows
-// (what it reads of the activations then serves as many products as the matrix units do
-// while LDS gives them), two waves side by side; four such pairs of waves take the groups
-// of K in turn.  A slab, a stretch of each of the four's groups, of the activations is in
-// LDS for all; the next one is on its way in registers.  Matrix, vector and LDS
-// instructions bound it, some 2000 of a stretch's 5900 cycles each: 64 x 28672 x 8192
-// packed 47 us, of which the weight's bytes are 26.
-constexpr int WIDE_PARTS = 4, WIDE_ROW_WAVES = 2, WIDE_K_WAVES = 4;
-constexpr int WIDE_ROWS = 16 * WIDE_PARTS * WIDE_ROW_WAVES;
-constexpr int WIDE_THREADS = WIDE_ROW_WAVES * WIDE_K_WAVES * WAVE;
+// More tokens, bf16: 16 TILES of them and 64 ROW_WAVES weight rows a workgroup.  A wave
+// has 64 rows (what it reads of the activations then serves as many products as the matrix
+// units do while LDS gives them); ROW_WAVES waves side by side take a group of K, the
+// others of the eight the next ones.  A slab, a stretch of each of these groups, of the
+// activations is in LDS for all; the next one is on its way in registers.  Matrix, vector
+// and LDS instructions bound it, with tiles of 4 some 2000 of a stretch's 5900 cycles each:
+// 64 x 28672 x 8192 packed 47 us, of which the weight's bytes are 26.
+constexpr int WIDE_PARTS = 4, WIDE_WAVES = 8;
+constexpr int WIDE_THREADS = WIDE_WAVES * WAVE;
 
-template <int FMT, bool PACKED, int TILES>
+template <int FMT, bool PACKED, int TILES, int ROW_WAVES>
 __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearArgs A) {
     constexpr int BLK = FMT == 0 ? 32 : 16, PARTS = WIDE_PARTS;
-    constexpr int SLAB = WIDE_K_WAVES * TILES * 256;  // pieces: [K wave][tile][v][row ^ v]
+    constexpr int K_WAVES = WIDE_WAVES / ROW_WAVES, ROWS = 16 * PARTS * ROW_WAVES;
+    constexpr int SLAB = K_WAVES * TILES * 256;  // pieces: [K wave][tile][v][row ^ v]
     constexpr int LOADS = SLAB / WIDE_THREADS;
     using W = std::conditional_t<PACKED, PackedAt<FMT, PARTS>, RowsAt<FMT, PARTS>>;
     extern __shared__ u32x4_t lds[];  // [2][SLAB], then the waves' own
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int k_wave = wave % WIDE_K_WAVES, row_wave = wave / WIDE_K_WAVES;
+    const int k_wave = wave % K_WAVES, row_wave = wave / K_WAVES;
     const int r = lane & 15, g = lane >> 4, part = PACKED ? packed_group(g) : g;
     const int m0 = blockIdx.y * (16 * TILES), K = A.K;
-    const int row0 = blockIdx.x * WIDE_ROWS + 16 * PARTS * row_wave;
+    const int row0 = blockIdx.x * ROWS + 16 * PARTS * row_wave;
     const int tokens = min(16 * TILES, A.M - m0);
     const int groups = (uint32_t)K / W4_GROUP;
-    const int slabs = (groups + WIDE_K_WAVES - 1) / WIDE_K_WAVES * 4;  // four stretches a group
+    const int slabs = (groups + K_WAVES - 1) / K_WAVES * 4;  // four stretches a group
 
     // a wave past the last row has the last ones' weights, for sums that are not stored
     const int first = min(row0, (A.N - 1) / 32 * 32);
@@ -178,17 +178,17 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
     const auto load_slab = [&](int s) {
 #pragma unroll
         for (int n = 0; n < LOADS; ++n) {
-            const int e = n * WIDE_THREADS + threadIdx.x, v = e / 16 % WIDE_K_WAVES;
-            const uint32_t k = group_k(s / 4 * WIDE_K_WAVES + v);
-            xs[n] = load16(x, (uint32_t)(e / (16 * WIDE_K_WAVES) * K + 8 * (e & 15)) * 2 +
+            const int e = n * WIDE_THREADS + threadIdx.x, v = e / 16 % K_WAVES;
+            const uint32_t k = group_k(s / 4 * K_WAVES + v);
+            xs[n] = load16(x, (uint32_t)(e / (16 * K_WAVES) * K + 8 * (e & 15)) * 2 +
                                   (k == NOWHERE ? NOWHERE / 2 : (k + (s & 3) * W4_STRETCH) * 2));
         }
     };
     const auto store_slab = [&](u32x4_t *to) {
 #pragma unroll
         for (int n = 0; n < LOADS; ++n) {
-            const int e = n * WIDE_THREADS + threadIdx.x, piece = e & 15, v = e / 16 % WIDE_K_WAVES;
-            const int row = e / (16 * WIDE_K_WAVES);
+            const int e = n * WIDE_THREADS + threadIdx.x, piece = e & 15, v = e / 16 % K_WAVES;
+            const int row = e / (16 * K_WAVES);
             to[((v * TILES + row / 16) * 16 + piece) * 16 + ((row & 15) ^ piece)] = xs[n];
         }
     };
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
     f32x4_t acc[PARTS][TILES] = {};
     uint32_t top[PARTS] = {};
     for (int s = 0; s < slabs; s += 4) {
-        const uint32_t next = group_k(s / 4 * WIDE_K_WAVES + WIDE_K_WAVES + k_wave);
+        const uint32_t next = group_k(s / 4 * K_WAVES + K_WAVES + k_wave);
         const typename W::Scales here = scale;
         w.put(here);
         scale = w.load_scales(next);
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
     }
     if constexpr (!PACKED) {
         // the stretches past the last whole group, in turn
-        for (int q = groups * W4_GROUP + W4_STRETCH * k_wave; q < K; q += W4_STRETCH * WIDE_K_WAVES) {
+        for (int q = groups * W4_GROUP + W4_STRETCH * k_wave; q < K; q += W4_STRETCH * K_WAVES) {
             W4Unit u[PARTS];
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
@@ -252,8 +252,8 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
     if constexpr (FMT == 0) w4_nan_rows(top, acc);
     // the K waves' sums, one part after the other, added in their order
     f32x4_t *sums = (f32x4_t *)lds;  // [K wave][row wave][TILES][64]
-    constexpr int EACH = WIDE_ROW_WAVES * TILES * WAVE;
-    static_assert(WIDE_K_WAVES * EACH <= 2 * SLAB);
+    constexpr int EACH = ROW_WAVES * TILES * WAVE;
+    static_assert(K_WAVES * EACH <= 2 * SLAB);
     const float s_g = FMT == 0 ? 1.0f : *A.s_g;
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
@@ -265,10 +265,10 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
         for (int i = threadIdx.x; i < EACH; i += WIDE_THREADS) {
             f32x4_t y = sums[i];
 #pragma unroll
-            for (int v = 1; v < WIDE_K_WAVES; ++v) y += sums[v * EACH + i];
+            for (int v = 1; v < K_WAVES; ++v) y += sums[v * EACH + i];
             if constexpr (FMT == 1) y = y * s_g;
             const int l = i % WAVE, m = m0 + 16 * (i / WAVE % TILES) + (l & 15);
-            const int n = blockIdx.x * WIDE_ROWS + i / (TILES * WAVE) * 16 * PARTS + 16 * p + 4 * (l >> 4);
+            const int n = blockIdx.x * ROWS + i / (TILES * WAVE) * 16 * PARTS + 16 * p + 4 * (l >> 4);
             if (m >= A.M) continue;
             const int64_t to = (int64_t)m * A.N + n;
 #pragma unroll
@@ -281,30 +281,35 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void linear_w4_wide_kernel(LinearA
     }
 }
 
-template <int FMT, bool PACKED, int TILES>
+template <int FMT, bool PACKED, int TILES, int ROW_WAVES>
 hipError_t launch_wide(const LinearArgs &A, hipStream_t s) {
-    const size_t lds = 2 * WIDE_K_WAVES * TILES * 256 * 16 +
-                       (PACKED ? 0 : WIDE_THREADS / WAVE * RowsAt<FMT, WIDE_PARTS>::LDS * 16);
-    const dim3 grid((uint32_t)((A.N + WIDE_ROWS - 1) / WIDE_ROWS),
+    constexpr int ROWS = 16 * WIDE_PARTS * ROW_WAVES;
+    const size_t lds = 2 * (WIDE_WAVES / ROW_WAVES) * TILES * 256 * 16 +
+                       (PACKED ? 0 : WIDE_WAVES * RowsAt<FMT, WIDE_PARTS>::LDS * 16);
+    const dim3 grid((uint32_t)((A.N + ROWS - 1) / ROWS),
                     (uint32_t)((A.M + 16 * TILES - 1) / (16 * TILES)));
-    linear_w4_wide_kernel<FMT, PACKED, TILES><<<grid, WIDE_THREADS, lds, s>>>(A);
+    linear_w4_wide_kernel<FMT, PACKED, TILES, ROW_WAVES><<<grid, WIDE_THREADS, lds, s>>>(A);
     return hipGetLastError();
 }
 
-// Tiles of tokens for 17 tokens and more, in 16 tokens each: of the wide kernel, or 0 for
-// the 16-token one.  A kernel's time is its rounds of a workgroup a CU; a round of K = 8192
-// takes some 10 us in the 16-token kernel, 20, 25 and 38 us with tiles of 1, 2 and 4 in the
-// wide one.  (Packed MXFP4, 0, 1, 2, 4: 64 x 2048 x 8192 9.9, 20, 24, 38 us; 32 x 8192 21,
-// 22, 26, 37; 64 x 8192 39, 22, 25, 39; 32 x 28672 65, 53, 33, 43; 64 x 28672 126, 103, 62,
-// 47; 128 x 8192 74, 41, 27, 39.)
-int wide_tiles(int64_t M, int64_t N) {
-    const int64_t tokens = (M + 15) / 16, row_tiles = (N + WIDE_ROWS - 1) / WIDE_ROWS;
+// The kernel for 17 tokens and more: the wide one with `tiles` of 16 tokens and 64
+// row_waves rows, or (0) the 16-token one.  A kernel's time is its rounds of a workgroup a
+// CU; `cost` is a round's.  (Packed MXFP4, K = 8192, the 16-token kernel, then 64 rows x 16
+// and 32 tokens, then 128 x 16, 32 and 64: 64 x 2048 9.8, 13.7, 17.8, 20, 24, 38 us; 32 x
+// 8192 21, 16, 20, 22, 26, 37; 64 x 8192 39, 30, 20, 22, 25, 39; 32 x 28672 65, 65, 43, 53,
+// 33, 43; 64 x 28672 126, 112, 80, 103, 62, 47; 128 x 8192 74, 56, 39, 41, 27, 39.)
+struct Wide {
+    int tiles, row_waves, cost;
+};
+Wide wide_tile(int64_t M, int64_t N) {
+    const int64_t tokens = (M + 15) / 16;
     const auto rounds = [](int64_t workgroups) { return (workgroups + 255) / 256; };
-    int best = 0;
-    int64_t least = 4 * rounds((N + LINEAR_ROWS - 1) / LINEAR_ROWS * tokens);
-    for (const auto &[tiles, cost] : {std::pair{1, 8}, {2, 10}, {4, 15}}) {
-        const int64_t time = cost * rounds(row_tiles * ((tokens + tiles - 1) / tiles));
-        if (time < least) least = time, best = tiles;
+    Wide best = {0, 0, 8};
+    int64_t least = best.cost * rounds((N + LINEAR_ROWS - 1) / LINEAR_ROWS * tokens);
+    for (const Wide w : {Wide{1, 1, 12}, {2, 1, 15}, {1, 2, 17}, {2, 2, 20}, {4, 2, 30}}) {
+        const int rows = 16 * WIDE_PARTS * w.row_waves;
+        const int64_t time = w.cost * rounds((N + rows - 1) / rows * ((tokens + w.tiles - 1) / w.tiles));
+        if (time < least) least = time, best = w;
     }
     return best;
 }
@@ -316,10 +321,14 @@ hipError_t launch_tokens(const LinearArgs &A, hipStream_t s) {
     if (A.M <= 4) return launch_tile<FMT, X_F32, PACKED, 4>(A, s);
     if (A.M <= 8) return launch_tile<FMT, X_F32, PACKED, 8>(A, s);
     if constexpr (!X_F32) {
-        const int tiles = A.M > 16 ? wide_tiles(A.M, A.N) : 0;
-        if (tiles == 1) return launch_wide<FMT, PACKED, 1>(A, s);
-        if (tiles == 2) return launch_wide<FMT, PACKED, 2>(A, s);
-        if (tiles == 4) return launch_wide<FMT, PACKED, 4>(A, s);
+        if (A.M > 16) {
+            const Wide w = wide_tile(A.M, A.N);
+            if (w.row_waves == 1)
+                return w.tiles == 1 ? launch_wide<FMT, PACKED, 1, 1>(A, s) : launch_wide<FMT, PACKED, 2, 1>(A, s);
+            if (w.tiles == 1) return launch_wide<FMT, PACKED, 1, 2>(A, s);
+            if (w.tiles == 2) return launch_wide<FMT, PACKED, 2, 2>(A, s);
+            if (w.tiles == 4) return launch_wide<FMT, PACKED, 4, 2>(A, s);
+        }
     }
     return launch_tile<FMT, X_F32, PACKED, 16>(A, s);
 }
