@@ -402,22 +402,24 @@ __device__ __forceinline__ void w4_multiply(const W4Unit (&w)[PARTS], const X &x
     }
 }
 
-// A scale byte of 255 in any lane of a row makes the row's sums NaN (MXFP4).
+// A scale byte of 255 in any lane of a row makes the row's sums NaN (MXFP4).  No branch:
+// behind one that joins again before a product's result is read, the compiler counts the
+// waits that it needs along one way only, and on the shorter one the result may come too
+// late.
 template <int PARTS, int TILES>
 __device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[PARTS],
                                             f32x4_t (&acc)[PARTS][TILES]) {
     const int g = (threadIdx.x & (WAVE - 1)) >> 4;
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        uint64_t bad = __ballot(top[p] == 255u);
-        if (bad == 0) continue;
-        bad |= bad >> 32;
-        bad |= bad >> 16;
+        const uint64_t lanes = __ballot(top[p] == 255u);
+        uint32_t bad = (uint32_t)lanes | (uint32_t)(lanes >> 32);
+        bad = (bad | bad >> 16) >> (4 * g);  // bit i: row 4 g + i
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (bad >> (4 * g + i) & 1)
 #pragma unroll
-                for (int t = 0; t < TILES; ++t) acc[p][t][i] = __builtin_nanf("");
+            for (int t = 0; t < TILES; ++t)
+                acc[p][t][i] = (bad >> i & 1) != 0 ? __builtin_nanf("") : acc[p][t][i];
     }
 }
 
