@@ -588,8 +588,8 @@ typedef struct {
  *   workspace  fp4_moe_experts_workspace_bytes(...) bytes, 16-byte aligned scratch
  *              (calls that share one must be stream-ordered)
  * Products are exact as in fp4_linear_w4, sums fp32 in a fixed order; the gated
- * values go to the second product as two bf16 terms (17 bits) for bf16 x, three
- * for fp32 x.  An expert's weights reach only the tokens that name it, those of an
+ * values are fp32 and go to the second product with all their bits, as fp32 x does
+ * to the first.  An expert's weights reach only the tokens that name it, those of an
  * expert that no token names are not read.  At most 2^19 tokens, 32 experts of a
  * token; out is apart from the inputs.  Two launches, or three where rows are few and
  * tokens many.  Deterministic.

@@ -54,6 +54,7 @@ constexpr int kBufferRsrcWord3 = 0x00020000;
 // ---- DPP lane exchange inside quads -------------------------------------
 constexpr int QP_XOR1 = 0xB1;  // quad_perm [1,0,3,2]
 constexpr int QP_XOR2 = 0x4E;  // quad_perm [2,3,0,1]
+constexpr int DPP_ROW_SHL = 0x100;  // + n: lane l of 16 gets lane l + n's, or 0
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {

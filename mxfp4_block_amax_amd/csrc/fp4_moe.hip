@@ -166,7 +166,7 @@ struct MoeArgs {
     const int32_t *ids;
     const float *weights;
     MoeWeights W;
-    uint16_t *act;   // [tokens, top_k][terms][inner] bf16
+    void *act;       // the gated values, [tokens, top_k][Gated::PLANES][inner] Gated::Value
     float *partial;  // [splits][tokens][hidden], of a down product in splits
     void *out;
     int64_t tokens;
@@ -197,37 +197,42 @@ __device__ __forceinline__ uint64_t own_slots(int p, int top_k) {
     return ((1ull << top_k) - 1) << (p / top_k * top_k);
 }
 
-// A value as N bf16 terms: each the nearest to what the ones before left.
-template <int N>
-__device__ __forceinline__ void store_terms(uint16_t *p, int64_t stride, float v) {
+// The gated values between the products, all 24 bits of them: of bf16 activations in
+// fp32, which the second product splits into three bf16 terms, of fp32 ones in these terms
+// already (4 and 6 bytes a value).  (Two terms, 17 bits, showed: outputs in bf16 were 1.4e-4
+// away from those of a product in 32 bits, now 5e-6, and outputs in fp32 had their error.)
+// The terms are columns of the second product, so the third one costs no matrix
+// instruction.  Next to two terms side by side: 16 tokens of 128 experts, 4096 x 1536, 172
+// us and 170; 64 of 128, 2048 x 768, 150 and 140; 32 of 64, 1408 in NVFP4, 119 and 121; 64
+// of 8, 2816, 88 and 83: the splitting, by every workgroup.
+template <bool X_F32, int TOKENS>
+struct Gated {
+    using X = std::conditional_t<X_F32, XPart<false, TOKENS, 3, true>, XPart<true, TOKENS, 1, true>>;
+    using Value = std::conditional_t<X_F32, uint16_t, float>;
+    static constexpr int PLANES = X_F32 ? 3 : 1;
+};
+
+__device__ __forceinline__ void store_gated(float *p, int64_t, const float (&v)[4]) {
+    *(f32x4_t *)p = {v[0], v[1], v[2], v[3]};
+}
+__device__ __forceinline__ void store_gated(uint16_t *p, int64_t plane, const float (&v)[4]) {
+    u32x2_t t[3];
+    split_f32x4(v, t);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const __bf16 b = (__bf16)v;
-        p[k * stride] = __builtin_bit_cast(uint16_t, b);
-        const float rest = v - (float)b;
-        v = __builtin_fabsf((float)b) < __builtin_inff() ? rest : 0.0f;
-    }
+    for (int n = 0; n < 3; ++n) *(u32x2_t *)(p + n * plane) = t[n];
 }
 
-// The products of what K has past its last whole group, stretch k of weight rows base
-// + the lane's row; x(at, i) gives the terms of values at .. at + 7.
-template <int FMT, int TERMS, int PARTS, typename RowOf, typename X>
-__device__ __forceinline__ void multiply_tail(const uint8_t *codes, const uint8_t *scales, int k, int K,
-                                              const RowOf &row_of, const X &x,
-                                              f32x4_t (&acc)[PARTS][1], uint32_t (&top)[PARTS]) {
+// The weights of what K has past its last whole group, stretch k of the rows row_of(part,
+// the lane's row).
+template <int FMT, int PARTS, typename RowOf>
+__device__ __forceinline__ void load_tails(const uint8_t *codes, const uint8_t *scales, int k, int K,
+                                           const RowOf &row_of, W4Unit (&w)[PARTS]) {
     constexpr int BLK = FMT == 0 ? 32 : 16;
-    const int lane = threadIdx.x & (WAVE - 1), at = k + 32 * (lane >> 4);
-    W4Unit w[PARTS];
 #pragma unroll
     for (int p = 0; p < PARTS; ++p) {
-        const int64_t row = row_of(p, lane & 15);
+        const int64_t row = row_of(p, threadIdx.x & 15);
         w[p] = load_tail<FMT>(codes + row * (K / 2), scales + row * (K / BLK), k, K);
     }
-    Terms<TERMS> b[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (at + 8 * i < K) b[i] = x(at + 8 * i);
-    w4_multiply<FMT, TERMS>(w, [&](int, int i, int n) { return b[i].p[n]; }, acc, top);
 }
 
 constexpr int UP_WAVES = 4;
@@ -242,7 +247,8 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
     using XT = std::conditional_t<X_F32, float, uint16_t>;
     using X = XPart<X_F32, TOKENS>;
     using W = RowsAt<FMT, 2>;
-    constexpr int NA = X_F32 ? 3 : 2, BLK = FMT == 0 ? 32 : 16;
+    using G = Gated<X_F32, TOKENS>;
+    constexpr int BLK = FMT == 0 ? 32 : 16;
     extern __shared__ u32x4_t lds[];
     __shared__ uint16_t lists[UP_WAVES][MOE_BLOCK];
     __shared__ int count;
@@ -326,15 +332,19 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
             },
             x, mine, wave, waves, groups, acc, top, [](int) {});
         const int t = (wave - groups % waves + waves) % waves;
-        for (int k = groups * W4_GROUP + W4_STRETCH * t; k < K; k += W4_STRETCH * waves)
-            multiply_tail<FMT, X::TERMS>(
-                codes, scales, k, K, [&](int p, int row) { return (int64_t)p * inner + row; },
-                [&](int at) {
-                    Terms<X::TERMS> b = {};
-                    if (r < rows) b = load_terms(x0 + list[c0 + r] / A.top_k * (int64_t)K + at);
-                    return b;
-                },
-                acc, top);
+        for (int k = groups * W4_GROUP + W4_STRETCH * t; k < K; k += W4_STRETCH * waves) {
+            W4Unit w[2];
+            load_tails<FMT>(codes, scales, k, K,
+                            [&](int p, int row) { return (int64_t)p * inner + row; }, w);
+            Terms<X::TERMS> b[4] = {};
+            const int at = k + 32 * g;
+            if (r < rows)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at + 8 * i < K)
+                        b[i] = load_terms(x0 + list[c0 + r] / A.top_k * (int64_t)K + at + 8 * i);
+            w4_multiply<FMT, X::TERMS>(w, [&](int, int i, int n) { return b[i].p[n]; }, acc, top);
+        }
         if constexpr (FMT == 0) w4_nan_rows(top, acc);
         __syncthreads();
         f32x4_t *sums = (f32x4_t *)lds;  // [waves][2][64]
@@ -348,12 +358,13 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
                 up += sums[(v * 2 + 1) * WAVE + lane];
             }
             const int64_t pair = token0 * A.top_k + list[c0 + r];
-            uint16_t *to = A.act + pair * NA * inner + row0 + 4 * g;
+            float v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float gj = gate[j] * s_g, uj = up[j] * s_g;
-                store_terms<NA>(to + j, inner, gj / (1.0f + expf(-gj)) * uj);
+                v[j] = gj / (1.0f + expf(-gj)) * uj;
             }
+            store_gated((typename G::Value *)A.act + pair * G::PLANES * inner + row0 + 4 * g, inner, v);
         }
         __syncthreads();
     }
@@ -506,8 +517,10 @@ __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *w
 // for 42 % of the cycles; one token of 64, 2048 x 768: 6 us of latency.
 template <int FMT, bool X_F32, int TOKENS>
 __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeArgs A, int block_tokens) {
-    constexpr int NA = X_F32 ? 3 : 2, BLK = FMT == 0 ? 32 : 16;
-    using X = XPart<false, TOKENS, NA>;
+    using G = Gated<X_F32, TOKENS>;
+    using X = typename G::X;
+    using Value = typename G::Value;
+    constexpr int PLANES = G::PLANES, BLK = FMT == 0 ? 32 : 16;
     using W = RowsAt<FMT, 1>;
     extern __shared__ u32x4_t lds[];
     const int lane = threadIdx.x & (WAVE - 1);
@@ -539,28 +552,38 @@ __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeA
         items = make_plan<TOKENS>(plan, ids, weights, pairs, A.top_k, A.W.experts);
     }
 
-    const uint16_t *act0 = A.act + token0 * A.top_k * NA * K;
-    const Rsrc act = span(act0, pairs * NA * K * 2);
+    const Value *act0 = (const Value *)A.act + token0 * A.top_k * PLANES * K;
+    const Rsrc act = span(act0, pairs * PLANES * K * (int)sizeof(Value));
     const int per = K / W4_GROUP;
     const int splits = gridDim.z, step = splits * DOWN_WAVES<TOKENS>;
     const int turn = blockIdx.z * DOWN_WAVES<TOKENS> + wave;
-    f32x4_t acc[1][1] = {};
+    f32x4_t acc[1][X::TILES] = {};
     uint32_t top[1] = {0};
     // the sums of an item's products so far go to its tokens
     const auto add = [&](const MoeItem &it) {
         if constexpr (FMT == 0) w4_nan_rows(top, acc);
+        const f32x4_t sum = X::sum_columns(acc[0]);
         if (r < it.count) {
             const float s_g = FMT == 0 ? 1.0f : A.W.down_global[(int64_t)it.expert * A.W.global_stride];
             f32x4_t *to = sums + (wave * block_tokens + plan.pair[it.first + r] / A.top_k) * 4 + g;
-            *to += acc[0][0] * (plan.share[it.first + r] * s_g);
+            *to += sum * (plan.share[it.first + r] * s_g);
         }
-        acc[0][0] = {0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < X::TILES; ++t) acc[0][t] = {0, 0, 0, 0};
         top[0] = 0;
     };
     const auto item_of = [&](int i) {
         MoeItem it = plan.items[i];
         it.expert = __builtin_amdgcn_readfirstlane(it.expert);
         return it;
+    };
+    // where the lane's load i has an item's values, of the stretch at 0
+    const auto x_at = [&](const MoeItem &it, int i) {
+        const auto p = X::place(i);
+        return p.row < it.count
+                   ? (uint32_t)((plan.pair[it.first + p.row] * PLANES + p.plane) * K + p.k) *
+                         (uint32_t)sizeof(Value)
+                   : NOWHERE;
     };
     multiply_groups<FMT, false, W, X>(
         [&](int n) {
@@ -570,12 +593,7 @@ __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeA
                                K, mine + X::PIECES),
                              (uint32_t)(n % per * W4_GROUP), {}};
 #pragma unroll
-            for (int i = 0; i < X::LOADS; ++i) {
-                const auto p = X::place(i);
-                a.x_at[i] = p.row < it.count
-                                ? (uint32_t)((plan.pair[it.first + p.row] * NA + p.plane) * K + p.k) * 2
-                                : NOWHERE;
-            }
+            for (int i = 0; i < X::LOADS; ++i) a.x_at[i] = x_at(it, i);
             return a;
         },
         act, mine, turn, step, items * per, acc, top, [&](int n) { add(item_of(n / per)); });
@@ -584,19 +602,18 @@ __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeA
     for (int n = (turn - items * per % step + step) % step; n < items * rest; n += step) {
         const MoeItem it = item_of(n / rest);
         const int64_t row = (int64_t)it.expert * hidden + row0;
-        multiply_tail<FMT, NA>(
-            A.W.down_codes + row * (K / 2), A.W.down_scales + row * (K / BLK),
-            per * W4_GROUP + n % rest * W4_STRETCH, K, [](int, int rr) { return (int64_t)rr; },
-            [&](int at) {
-                Terms<NA> b = {};
-                if (r < it.count) {
-                    const uint16_t *from = act0 + (int64_t)plan.pair[it.first + r] * NA * K + at;
+        const int k = per * W4_GROUP + n % rest * W4_STRETCH;
+        W4Unit w[1];
+        load_tails<FMT>(A.W.down_codes + row * (K / 2), A.W.down_scales + row * (K / BLK), k, K,
+                        [](int, int rr) { return (int64_t)rr; }, w);
+        X xs;
+        uint32_t at[X::LOADS];
 #pragma unroll
-                    for (int m = 0; m < NA; ++m) b.p[m] = load_terms(from + (int64_t)m * K).p[0];
-                }
-                return b;
-            },
-            acc, top);
+        for (int i = 0; i < X::LOADS; ++i) at[i] = k + X::place(i).k < K ? x_at(it, i) : NOWHERE;
+        xs.load(act, at, k);
+        xs.store(mine);
+        w4_multiply<FMT, X::TERMS>(
+            w, [&](int t, int i, int m) { return X::piece(mine, g, t, i, m); }, acc, top);
         add(it);
     }
     __syncthreads();
@@ -653,10 +670,9 @@ hipError_t launch_tile(MoeArgs A, int32_t *status, hipStream_t s) {
     moe_up_kernel<FMT, X_F32, TOKENS><<<up_grid, UP_WAVES * WAVE, up_lds, s>>>(A, status);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    constexpr int NA = X_F32 ? 3 : 2;
     const auto down_lds = [&](int tokens) {
         return (size_t)DOWN_WAVES<TOKENS> *
-                   (tokens * 4 + XPart<false, TOKENS, NA>::PIECES + RowsAt<FMT, 1>::LDS) * 16 +
+                   (tokens * 4 + Gated<X_F32, TOKENS>::X::PIECES + RowsAt<FMT, 1>::LDS) * 16 +
                MoePlan::bytes(tokens * A.top_k, A.W.experts);
     };
     int down_block = block;  // fewer tokens where a plan of many pairs leaves no room for them
@@ -744,7 +760,7 @@ hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidd
 }
 
 static size_t act_bytes(int64_t tokens, int top_k, int64_t inner, bool x_bf16) {
-    return (size_t)tokens * top_k * (x_bf16 ? 2 : 3) * inner * sizeof(uint16_t);
+    return (size_t)tokens * top_k * inner * (x_bf16 ? sizeof(float) : 3 * sizeof(uint16_t));
 }
 
 size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner, bool x_bf16) {

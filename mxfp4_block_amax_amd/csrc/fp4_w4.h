@@ -89,9 +89,9 @@ struct Terms {
 };
 
 // Four fp32 values as three bf16 terms each: a value's upper 16 bits, those of what
-// they leave, and the rest (differences are exact, and nothing overflows).  A
-// value that is not finite is its first term alone.
-__device__ __forceinline__ void split_f32x4(const float (&x)[4], u32x2_t (&t)[3]) {
+// they leave, and the rest (differences are exact, and nothing overflows).  Of a value
+// that is not finite the first term is right, the others are NaN.
+__device__ __forceinline__ void split_finite_f32x4(const float (&x)[4], u32x2_t (&t)[3]) {
     float rest[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) rest[i] = x[i];
@@ -102,6 +102,10 @@ __device__ __forceinline__ void split_f32x4(const float (&x)[4], u32x2_t (&t)[3]
 #pragma unroll
         for (int i = 0; i < 4; ++i) rest[i] = rest[i] - u2f(f2u(rest[i]) & 0xFFFF0000u);
     }
+}
+// The same of any values: one that is not finite is its first term alone.
+__device__ __forceinline__ void split_f32x4(const float (&x)[4], u32x2_t (&t)[3]) {
+    split_finite_f32x4(x, t);
     const uint32_t top = max(max(f2u(x[0]) & 0x7FFFFFFFu, f2u(x[1]) & 0x7FFFFFFFu),
                              max(f2u(x[2]) & 0x7FFFFFFFu, f2u(x[3]) & 0x7FFFFFFFu));
     if (top >= 0x7F800000u) {
@@ -437,10 +441,18 @@ __device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[PARTS],
 // write at a time (a row's v) and what they read (all rows of v / 4 = 0 .. 3, the four
 // lane groups) are both next to each other, so over all banks (with [v][n][row ^ v] the
 // lane groups' reads shared banks: 16 tokens of 128 experts 180 us, not 170).
-template <bool F32, int ROWS, int PLANES = 1>
+//
+// COLUMNS: a product has 16 columns, of which ROWS tokens leave some without use; the
+// terms are then columns of their own, token r's term n in column ROWS n + r, TILES
+// products of 16 hold them all, and sum_columns adds them up.  (Three terms of four
+// tokens are one product instead of three, with a third of the reads.)  Pieces are at
+// [v % 4][v / 4][n][row ^ v].
+template <bool F32, int ROWS, int PLANES = 1, bool COLUMNS = false>
 struct XPart {
-    static constexpr int TERMS = F32 ? 3 : PLANES;
-    static constexpr int PIECES = ROWS * 16 * TERMS;                      // in LDS
+    static constexpr int SPLIT = F32 ? 3 : PLANES;                        // terms of a value
+    static constexpr int TERMS = COLUMNS ? 1 : SPLIT;          // products of a tile
+    static constexpr int TILES = COLUMNS ? (SPLIT * ROWS + 15) / 16 : 1;
+    static constexpr int PIECES = ROWS * 16 * SPLIT;           // in LDS
     static constexpr int HALVES = F32 ? 2 : 1;                            // loads of a piece
     static constexpr int LOADS = ROWS * 16 * HALVES * PLANES / WAVE;      // of a lane
     static_assert(ROWS * 16 * HALVES * PLANES % WAVE == 0, "every lane loads");
@@ -465,7 +477,9 @@ struct XPart {
     }
 
     static __device__ __forceinline__ int at(int v, int n, int row) {
-        return (((v & 3) * TERMS + n) * 4 + (v >> 2)) * ROWS + (row ^ (v & (ROWS - 1)));
+        const int place = row ^ (v & (ROWS - 1));
+        if constexpr (COLUMNS) return (((v & 3) * 4 + (v >> 2)) * SPLIT + n) * ROWS + place;
+        else return (((v & 3) * SPLIT + n) * 4 + (v >> 2)) * ROWS + place;
     }
 
     __device__ __forceinline__ void store(u32x4_t *lds) const {
@@ -478,20 +492,46 @@ struct XPart {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = u2f(v[n][j]);
                 u32x2_t t[3];
-                split_f32x4(x, t);
+                if constexpr (COLUMNS) split_finite_f32x4(x, t);
+                else split_f32x4(x, t);
                 u32x2_t *to = (u32x2_t *)(lds + at(piece, 0, from.row)) + (from.k / 4 & 1);
 #pragma unroll
-                for (int m = 0; m < 3; ++m) to[m * 8 * ROWS] = t[m];
+                for (int m = 0; m < 3; ++m) to[m * (COLUMNS ? 2 : 8) * ROWS] = t[m];
             } else {
                 lds[at(piece, from.plane, from.row)] = v[n];
             }
         }
     }
 
-    // Term n of values 8 i .. 8 i + 7 of the lane's 32 for its row; the 32 values of lane
-    // group g are the stretch's group_of(g)-th.
-    static __device__ __forceinline__ bf16x8_t piece(const u32x4_t *lds, int group, int i, int n) {
-        return __builtin_bit_cast(bf16x8_t, lds[at(4 * group + i, n, threadIdx.x & (ROWS - 1))]);
+    // The term and row of the lane's column of tile t (COLUMNS).  Columns past the last
+    // term have the last one again: nothing reads their sums.
+    static __device__ __forceinline__ int column_term(int t) {
+        return min((16 * t + (int)(threadIdx.x & 15)) / ROWS, SPLIT - 1);
+    }
+    static __device__ __forceinline__ int column_row() { return threadIdx.x & (ROWS - 1); }
+
+    // Values 8 i .. 8 i + 7 of the lane's 32 for its row, term n of them, or that of its
+    // column of tile t; the 32 values of lane group g are the stretch's group_of(g)-th.
+    static __device__ __forceinline__ bf16x8_t piece(const u32x4_t *lds, int group, int t, int i,
+                                                     int n) {
+        const int term = COLUMNS ? column_term(t) : n;
+        return __builtin_bit_cast(bf16x8_t, lds[at(4 * group + i, term, column_row())]);
+    }
+
+    // The sums of the lane's token, in the columns of its first term (COLUMNS, three
+    // terms of 4 or 8 tokens): the small terms' first.  A first term that is not finite
+    // makes a sum that is not either, and then it is the sum: the other terms may be NaN.
+    static __device__ __forceinline__ f32x4_t sum_columns(const f32x4_t (&acc)[TILES]) {
+        static_assert(COLUMNS && SPLIT == 3 && (ROWS == 4 || ROWS == 8));
+        f32x4_t s;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float second = dppf<DPP_ROW_SHL + ROWS>(acc[0][j]);
+            const float third = ROWS == 4 ? dppf<DPP_ROW_SHL + 8>(acc[0][j]) : acc[TILES - 1][j];
+            s[j] = __builtin_fabsf(acc[0][j]) < __builtin_inff() ? acc[0][j] + (second + third)
+                                                                 : acc[0][j];
+        }
+        return s;
     }
 };
 
@@ -518,8 +558,8 @@ struct Group {
 template <int FMT, bool PACKED, typename W, typename X, int PARTS, typename GroupAt, typename Done>
 __device__ __forceinline__ void multiply_groups(const GroupAt &group, Rsrc x, u32x4_t *x_lds,
                                                 int first, int step, int groups,
-                                                f32x4_t (&acc)[PARTS][1], uint32_t (&top)[PARTS],
-                                                const Done &done) {
+                                                f32x4_t (&acc)[PARTS][X::TILES],
+                                                uint32_t (&top)[PARTS], const Done &done) {
     const int g = (threadIdx.x & (WAVE - 1)) >> 4, part = PACKED ? packed_group(g) : g;
     const auto from = [](uint32_t k, int more) { return k == NOWHERE ? k : k + more; };
     if (first >= groups) return;
@@ -551,7 +591,7 @@ __device__ __forceinline__ void multiply_groups(const GroupAt &group, Rsrc x, u3
             W4Unit u[PARTS];
             here.w.units(s, pair[j / 2], j, u);
             w4_multiply<FMT, X::TERMS>(
-                u, [&](int, int i, int m) { return X::piece(x_lds, part, i, m); }, acc, top);
+                u, [&](int t, int i, int m) { return X::piece(x_lds, part, t, i, m); }, acc, top);
             if (j % 2 == 1) pair[j / 2] = next.w.load_pair(from(next.k, W4_STRETCH * (j - 1)));
             __builtin_amdgcn_sched_barrier(0);
         }
