@@ -549,7 +549,8 @@ fp4_status fp4_linear_w4_packed(fp4_format fmt, const void *x, fp4_dtype xt, int
  * or over all experts (0).
  *   x          [tokens, hidden] fp32 or bf16     router [experts, hidden] fp32 or bf16
  *   chosen     [tokens, top_k] int32             weights [tokens, top_k] fp32
- *   workspace  fp4_moe_route_workspace_bytes(...) bytes, scratch
+ *   workspace  fp4_moe_route_workspace_bytes(...) bytes, scratch; of the largest
+ *              batch, enough for every smaller one
  * hidden is a multiple of 8; at most 1024 experts, 32 of a token, 2^19 tokens; x,
  * router and workspace 16-byte aligned.  Sums are 64-bit, their order is fixed:
  * deterministic.  A NaN logit is below every other.  Two launches.
@@ -586,7 +587,8 @@ typedef struct {
  *   weights    [tokens, top_k] fp32
  *   out        [tokens, hidden] fp32 or bf16; zeros for a token without experts
  *   workspace  fp4_moe_experts_workspace_bytes(...) bytes, 16-byte aligned scratch
- *              (calls that share one must be stream-ordered)
+ *              (calls that share one must be stream-ordered); of the largest batch,
+ *              enough for every smaller one
  * Products are exact as in fp4_linear_w4, sums fp32 in a fixed order; the gated
  * values are fp32 and go to the second product with all their bits, as fp32 x does
  * to the first.  An expert's weights reach only the tokens that name it, those of an

@@ -731,8 +731,14 @@ hipError_t launch_logits(const void *x, const void *router, double *logits, int6
 
 }  // namespace
 
+// The workspaces' sizes do not fall with the tokens: one for the largest batch serves every
+// smaller one.  Shares get fewer where tiles of tokens get more, and within a tile the
+// largest count needs most, so these are the counts to look at.
 size_t route_workspace_bytes(int64_t tokens, int64_t hidden, int experts) {
-    return (size_t)route_shape(tokens, hidden, experts).splits * tokens * experts * sizeof(double);
+    const auto rows = [&](int64_t t) { return route_shape(t, hidden, experts).splits * t; };
+    int64_t most = rows(tokens);
+    for (int64_t t = 16; t < tokens && rows(t) > t; t += 16) most = rows(t) > most ? rows(t) : most;
+    return (size_t)most * experts * sizeof(double);
 }
 
 hipError_t launch_route(const void *x, bool x_bf16, int64_t tokens, int64_t hidden,
@@ -764,9 +770,15 @@ static size_t act_bytes(int64_t tokens, int top_k, int64_t inner, bool x_bf16) {
 }
 
 size_t experts_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner, bool x_bf16) {
-    const int splits = down_splits(tokens, top_k, hidden, inner);
-    return act_bytes(tokens, top_k, inner, x_bf16) +
-           (splits > 1 ? (size_t)splits * tokens * hidden * sizeof(float) : 0);
+    const auto bytes = [&](int64_t t) {
+        const int splits = down_splits(t, top_k, hidden, inner);
+        return act_bytes(t, top_k, inner, x_bf16) +
+               (splits > 1 ? (size_t)splits * t * hidden * sizeof(float) : 0);
+    };
+    size_t most = bytes(tokens);
+    for (int64_t t = MOE_BLOCK; t < tokens && down_splits(t, top_k, hidden, inner) > 1; t += MOE_BLOCK)
+        most = bytes(t) > most ? bytes(t) : most;
+    return most;
 }
 
 hipError_t launch_experts(int fmt, const MoeWeights &W, const void *x, bool x_bf16, int64_t tokens,
