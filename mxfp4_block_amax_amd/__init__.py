@@ -737,13 +737,15 @@ def linear_w4(fmt: int, x: torch.Tensor, bt_codes: torch.Tensor, bt_scales: torc
         raise ValueError("fmt must be MXFP4 or NVFP4")
     if len(weight) != 2 or len(shape) < 1 or shape[-1] != 2 * weight[1]:
         raise ValueError("x must be [.., K], the weight's codes [N, K/2]")
+    if weight[1] == 0:
+        raise ValueError("K must be at least one block")
     device, code = _dense(x)
     N, kh = weight
     codes = _bytes(bt_codes, N * kh, "bt_codes", device)
     scales = _bytes(bt_scales, N * kh // (16 if fmt == MXFP4 else 8), "bt_scales", device)
     s_g = None if fmt == MXFP4 else _scalar(global_scale, "global_scale", device)
     out, out_code = _output(out, (*shape[:-1], N), x, out_dtype)
-    M = x.numel() // (2 * kh) if kh else 0
+    M = x.numel() // (2 * kh)
     if M > 0:
         _on(device, (_lib or lib()).fp4_linear_w4, fmt, x.data_ptr(), code, M, 2 * kh, codes,
             scales, s_g, N, out.data_ptr(), out_code)
