@@ -723,7 +723,8 @@ typedef struct {
  *   cu_tokens, lengths, seqs, tokens   as in fp4_kv_batch: they give the positions
  *   frequencies [rotary/2] device doubles, radians per position
  * head_dim is 64, 128, 192 or 256, rotary a multiple of 16 up to head_dim, eps >= 0.
- * Sums and rotations are fp32 (rounded once), angles 64-bit.  Rows of no sequence
+ * Sums and rotations are fp32 (rounded once; a norm's squares may be past its range),
+ * angles 64-bit.  Rows of no sequence
  * come out as zeros; so do those at positions below 0, which raise
  * FP4_FLAG_CACHE_INDEX, as prefix sums that are none do.  One launch.
  * Deterministic.

@@ -6,8 +6,9 @@
 //
 // for the pairs i of the first `rotary` values of a head: (i, i + rotary / 2), or
 // (2 i, 2 i + 1) interleaved; the others are y = z.  Sums and rotations are fp32,
-// rounded once.  Angles are 64-bit: at position 10^6 an angle of 32 bits is off by
-// some 0.06.  Bound by memory on prompts, by a launch on single tokens.
+// rounded once; a head's squares may be past fp32's range.  Angles are 64-bit: at
+// position 10^6 an angle of 32 bits is off by some 0.06.  Bound by memory on prompts, by
+// a launch on single tokens.
 #include <type_traits>
 
 #include "fp4_kernels.h"
@@ -78,6 +79,48 @@ __device__ __forceinline__ float head_sum(float s, int base) {
     return s;
 }
 
+// And the largest of non-negative floats, by their bits.
+template <int LANES>
+__device__ __forceinline__ uint32_t head_max(uint32_t m, int base) {
+    m = max(m, dpp<QP_XOR1>(m));
+    m = max(m, dpp<QP_XOR2>(m));
+    if constexpr (LANES == 12) {
+        const uint32_t a = __shfl(m, base, WAVE), b = __shfl(m, base + 4, WAVE);
+        return max(max(a, b), (uint32_t)__shfl(m, base + 8, WAVE));
+    }
+    if constexpr (LANES >= 8) m = max(m, (uint32_t)__shfl_xor(m, 4, WAVE));
+    if constexpr (LANES >= 16) m = max(m, (uint32_t)__shfl_xor(m, 8, WAVE));
+    return m;
+}
+
+__device__ __forceinline__ float sum_of_squares(const Eight &a, const Eight &b) {
+    float s = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        s = __builtin_fmaf(a.v[i], a.v[i], __builtin_fmaf(b.v[i], b.v[i], s));
+    return s;
+}
+
+// A head whose squares fp32 does not hold, their mean below 2^-100 or infinite: scaled by
+// the power of two that makes the largest of its values and sqrt(eps) 0.5 to 1, and eps by
+// its square, so that values over the mean's root are what they were.  Returns 1 / root.
+// Zeros and what is not finite stay as they are.
+template <int D>
+__device__ __forceinline__ float far_norm(Eight &a, Eight &b, float mean, float eps, int base) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, max(f2u(a.v[i]) & 0x7FFFFFFFu, f2u(b.v[i]) & 0x7FFFFFFFu));
+    top = max(head_max<D / 16>(top, base), f2u(__builtin_sqrtf(eps)));
+    if (top == 0 || top >= 0x7F800000u) return 1.0f / __builtin_sqrtf(mean);
+    int e;
+    (void)__builtin_frexpf(u2f(top), &e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a.v[i] = ldexpf(a.v[i], -e), b.v[i] = ldexpf(b.v[i], -e);
+    const float s = head_sum<D / 16>(sum_of_squares(a, b), base);
+    return 1.0f / __builtin_sqrtf(s * (1.0f / D) + ldexpf(eps, -2 * e));
+}
+
 // A workgroup has a token and some of its heads, a wave 64 / (D / 16) heads at a
 // time.  A lane has 16 values of a head, eight pairs: both halves of them, so that
 // nothing is exchanged between lanes but a head's sum, and the pair's angles are
@@ -122,13 +165,14 @@ __global__ __launch_bounds__(ROTATE_WAVES *WAVE) void norm_rotate_kernel(RotateA
             a = load_eight<F32>(x, at + at0);
             b = load_eight<F32>(x, at + at1);
         }
-        float s = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s = __builtin_fmaf(a.v[i], a.v[i], __builtin_fmaf(b.v[i], b.v[i], s));
-        s = head_sum<LANES>(s, lane / LANES * LANES);
+        const int base = lane / LANES * LANES;
+        const float s = head_sum<LANES>(sum_of_squares(a, b), base);
         if (real && weight != nullptr) {
-            const float inv = 1.0f / __builtin_sqrtf(s * (1.0f / D) + A.eps);
+            const float mean = s * (1.0f / D) + A.eps;
+            // (all of a head's lanes go the same way)
+            const float inv = __builtin_expect(mean >= 0x1p-100f && mean < __builtin_inff(), 1)
+                                  ? 1.0f / __builtin_sqrtf(mean)
+                                  : far_norm<D>(a, b, mean, A.eps, base);
             const Eight wa = A.weight_f32 ? load_eight<true>(weight, at0)
                                           : load_eight<false>(weight, at0);
             const Eight wb = A.weight_f32 ? load_eight<true>(weight, at1)
