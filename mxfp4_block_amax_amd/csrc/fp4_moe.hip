@@ -281,6 +281,7 @@ __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_ke
         n = __builtin_popcountll(firsts);
         if (firsts >> lane & 1)
             list[__builtin_popcountll(firsts & ((1ull << lane) - 1))] = (uint16_t)lane;
+        wave_order();
     } else {
         if (A.slots) {
             const int slot = e;
@@ -611,7 +612,9 @@ __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeA
 #pragma unroll
         for (int i = 0; i < X::LOADS; ++i) at[i] = k + X::place(i).k < K ? x_at(it, i) : NOWHERE;
         xs.load(act, at, k);
+        wave_order();
         xs.store(mine);
+        wave_order();
         w4_multiply<FMT, X::TERMS>(
             w, [&](int t, int i, int m) { return X::piece(mine, g, t, i, m); }, acc, top);
         add(it);

@@ -147,6 +147,15 @@ __device__ __forceinline__ f32x4_t mfma_w4(bf16x8_t w, bf16x8_t x, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
 }
 
+// What a wave's lanes put into LDS for each other, in order: those before are there for
+// those after.  The hardware keeps the order of a wave's LDS operations; this keeps the
+// compiler from changing it, and is no instruction.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // ---- loads ------------------------------------------------------------------
 // Buffer loads: past the end of what the resource spans they give zeros and move
 // nothing, so that a pipeline's loads need no branches (around which the waits for
@@ -244,7 +253,9 @@ struct RowsAt {
             if (n * WAVE + lane < 16 * PARTS * EACH) lds[128 + n * WAVE + lane] = s.v[n];
     }
     // to the products' order, v[PARTS * stretch + part]: piece v of row r goes through
-    // 8 r + (v ^ r), which spreads what is written and what is read over the banks
+    // 8 r + (v ^ r), which spreads what is written and what is read over the banks.  Also
+    // orders scales that were put before it; the next pair's spread, and the next put, want
+    // a barrier or wave_order after the last use of this one's.
     __device__ __forceinline__ void spread(Pair &pair) const {
         const int lane = threadIdx.x & (WAVE - 1), r = lane & 15, g = lane >> 4;
         u32x4_t in[2 * PARTS];
@@ -254,8 +265,10 @@ struct RowsAt {
         for (int p = 0; p < PARTS; ++p) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) lds[64 * n + (lane ^ (lane >> 3))] = in[2 * p + n];
+            wave_order();
 #pragma unroll
             for (int h = 0; h < 2; ++h) pair.v[PARTS * h + p] = lds[8 * r + ((4 * h + g) ^ (r & 7))];
+            if (p + 1 < PARTS) wave_order();
         }
     }
     // stretch j of the group, of a spread pair
@@ -435,7 +448,7 @@ __device__ __forceinline__ void w4_nan_rows(const uint32_t (&top)[PARTS],
 // 16 - ROWS of 16 lanes would load nothing), and fp32 is split into its terms once a
 // value, not once for each row of a tile.  Rows that are not there are others' or
 // whatever LDS held: they end in sums that nothing stores.  A wave's LDS operations keep
-// their order, so there is no barrier.
+// their order, so there is no barrier but wave_order.
 //
 // Piece of values 8 v .. of row `row`, term n: at [v % 4][n][v / 4][row ^ v].  What lanes
 // write at a time (a row's v) and what they read (all rows of v / 4 = 0 .. 3, the four
@@ -585,6 +598,7 @@ __device__ __forceinline__ void multiply_groups(const GroupAt &group, Rsrc x, u3
         for (int j = 0; j < 4; ++j) {
             if (j % 2 == 0) here.w.spread(pair[j / 2]);
             xs[j & 1].store(x_lds);
+            wave_order();
             if (j < 2) xs[j].load(x, here.x_at, here.k + W4_STRETCH * (j + 2));
             else xs[j & 1].load(x, next.x_at, from(next.k, W4_STRETCH * (j - 2)));
             __builtin_amdgcn_sched_barrier(0);
@@ -593,6 +607,7 @@ __device__ __forceinline__ void multiply_groups(const GroupAt &group, Rsrc x, u3
             w4_multiply<FMT, X::TERMS>(
                 u, [&](int t, int i, int m) { return X::piece(x_lds, part, t, i, m); }, acc, top);
             if (j % 2 == 1) pair[j / 2] = next.w.load_pair(from(next.k, W4_STRETCH * (j - 1)));
+            wave_order();  // before the next stretch's stores
             __builtin_amdgcn_sched_barrier(0);
         }
         done(n);
