@@ -5,9 +5,8 @@
 //
 // s_g = 1 for MXFP4.  What it cannot do without is reading the weight once: a
 // token's 2 N K operations are far below the MFMA's rate up to some 64 tokens.
-#include <initializer_list>
-
 #include "fp4_kernels.h"
+#include "fp4_linear.h"
 #include "fp4_w4.h"
 
 namespace fp4dev {
@@ -22,7 +21,6 @@ struct LinearArgs {
     bool out_bf16;
 };
 
-constexpr int LINEAR_ROWS = 32;  // weight rows of a workgroup
 constexpr int LINEAR_WAVES = 16;
 
 // Waves of a workgroup: 16, or 8 where more tokens leave registers or LDS for no more.
@@ -140,7 +138,7 @@ hipError_t launch_tile(const LinearArgs &A, hipStream_t s) {
 // activations is in LDS for all; the next one is on its way in registers.  Matrix, vector
 // and LDS instructions bound it, with tiles of 4 some 2000 of a stretch's 5900 cycles each:
 // 64 x 28672 x 8192 packed 47 us, of which the weight's bytes are 26.
-constexpr int WIDE_PARTS = 4, WIDE_WAVES = 8;
+constexpr int WIDE_WAVES = 8;
 constexpr int WIDE_THREADS = WIDE_WAVES * WAVE;
 
 template <int FMT, bool PACKED, int TILES, int ROW_WAVES>
@@ -290,28 +288,6 @@ hipError_t launch_wide(const LinearArgs &A, hipStream_t s) {
                     (uint32_t)((A.M + 16 * TILES - 1) / (16 * TILES)));
     linear_w4_wide_kernel<FMT, PACKED, TILES, ROW_WAVES><<<grid, WIDE_THREADS, lds, s>>>(A);
     return hipGetLastError();
-}
-
-// The kernel for 17 tokens and more: the wide one with `tiles` of 16 tokens and 64
-// row_waves rows, or (0) the 16-token one.  A kernel's time is its rounds of a workgroup a
-// CU; `cost` is a round's.  (Packed MXFP4, K = 8192, the 16-token kernel, then 64 rows x 16
-// and 32 tokens, then 128 x 16, 32 and 64: 64 x 2048 9.8, 13.7, 17.8, 20, 24, 38 us; 32 x
-// 8192 21, 16, 20, 22, 26, 37; 64 x 8192 39, 30, 20, 22, 25, 39; 32 x 28672 65, 65, 43, 53,
-// 33, 43; 64 x 28672 126, 112, 80, 103, 62, 47; 128 x 8192 74, 56, 39, 41, 27, 39.)
-struct Wide {
-    int tiles, row_waves, cost;
-};
-Wide wide_tile(int64_t M, int64_t N) {
-    const int64_t tokens = (M + 15) / 16;
-    const auto rounds = [](int64_t workgroups) { return (workgroups + 255) / 256; };
-    Wide best = {0, 0, 8};
-    int64_t least = best.cost * rounds((N + LINEAR_ROWS - 1) / LINEAR_ROWS * tokens);
-    for (const Wide w : {Wide{1, 1, 12}, {2, 1, 15}, {1, 2, 17}, {2, 2, 20}, {4, 2, 30}}) {
-        const int rows = 16 * WIDE_PARTS * w.row_waves;
-        const int64_t time = w.cost * rounds((N + rows - 1) / rows * ((tokens + w.tiles - 1) / w.tiles));
-        if (time < least) least = time, best = w;
-    }
-    return best;
 }
 
 // Tokens of a tile: the smallest that holds them (packed MXFP4, 8192 x 8192, tiles of 4, 8
