@@ -517,8 +517,9 @@ fp4_status fp4_linear_mxfp4(const void *x, fp4_dtype xt, int64_t M, int64_t K,
  *   c          [M, N] fp32 or bf16 (nearest, ties to even, of the fp32 sum
  *              times s_g)
  * Products are exact: a weight's value fits bf16 (MXFP4 for scale bytes up to
- * 252), fp32 activations count with all their bits.  Sums are fp32, their order
- * is fixed: deterministic.  A NaN scale byte makes its row's outputs NaN.  K is
+ * 252), fp32 activations from 2^-110 on count with all their bits, smaller ones
+ * with those from 2^-133 on (cut, not rounded).  Sums are fp32, their order is
+ * fixed: deterministic.  A NaN scale byte makes its row's outputs NaN.  K is
  * a multiple of the block (32 or 16) up to 2^20, M up to 2^19, N up to 2^26; c is
  * apart from the inputs.  bf16 tokens share a reading of the weight by up to 64,
  * fp32 ones by 16: for long prompts the W4A4 layers are faster.  One launch.

@@ -12,7 +12,8 @@
 // Values: E2M1 times the block's scale is exact in bf16: MXFP4's converter applies
 // its power of two, NVFP4's E4M3 scale makes products of at most six significant
 // bits.  bf16 activations multiply as they are; fp32 ones are three bf16 terms of 8
-// bits each, all 24.  Sums are fp32.
+// bits each, all 24 where the last is not below 2^-133, bf16's smallest, so from 2^-110 on.
+// Sums are fp32.
 #pragma once
 
 #include <type_traits>
