@@ -380,14 +380,15 @@ struct MoeItem {
 struct MoePlan {
     MoeItem *items;     // [pairs]
     float *share;       // [pairs]
-    uint32_t *used;     // [experts]: pairs of an expert; later where its next one goes
     uint16_t *pair;     // [pairs]
-    __host__ __device__ static size_t bytes(int pairs, int experts) {
-        return ((size_t)pairs * (sizeof(MoeItem) + 4 + 2) + (size_t)experts * 4 + 15) / 16 * 16;
+    uint32_t *used;     // [experts]: pairs of an expert; later where its next one goes
+    __host__ __device__ static size_t bytes(int pairs) {
+        return ((size_t)pairs * (sizeof(MoeItem) + 4 + 2) + 15) / 16 * 16;
     }
-    __device__ MoePlan(void *p, int pairs, int experts)
-        : items((MoeItem *)p), share((float *)(items + pairs)), used((uint32_t *)(share + pairs)),
-          pair((uint16_t *)(used + experts)) {}
+    // scratch: 4 bytes an expert, until the plan is made
+    __device__ MoePlan(void *p, int pairs, void *scratch)
+        : items((MoeItem *)p), share((float *)(items + pairs)), pair((uint16_t *)(share + pairs)),
+          used((uint32_t *)scratch) {}
 };
 
 // Tokens of an item, a pass over an expert's weights: 4, or 8 where a block's tokens go to
@@ -532,9 +533,11 @@ __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeA
     const int pairs = block * A.top_k;
     const int K = (int)A.W.inner, hidden = (int)A.W.hidden, row0 = blockIdx.x * 16;
     f32x4_t *sums = (f32x4_t *)lds;  // [waves][tokens][4]: 16 rows
-    u32x4_t *mine = lds + DOWN_WAVES<TOKENS> * block_tokens * 4 + wave * (X::PIECES + W::LDS);
-    const MoePlan plan(lds + DOWN_WAVES<TOKENS> * (block_tokens * 4 + X::PIECES + W::LDS),
-                       block_tokens * A.top_k, A.W.experts);
+    u32x4_t *pieces = lds + DOWN_WAVES<TOKENS> * block_tokens * 4;  // the waves' own
+    u32x4_t *mine = pieces + wave * (X::PIECES + W::LDS);
+    static_assert(DOWN_WAVES<TOKENS> * X::PIECES * 16 >= MOE_EXPERTS * 4);
+    const MoePlan plan(pieces + DOWN_WAVES<TOKENS> * (X::PIECES + W::LDS), block_tokens * A.top_k,
+                       pieces);
 
     for (int i = threadIdx.x; i < DOWN_WAVES<TOKENS> * block_tokens * 4; i += DOWN_WAVES<TOKENS> * WAVE)
         sums[i] = {0, 0, 0, 0};
@@ -676,7 +679,7 @@ hipError_t launch_tile(MoeArgs A, int32_t *status, hipStream_t s) {
     const auto down_lds = [&](int tokens) {
         return (size_t)DOWN_WAVES<TOKENS> *
                    (tokens * 4 + Gated<X_F32, TOKENS>::X::PIECES + RowsAt<FMT, 1>::LDS) * 16 +
-               MoePlan::bytes(tokens * A.top_k, A.W.experts);
+               MoePlan::bytes(tokens * A.top_k);
     };
     int down_block = block;  // fewer tokens where a plan of many pairs leaves no room for them
     while (down_block > 16 && down_lds(down_block) > LDS_BYTES) down_block = (down_block + 1) / 2;
