@@ -35,7 +35,7 @@ constexpr int tile_waves() {
 // rows 8192 of them fill the CUs.  The weight's bytes bound it: captured, with inputs from
 // memory, 1 x 8192 x 8192 packed takes 9.8 us (3.6 TB/s; 2 us are a node's start), 1 x 8192
 // x 28672 23.8 (5.3 TB/s), 16 x 8192 x 28672 in NVFP4 38.5 (3.4 TB/s, vector instructions
-// 44 % of the cycles), and 1 x 512 x 2048 3.9, a chain of load, decode and join.
+// 35 % of the cycles), and 1 x 512 x 2048 3.9, a chain of load, decode and join.
 template <int FMT, bool X_F32, bool PACKED, int TOKENS, int WAVES>
 __global__ __launch_bounds__(WAVES *WAVE) void linear_w4_kernel(LinearArgs A) {
     using XT = std::conditional_t<X_F32, float, uint16_t>;
@@ -135,8 +135,9 @@ hipError_t launch_tile(const LinearArgs &A, hipStream_t s) {
 // has 64 rows (what it reads of the activations then serves as many products as the matrix
 // units do while LDS gives them); ROW_WAVES waves side by side take a group of K, the
 // others of the eight the next ones.  A slab, a stretch of each of these groups, of the
-// activations is in LDS for all; the next one is on its way in registers.  Matrix, vector
-// and LDS instructions bound it, with tiles of 4 some 2000 of a stretch's 5900 cycles each:
+// activations is in LDS for all; the next one is on its way in registers.  With tiles of 4
+// the matrix, vector and LDS instructions of a stretch take some 2000 cycles each, one
+// after the other, 5900 in all: barriers keep the waves in step, so that little overlaps.
 // 64 x 28672 x 8192 packed 47 us, of which the weight's bytes are 26.
 constexpr int WIDE_WAVES = 8;
 constexpr int WIDE_THREADS = WIDE_WAVES * WAVE;

@@ -240,7 +240,7 @@ constexpr int UP_WAVES = 4;
 // Gate and up: a workgroup has 16 rows of each of one expert and the tokens of a
 // block that go there, up to TOKENS of them at a time; its waves share K = hidden (four:
 // each has several groups, whose loads overlap; with more, 16 tokens of 128 experts, 4096 x
-// 1536, took 30 us more).  The weights' bytes bound it: there 102 us, 5.3 TB/s.
+// 1536, took 30 us more).  The weights' bytes bound it: there 107 us, 5.1 TB/s.
 template <int FMT, bool X_F32, int TOKENS>
 __global__ __launch_bounds__(UP_WAVES *WAVE, TOKENS <= 4 ? 4 : 2) void moe_up_kernel(MoeArgs A,
                                                                                     int32_t *status) {
@@ -515,8 +515,9 @@ __device__ int make_plan(const MoePlan &plan, const int32_t *ids, const float *w
 // those of gridDim.z workgroups, go through the items' groups of K = inner in turn.  A
 // wave adds each group's sums, weighted, to its own of the tokens, in LDS: a token that an
 // expert does not have takes nothing of it, not a zero times its values, and no order of
-// arrival changes a sum.  16 tokens of 128 experts, 4096 x 1536: 62 us, 4.5 TB/s, LDS busy
-// for 42 % of the cycles; one token of 64, 2048 x 768: 6 us of latency.
+// arrival changes a sum.  16 tokens of 128 experts, 4096 x 1536: 74 us, 3.7 TB/s, vector
+// instructions 52 % of the cycles (half of them split the gated values), LDS busy for 46 %;
+// one token of 64, 2048 x 768: 6.4 us of latency.
 template <int FMT, bool X_F32, int TOKENS>
 __global__ __launch_bounds__(DOWN_WAVES<TOKENS> *WAVE) void moe_down_kernel(MoeArgs A, int block_tokens) {
     using G = Gated<X_F32, TOKENS>;
