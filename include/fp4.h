@@ -732,8 +732,9 @@ typedef struct {
  */
 typedef struct {
     const void *x;      /* element (t, h, d) at t * x_token_stride + h * x_head_stride + d */
-    void *y;            /* likewise; y == x with equal strides works in place, any other
-                           overlap does not.  Pointers and strides multiples of 16 bytes */
+    void *y;            /* likewise, rows apart; y == x with equal strides works in place,
+                           any other overlap does not.  Pointers and strides multiples of
+                           16 bytes */
     int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
     const void *weight; /* [head_dim], 16-byte aligned, or NULL */
     int32_t heads;      /* 1 .. 65535 */

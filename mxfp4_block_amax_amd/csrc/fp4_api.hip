@@ -731,13 +731,14 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache *cache, const fp4_kv_batch *batc
 }
 
 // One side of fp4_norm_rotate, checked.
-static fp4_status head_rows(const fp4_head_rows *r, fp4_dtype xt, int64_t dim,
+static fp4_status head_rows(const fp4_head_rows *r, fp4_dtype xt, int64_t dim, int64_t tokens,
                             fp4dev::HeadRows *R) {
     if (r->heads < 1 || r->heads > 65535) return FP4_E_SHAPE;
     if (!r->x || !r->y) return FP4_E_ARG;
     fp4_status st = kv_rows(r->x, r->x_token_stride, r->x_head_stride, xt, dim);
     if (st == FP4_OK) st = kv_rows(r->y, r->y_token_stride, r->y_head_stride, xt, dim);
     if (st != FP4_OK) return st;
+    if (tokens > 1 && r->y_token_stride < dim) return FP4_E_SHAPE;  // tokens over each other
     if (!aligned(r->weight, 16)) return FP4_E_ALIGN;
     *R = {r->x, r->y, r->x_token_stride, r->x_head_stride, r->y_token_stride, r->y_head_stride,
           r->weight, r->heads};
@@ -761,8 +762,8 @@ fp4_status fp4_norm_rotate(const fp4_head_rows *q, const fp4_head_rows *k, fp4_d
         return FP4_E_ALIGN;
     if (tokens == 0) return FP4_OK;
     fp4dev::RotateArgs A;
-    fp4_status st = head_rows(q, xt, head_dim, &A.q);
-    if (st == FP4_OK) st = head_rows(k, xt, head_dim, &A.k);
+    fp4_status st = head_rows(q, xt, head_dim, tokens, &A.q);
+    if (st == FP4_OK) st = head_rows(k, xt, head_dim, tokens, &A.k);
     if (st != FP4_OK) return st;
     A.frequencies = frequencies;
     A.eps = eps;
